@@ -243,11 +243,14 @@ def _run_own(st, c):
         return st["out"]
     plan = (st["srt"], st["eids"], st["ntp"], c["top_k"], c["block_m"])
     if c["op"] == "gmm":
-        moe.moe_group_mm(st["x"], st["w"], *plan, st["out"], st["workspace"])
+        moe.moe_group_mm(st["x"], st["w"], *plan, st["out"], st["workspace"],
+                         x_per_route=c["per_route"])
     elif c["op"] == "gmm_dx":
-        moe.moe_group_mm_dx(st["dy"], st["w"], *plan, st["out"], st["workspace"])
+        moe.moe_group_mm_dx(st["dy"], st["w"], *plan, st["out"], st["workspace"],
+                            x_per_route=c["per_route"])
     else:
-        moe.moe_group_mm_dw(st["dy"], st["x"], *plan, st["out"], st["workspace"])
+        moe.moe_group_mm_dw(st["dy"], st["x"], *plan, st["out"], st["workspace"],
+                            x_per_route=c["per_route"])
     return st["out"]
 
 
