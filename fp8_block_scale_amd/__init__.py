@@ -32,6 +32,9 @@ MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_PERSISTENT, MOE_PATH_COLUMNS = 0, 1, 2,
 MOE_F_FUSE_SHIFT = 20
 MOE_F_W13_PACKED = 0x400000
 MOE_FUSE_AUTO, MOE_FUSE_OFF, MOE_FUSE_ON = 0, 1, 2
+MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32 = 0, 1, 2
+MOE_GMM_FWD, MOE_GMM_DX, MOE_GMM_DW = 0, 1, 2
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_SWIGLU = 0, 1, 2, 3
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_ALIGN",
                 4: "MOE_ERR_CAPACITY", 5: "MOE_ERR_UNSUPPORTED", 6: "MOE_ERR_HIP"}
@@ -44,7 +47,9 @@ EXPORTED = ("moe_plan_capacity", "moe_plan_workspace_size", "moe_plan", "moe_qua
             "moe_last_hip_error", "moe_last_error", "moe_debug_e4m3_encode",
             "moe_debug_count_non_pow2", "moe_fp8_experts_noalloc", "moe_route_plan",
             "moe_w4a8_experts_workspace_size", "moe_w4a8_experts", "moe_prepack_w13_size",
-            "moe_prepack_w13", "moe_fp8_layer")
+            "moe_prepack_w13", "moe_fp8_layer", "moe_group_mm_workspace_size", "moe_group_mm",
+            "moe_group_mm_dx", "moe_group_mm_dw", "moe_fp8_linear_workspace_size",
+            "moe_fp8_linear")
 
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -109,6 +114,19 @@ _c = {
                                _sz, _vp),
     "moe_prepack_w13_size": _proto("moe_prepack_w13_size", _sz, _i64, _i64, _i64),
     "moe_prepack_w13": _proto("moe_prepack_w13", _i32, _vp, _i64, _i64, _i64, _vp, _vp),
+    "moe_group_mm_workspace_size": _proto("moe_group_mm_workspace_size", _sz, _i32, _i64, _i64, _i64,
+                                          _i32, _i32, _i32, _i64, _i32),
+    "moe_group_mm": _proto("moe_group_mm", _i32, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _i64, _i64,
+                           _i64, _i32, _i32, _i32, _i64, _vp, _i64, _vp, _sz, _vp),
+    "moe_group_mm_dx": _proto("moe_group_mm_dx", _i32, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _i64, _i64,
+                              _i64, _i32, _i32, _i32, _i64, _vp, _i64, _i32, _vp, _sz, _vp),
+    "moe_group_mm_dw": _proto("moe_group_mm_dw", _i32, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _vp,
+                              _i64, _i64, _i64, _i32, _i32, _i32, _i64, _vp, _i32, _i32, _vp, _sz,
+                              _vp),
+    "moe_fp8_linear_workspace_size": _proto("moe_fp8_linear_workspace_size", _sz, _i64, _i64, _i64,
+                                            _i32),
+    "moe_fp8_linear": _proto("moe_fp8_linear", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                             _i64, _i32, _vp, _i64, _vp, _sz, _vp),
     "moe_status_str": _proto("moe_status_str", ctypes.c_char_p, _i32),
     "moe_last_hip_error": _proto("moe_last_hip_error", ctypes.c_char_p),
     "moe_last_error": _proto("moe_last_error", ctypes.c_char_p),
@@ -408,6 +426,182 @@ def moe_fp8_down_reduce(w2, w2_s, topk_weights, sorted_token_ids, expert_ids,
                                      _ptr(out_bf16), _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), _stream(stream)),
            "moe_fp8_down_reduce")
+
+
+# ------------------------------------------------- 16-bit grouped products --
+
+_DT = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
+
+
+def _need(cond, where, what):
+    """Argument check of the entry points below: raises as the library does
+    for the sizes it sees (these are the ones it cannot see)."""
+    if not cond:
+        raise MoeError(MOE_ERR_SHAPE, where, what)
+
+
+def _on_device(where, stream, first, *rest):
+    """All tensors on one GPU, and the stream (default: that GPU's current
+    one) on it too; returns (device, stream)."""
+    dev = first.device
+    _need(dev.type == "cuda", where, "tensors must be on a GPU")
+    for t in rest:
+        _need(t is None or t.device == dev, where, "tensors are on different devices")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    _need(stream.device == dev, where, "the stream is on another device than the tensors")
+    return dev, stream
+
+
+def _rows_arg(where, name, t, dtype, cols=None):
+    """A 2-d operand with unit column stride: (pointer, leading dimension)."""
+    _need(t.dim() == 2 and t.dtype == dtype, where, f"{name} must be a 2-d {dtype} tensor")
+    _need(cols is None or t.shape[1] == cols, where, f"{name} must have {cols} columns")
+    _need(t.shape[1] == 1 or t.stride(1) == 1, where, f"{name} must have unit column stride")
+    # a single row may carry any stride; below, rows must not overlap
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    _need(ld >= t.shape[1], where, f"rows of {name} overlap")
+    return _ptr(t), ld
+
+
+def _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m):
+    for n, t in (("sorted_token_ids", sorted_token_ids), ("expert_ids", expert_ids),
+                 ("num_tokens_post_padded", num_tokens_post_padded)):
+        _need(t.dtype == torch.int32 and t.is_contiguous(), where, f"{n} must be contiguous int32")
+    _need(num_tokens_post_padded.numel() >= 1, where, "num_tokens_post_padded is empty")
+    _need(top_k >= 1 and R % top_k == 0, where, f"{R} routes are no multiple of top_k ({top_k})")
+    # blocks past the plan's length are never read: P / block_m is at most
+    # the plan's block capacity and at most sorted_cap / block_m
+    need = sorted_token_ids.numel() // block_m if block_m > 0 else 0
+    if R > 0:
+        need = min(need, moe_plan_capacity(R // top_k, top_k, E, block_m)[1])
+    _need(expert_ids.numel() >= need, where, "expert_ids shorter than the plan can need")
+    return _ptr(sorted_token_ids), _ptr(expert_ids), _ptr(num_tokens_post_padded)
+
+
+def _x_rows(where, name, t, R, top_k, per_route):
+    """Whether x / dx has one row per route (else one per token): as told, or
+    (None) as its rows say, one per token if top_k is 1."""
+    if per_route is None:
+        per_route = t.shape[0] * top_k != R
+    _need(t.shape[0] == (R if per_route else R // top_k), where,
+          f"{name} must have one row per token or per route")
+    return int(bool(per_route))
+
+
+def _ws(workspace):
+    return (_ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def moe_group_mm_workspace_size(op, M, K, N, E, top_k, block_m, sorted_cap, x_per_route=False):
+    return _c["moe_group_mm_workspace_size"](op, M, K, N, E, top_k, block_m, sorted_cap,
+                                             int(bool(x_per_route)))
+
+
+def moe_group_mm(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, out,
+                 workspace=None, stream=None, x_per_route=None):
+    """out[r] = x[t(r)] @ w[e(r)]^T for every route r of the plan.  w [E, N, K]
+    bf16 or fp16; out [M * top_k, N]; x [M, K] (t(r) = r // top_k) or
+    [M * top_k, K] (t(r) = r), all of w's type; x_per_route tells which (None:
+    by x's rows).  Rows of masked routes are left as they were."""
+    where = "moe_group_mm"
+    _need(w.dim() == 3 and w.is_contiguous() and w.dtype in (torch.bfloat16, torch.float16), where,
+          "w must be a contiguous 3-d bf16 or fp16 tensor")
+    E, N, K = w.shape
+    xp, ld_x = _rows_arg(where, "x", x, w.dtype, K)
+    yp, ld_y = _rows_arg(where, "out", out, w.dtype, N)
+    R = out.shape[0]
+    plan = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
+    per_route = _x_rows(where, "x", x, R, top_k, x_per_route)
+    dev, stream = _on_device(where, stream, x, w, out, sorted_token_ids, expert_ids,
+                             num_tokens_post_padded, workspace)
+    with torch.cuda.device(dev):
+        _check(_c[where](xp, ld_x, per_route, _ptr(w), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k,
+                         block_m, sorted_token_ids.numel(), yp, ld_y, *_ws(workspace),
+                         _stream(stream)), where)
+
+
+def moe_group_mm_dx(dy, w, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, dx,
+                    workspace=None, stream=None, x_per_route=None):
+    """The gradient of moe_group_mm by x: dx [M, K] (the gradients of a
+    token's routes added) or [M * top_k, K] (one row per route; rows of masked
+    routes left as they were) from dy [M * top_k, N] and w [E, N, K]."""
+    where = "moe_group_mm_dx"
+    _need(w.dim() == 3 and w.is_contiguous() and w.dtype in (torch.bfloat16, torch.float16), where,
+          "w must be a contiguous 3-d bf16 or fp16 tensor")
+    E, N, K = w.shape
+    yp, ld_y = _rows_arg(where, "dy", dy, w.dtype, N)
+    xp, ld_x = _rows_arg(where, "dx", dx, w.dtype, K)
+    R = dy.shape[0]
+    plan = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
+    per_route = _x_rows(where, "dx", dx, R, top_k, x_per_route)
+    dev, stream = _on_device(where, stream, dy, w, dx, sorted_token_ids, expert_ids,
+                             num_tokens_post_padded, workspace)
+    with torch.cuda.device(dev):
+        _check(_c[where](yp, ld_y, _ptr(w), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
+                         sorted_token_ids.numel(), xp, ld_x, per_route, *_ws(workspace),
+                         _stream(stream)), where)
+
+
+def moe_group_mm_dw(dy, x, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, dw,
+                    workspace=None, accumulate=False, stream=None, x_per_route=None):
+    """The gradient of moe_group_mm by w: dw [E, N, K] (of dy's type or fp32)
+    from dy [M * top_k, N] and x [M, K] or [M * top_k, K]; accumulate adds to
+    dw instead of overwriting it."""
+    where = "moe_group_mm_dw"
+    _need(dy.dtype in (torch.bfloat16, torch.float16), where, "dy must be bf16 or fp16")
+    _need(dw.dim() == 3 and dw.is_contiguous() and dw.dtype in (dy.dtype, torch.float32), where,
+          "dw must be a contiguous 3-d tensor of dy's type or fp32")
+    E, N, K = dw.shape
+    yp, ld_y = _rows_arg(where, "dy", dy, dy.dtype, N)
+    xp, ld_x = _rows_arg(where, "x", x, dy.dtype, K)
+    R = dy.shape[0]
+    plan = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
+    per_route = _x_rows(where, "x", x, R, top_k, x_per_route)
+    dev, stream = _on_device(where, stream, dy, x, dw, sorted_token_ids, expert_ids,
+                             num_tokens_post_padded, workspace)
+    with torch.cuda.device(dev):
+        _check(_c[where](yp, ld_y, xp, ld_x, per_route, _DT[dy.dtype], *plan, R // top_k, K, N, E,
+                         top_k, block_m, sorted_token_ids.numel(), _ptr(dw), _DT[dw.dtype],
+                         int(bool(accumulate)), *_ws(workspace), _stream(stream)), where)
+
+
+# --------------------------------------------------------- dense product --
+
+def moe_fp8_linear_workspace_size(M, N, K, act=MOE_ACT_NONE):
+    return _c["moe_fp8_linear_workspace_size"](M, N, K, act)
+
+
+def moe_fp8_linear(x_q, x_s, w, w_s, out, bias=None, residual=None, act=MOE_ACT_NONE, workspace=None,
+                   stream=None):
+    """out = act(x w^T + bias) + residual from FP8 block-scaled codes: x_q
+    [M, K] uint8 with x_s [M, K/128] fp32 (moe_quant_act's), w [N, K] uint8
+    with w_s [ceil(N/128), K/128] fp32, bias [N] fp32, residual and out bf16
+    [M, N] -- [M, N/2] with MOE_ACT_SWIGLU, whose w holds the gate rows, then
+    the up rows.  residual may be out itself."""
+    where = "moe_fp8_linear"
+    for n, t, dt in (("x_q", x_q, torch.uint8), ("x_s", x_s, torch.float32), ("w", w, torch.uint8),
+                     ("w_s", w_s, torch.float32)):
+        _need(t.dim() == 2 and t.dtype == dt and t.is_contiguous(), where,
+              f"{n} must be a contiguous 2-d {dt} tensor")
+    M, K = x_q.shape
+    N = w.shape[0]
+    _need(w.shape[1] == K, where, "w and x_q disagree on K")
+    _need(K % 128 == 0 and tuple(x_s.shape) == (M, K // 128), where, "x_s must be [M, K / 128]")
+    _need(tuple(w_s.shape) == ((N + 127) // 128, K // 128), where, "w_s must be [ceil(N / 128), K / 128]")
+    _need(bias is None or (bias.dtype == torch.float32 and bias.is_contiguous()
+                           and tuple(bias.shape) == (N,)), where, "bias must be contiguous fp32 [N]")
+    n_out = N // 2 if act == MOE_ACT_SWIGLU else N
+    op, ld_out = _rows_arg(where, "out", out, torch.bfloat16, n_out)
+    _need(out.shape[0] == M, where, "out and x_q disagree on M")
+    rp, ld_res = None, 0
+    if residual is not None:
+        rp, ld_res = _rows_arg(where, "residual", residual, torch.bfloat16, n_out)
+        _need(residual.shape[0] == M, where, "residual and x_q disagree on M")
+    dev, stream = _on_device(where, stream, x_q, x_s, w, w_s, out, bias, residual, workspace)
+    with torch.cuda.device(dev):
+        _check(_c[where](_ptr(x_q), _ptr(x_s), _ptr(w), _ptr(w_s), _ptr(bias), rp, ld_res, M, N, K, act,
+                         op, ld_out, *_ws(workspace), _stream(stream)), where)
 
 
 def moe_status_str(status):

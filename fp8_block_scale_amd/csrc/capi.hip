@@ -9,8 +9,10 @@
 #include <string.h>
 
 #include "../../include/moe_fp8.h"
+#include "group_mm.h"
 #include "internal.h"
 #include "layer.h"
+#include "linear.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
 
@@ -970,6 +972,264 @@ MOE_API moe_status moe_w4a8_experts(const uint8_t *x_q, const float *x_s, const 
                                           (const float *)(ws + l.ys), topk_weights,
                                           (const int32_t *)(ws + l.rpos), M, K, top_k, s),
                      "moe_w4a8_experts: finalize launch");
+}
+
+// ------------------------------------------------- 16-bit grouped products
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 20;
+
+moe_status check_group_shape(int64_t M, int64_t K, int64_t N, int32_t E, int32_t top_k, int32_t block_m,
+                             int64_t sorted_cap) {
+    if (M < 0 || K <= 0 || N <= 0 || E < 1 || top_k < 1)
+        return fail(MOE_ERR_SHAPE, "need M >= 0, K > 0, N > 0, E >= 1, top_k >= 1");
+    if (K % 8 != 0 || N % 8 != 0)
+        return fail(MOE_ERR_SHAPE, "K (%lld) and N (%lld) must be multiples of 8", (long long)K,
+                    (long long)N);
+    if (K > kMaxDim || N > kMaxDim)
+        return fail(MOE_ERR_UNSUPPORTED, "K (%lld) or N (%lld) exceeds 2^20", (long long)K, (long long)N);
+    if (E > kMaxE) return fail(MOE_ERR_UNSUPPORTED, "E = %d exceeds %d", E, kMaxE);
+    if (!valid_block_m(block_m))
+        return fail(MOE_ERR_UNSUPPORTED, "block_m %d not in {8, 16, 32, 64, 128}", block_m);
+    if (sorted_cap < 0 || sorted_cap % block_m != 0)
+        return fail(MOE_ERR_SHAPE, "sorted_cap must be a non-negative multiple of block_m");
+    if (M >= ((int64_t)1 << 31) / top_k || sorted_cap >= (int64_t)1 << 31)
+        return fail(MOE_ERR_SHAPE, "M * top_k and sorted_cap must fit in int32");
+    return MOE_OK;
+}
+
+moe::GroupMmArgs group_args(int op, int32_t dtype, const int32_t *sorted, const int32_t *eids,
+                            const int32_t *ntp, int64_t M, int64_t K, int64_t N, int32_t E, int32_t top_k,
+                            int32_t block_m, int64_t sorted_cap, int32_t per_route) {
+    moe::GroupMmArgs g = {};
+    g.op = op;
+    g.f16 = dtype == MOE_DT_F16;
+    g.per_route = per_route != 0;
+    g.sorted = sorted;
+    g.eids = eids;
+    g.ntp = ntp;
+    g.M = M;
+    g.R = M * top_k;
+    g.sorted_cap = sorted_cap;
+    g.K = (int)K;
+    g.N = (int)N;
+    g.E = E;
+    g.top_k = top_k;
+    g.block_m = block_m;
+    return g;
+}
+
+// A row-major operand [rows, ld] of 16-bit values with `cols` columns.
+moe_status check_rows(const char *name, const void *p, int64_t ld, int64_t cols) {
+    if (ld < cols)
+        return fail(MOE_ERR_SHAPE, "leading dimension of %s (%lld) < %lld", name, (long long)ld,
+                    (long long)cols);
+    if (!p) return fail(MOE_ERR_NULL, "%s is NULL", name);
+    if (!aligned16(p) || ld % 8 != 0)
+        return fail(MOE_ERR_ALIGN, "%s must be 16-byte aligned, its leading dimension a multiple of 8", name);
+    return MOE_OK;
+}
+
+// The checks that the three operators share, then their launches.
+moe_status run_group(moe::GroupMmArgs &g, int32_t dtype, void *workspace, size_t workspace_bytes,
+                     void *stream, const char *what) {
+    if (!g.sorted || !g.eids || !g.ntp)
+        return fail(MOE_ERR_NULL, "sorted_token_ids, expert_ids and num_tokens_post_padded are required");
+    if (((uintptr_t)g.sorted & 3u) || ((uintptr_t)g.eids & 3u) || ((uintptr_t)g.ntp & 3u))
+        return fail(MOE_ERR_ALIGN, "the plan must be 4-byte aligned");
+    const size_t need = moe::group_mm_workspace(g, nullptr);
+    if (need > 0) {
+        if (!workspace) return fail(MOE_ERR_NULL, "workspace is required");
+        if (((uintptr_t)workspace & 255u) != 0)
+            return fail(MOE_ERR_ALIGN, "workspace must be 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(MOE_ERR_CAPACITY, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    }
+    moe::group_mm_workspace(g, workspace);
+    return hip_check(moe::launch_group_mm(g, (hipStream_t)stream), what);
+}
+
+moe_status check_dtype(int32_t dtype) {
+    if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16)
+        return fail(MOE_ERR_SHAPE, "dtype %d is neither MOE_DT_BF16 nor MOE_DT_F16", dtype);
+    return MOE_OK;
+}
+
+}  // namespace
+
+MOE_API size_t moe_group_mm_workspace_size(int32_t op, int64_t M, int64_t K, int64_t N, int32_t E,
+                                           int32_t top_k, int32_t block_m, int64_t sorted_cap,
+                                           int32_t x_per_route) {
+    if (op < MOE_GMM_FWD || op > MOE_GMM_DW) {
+        fail(MOE_ERR_SHAPE, "unknown op %d", op);
+        return 0;
+    }
+    if (check_group_shape(M, K, N, E, top_k, block_m, sorted_cap) != MOE_OK || M == 0) return 0;
+    moe::GroupMmArgs g = group_args(op, MOE_DT_BF16, nullptr, nullptr, nullptr, M, K, N, E, top_k, block_m,
+                                    sorted_cap, x_per_route);
+    return moe::group_mm_workspace(g, nullptr);
+}
+
+MOE_API moe_status moe_group_mm(const void *x, int64_t ld_x, int32_t x_per_route, const void *w,
+                                int32_t dtype, const int32_t *sorted_token_ids,
+                                const int32_t *expert_ids, const int32_t *num_tokens_post_padded,
+                                int64_t M, int64_t K, int64_t N, int32_t E, int32_t top_k,
+                                int32_t block_m, int64_t sorted_cap, void *y, int64_t ld_y,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+    moe_status st = check_group_shape(M, K, N, E, top_k, block_m, sorted_cap);
+    if (st == MOE_OK) st = check_dtype(dtype);
+    if (st != MOE_OK) return st;
+    if (M == 0 || sorted_cap == 0) return MOE_OK;
+    if ((st = check_rows("x", x, ld_x, K)) != MOE_OK) return st;
+    if ((st = check_rows("w", w, K, K)) != MOE_OK) return st;
+    if ((st = check_rows("y", y, ld_y, N)) != MOE_OK) return st;
+    moe::GroupMmArgs g = group_args(moe::kGmmFwd, dtype, sorted_token_ids, expert_ids,
+                                    num_tokens_post_padded, M, K, N, E, top_k, block_m, sorted_cap,
+                                    x_per_route);
+    g.x = (const uint16_t *)x;
+    g.w = (const uint16_t *)w;
+    g.out = y;
+    g.ld_x = ld_x;
+    g.ld_out = ld_y;
+    return run_group(g, dtype, workspace, workspace_bytes, stream, "moe_group_mm: launch");
+}
+
+MOE_API moe_status moe_group_mm_dx(const void *dy, int64_t ld_dy, const void *w, int32_t dtype,
+                                   const int32_t *sorted_token_ids, const int32_t *expert_ids,
+                                   const int32_t *num_tokens_post_padded, int64_t M, int64_t K,
+                                   int64_t N, int32_t E, int32_t top_k, int32_t block_m,
+                                   int64_t sorted_cap, void *dx, int64_t ld_dx, int32_t x_per_route,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+    moe_status st = check_group_shape(M, K, N, E, top_k, block_m, sorted_cap);
+    if (st == MOE_OK) st = check_dtype(dtype);
+    if (st != MOE_OK) return st;
+    if (M == 0 || (sorted_cap == 0 && x_per_route)) return MOE_OK;
+    if ((st = check_rows("dy", dy, ld_dy, N)) != MOE_OK) return st;
+    if ((st = check_rows("w", w, K, K)) != MOE_OK) return st;
+    if ((st = check_rows("dx", dx, ld_dx, K)) != MOE_OK) return st;
+    moe::GroupMmArgs g = group_args(moe::kGmmDx, dtype, sorted_token_ids, expert_ids,
+                                    num_tokens_post_padded, M, K, N, E, top_k, block_m, sorted_cap,
+                                    x_per_route);
+    g.dy = (const uint16_t *)dy;
+    g.w = (const uint16_t *)w;
+    g.out = dx;
+    g.ld_dy = ld_dy;
+    g.ld_out = ld_dx;
+    return run_group(g, dtype, workspace, workspace_bytes, stream, "moe_group_mm_dx: launch");
+}
+
+MOE_API moe_status moe_group_mm_dw(const void *dy, int64_t ld_dy, const void *x, int64_t ld_x,
+                                   int32_t x_per_route, int32_t dtype,
+                                   const int32_t *sorted_token_ids, const int32_t *expert_ids,
+                                   const int32_t *num_tokens_post_padded, int64_t M, int64_t K,
+                                   int64_t N, int32_t E, int32_t top_k, int32_t block_m,
+                                   int64_t sorted_cap, void *dw, int32_t dw_dtype,
+                                   int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                   void *stream) {
+    moe_status st = check_group_shape(M, K, N, E, top_k, block_m, sorted_cap);
+    if (st == MOE_OK) st = check_dtype(dtype);
+    if (st != MOE_OK) return st;
+    if (dw_dtype != dtype && dw_dtype != MOE_DT_F32)
+        return fail(MOE_ERR_SHAPE, "dw_dtype %d is neither dtype (%d) nor MOE_DT_F32", dw_dtype, dtype);
+    if (M == 0 || sorted_cap == 0) {                 // no routes: dw = 0
+        if (accumulate) return MOE_OK;
+        if ((st = check_rows("dw", dw, K, K)) != MOE_OK) return st;
+        const size_t words = (size_t)E * N * K / (dw_dtype == MOE_DT_F32 ? 1 : 2);
+        return hip_check(moe::launch_fill_zero((uint32_t *)dw, words, (hipStream_t)stream),
+                         "moe_group_mm_dw: clear dw");
+    }
+    if ((st = check_rows("dy", dy, ld_dy, N)) != MOE_OK) return st;
+    if ((st = check_rows("x", x, ld_x, K)) != MOE_OK) return st;
+    if ((st = check_rows("dw", dw, K, K)) != MOE_OK) return st;
+    moe::GroupMmArgs g = group_args(moe::kGmmDw, dtype, sorted_token_ids, expert_ids,
+                                    num_tokens_post_padded, M, K, N, E, top_k, block_m, sorted_cap,
+                                    x_per_route);
+    g.dy = (const uint16_t *)dy;
+    g.x = (const uint16_t *)x;
+    g.out = dw;
+    g.ld_dy = ld_dy;
+    g.ld_x = ld_x;
+    g.out_f32 = dw_dtype == MOE_DT_F32;
+    g.accumulate = accumulate != 0;
+    return run_group(g, dtype, workspace, workspace_bytes, stream, "moe_group_mm_dw: launch");
+}
+
+// --------------------------------------------------------- dense product
+
+namespace {
+
+moe_status check_linear_shape(int64_t M, int64_t N, int64_t K, int32_t act) {
+    if (M < 0 || N <= 0 || K <= 0 || K % 128 != 0)
+        return fail(MOE_ERR_SHAPE, "need M >= 0, N > 0 and K a positive multiple of 128");
+    if (M >= (int64_t)1 << 31) return fail(MOE_ERR_SHAPE, "M must fit in int32");
+    if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return fail(MOE_ERR_SHAPE, "unknown act %d", act);
+    if (act == MOE_ACT_SWIGLU && N % 2 != 0)
+        return fail(MOE_ERR_SHAPE, "MOE_ACT_SWIGLU needs an even N (%lld)", (long long)N);
+    if (K > kMaxDim || N > kMaxDim)
+        return fail(MOE_ERR_UNSUPPORTED, "K (%lld) or N (%lld) exceeds 2^20", (long long)K, (long long)N);
+    return MOE_OK;
+}
+
+moe::LinearArgs linear_sizes(int64_t M, int64_t N, int64_t K, int32_t act) {
+    moe::LinearArgs a = {};
+    a.M = M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.act = act;
+    a.n_out = act == MOE_ACT_SWIGLU ? a.N / 2 : a.N;
+    return a;
+}
+
+}  // namespace
+
+MOE_API size_t moe_fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act) {
+    if (check_linear_shape(M, N, K, act) != MOE_OK || M == 0) return 0;
+    moe::LinearArgs a = linear_sizes(M, N, K, act);
+    return moe::linear_workspace(a, nullptr);
+}
+
+MOE_API moe_status moe_fp8_linear(const uint8_t *x_q, const float *x_s, const uint8_t *w,
+                                  const float *w_s, const float *bias, const void *residual,
+                                  int64_t ld_res, int64_t M, int64_t N, int64_t K, int32_t act,
+                                  void *out_bf16, int64_t ld_out, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    moe_status st = check_linear_shape(M, N, K, act);
+    if (st != MOE_OK) return st;
+    moe::LinearArgs a = linear_sizes(M, N, K, act);
+    if (ld_out < a.n_out || (residual && ld_res < a.n_out))
+        return fail(MOE_ERR_SHAPE, "ld_out (%lld) or ld_res (%lld) < %d columns", (long long)ld_out,
+                    (long long)ld_res, a.n_out);
+    if (residual && residual == out_bf16 && ld_res != ld_out)
+        return fail(MOE_ERR_SHAPE, "residual is out: ld_res (%lld) must equal ld_out (%lld)",
+                    (long long)ld_res, (long long)ld_out);
+    if (M == 0) return MOE_OK;
+    if (!x_q || !x_s || !w || !w_s || !out_bf16)
+        return fail(MOE_ERR_NULL, "x_q, x_s, w, w_s and out are required");
+    if (!aligned16(x_q) || !aligned16(w)) return fail(MOE_ERR_ALIGN, "x_q and w must be 16-byte aligned");
+    if (((uintptr_t)x_s & 3u) || ((uintptr_t)w_s & 3u) || ((uintptr_t)bias & 3u))
+        return fail(MOE_ERR_ALIGN, "x_s, w_s and bias must be 4-byte aligned");
+    if (((uintptr_t)residual & 1u) || ((uintptr_t)out_bf16 & 1u))
+        return fail(MOE_ERR_ALIGN, "residual and out must be 2-byte aligned");
+    const size_t need = moe::linear_workspace(a, nullptr);
+    if (need > 0) {
+        if (!workspace) return fail(MOE_ERR_NULL, "workspace is required");
+        if (((uintptr_t)workspace & 255u) != 0)
+            return fail(MOE_ERR_ALIGN, "workspace must be 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(MOE_ERR_CAPACITY, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    }
+    moe::linear_workspace(a, workspace);
+    a.xq = x_q;
+    a.xs = x_s;
+    a.w = w;
+    a.ws = w_s;
+    a.bias = bias;
+    a.res = (const uint16_t *)residual;
+    a.ld_res = ld_res;
+    a.out = (uint16_t *)out_bf16;
+    a.ld_out = ld_out;
+    return hip_check(moe::launch_linear(a, (hipStream_t)stream), "moe_fp8_linear: launch");
 }
 
 // ------------------------------------------------- no-allocation variant

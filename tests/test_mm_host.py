@@ -1,0 +1,174 @@
+"""The grouped 16-bit products and the dense FP8 product: their host checks
+refuse bad arguments before anything is launched (CPU only), through the C ABI
+and through the Python binding."""
+
+import ctypes
+
+import pytest
+import torch
+
+import fp8_block_scale_amd as moe
+
+FAKE = ctypes.c_void_p(0x10000)      # never dereferenced: validation fails first
+BIG = 1 << 40
+
+
+def _err(st):
+    return moe.STATUS_NAMES[st]
+
+
+GMM = dict(M=4, K=64, N=32, E=8, k=2, bm=16, sc=128, dt=0, x=FAKE, w=FAKE, y=FAKE, ldx=64, ldy=32, pr=0,
+           s=FAKE, e=FAKE, n=FAKE, ws=FAKE, wsb=BIG, dwt=0, acc=0)
+
+
+def _fwd(**kw):
+    a = dict(GMM, **kw)
+    return _err(moe._c["moe_group_mm"](a["x"], a["ldx"], a["pr"], a["w"], a["dt"], a["s"], a["e"], a["n"],
+                                       a["M"], a["K"], a["N"], a["E"], a["k"], a["bm"], a["sc"], a["y"],
+                                       a["ldy"], a["ws"], a["wsb"], None))
+
+
+def _dx(**kw):
+    a = dict(GMM, **kw)
+    return _err(moe._c["moe_group_mm_dx"](a["y"], a["ldy"], a["w"], a["dt"], a["s"], a["e"], a["n"], a["M"],
+                                          a["K"], a["N"], a["E"], a["k"], a["bm"], a["sc"], a["x"],
+                                          a["ldx"], a["pr"], a["ws"], a["wsb"], None))
+
+
+def _dw(**kw):
+    a = dict(GMM, **kw)
+    return _err(moe._c["moe_group_mm_dw"](a["y"], a["ldy"], a["x"], a["ldx"], a["pr"], a["dt"], a["s"],
+                                          a["e"], a["n"], a["M"], a["K"], a["N"], a["E"], a["k"], a["bm"],
+                                          a["sc"], a["w"], a["dwt"], a["acc"], a["ws"], a["wsb"], None))
+
+
+@pytest.mark.parametrize("f", [_fwd, _dx, _dw])
+def test_group_refusals(f):
+    assert f(K=60) == "MOE_ERR_SHAPE"
+    assert f(N=36) == "MOE_ERR_SHAPE"
+    assert f(K=0) == "MOE_ERR_SHAPE"
+    assert f(N=-8) == "MOE_ERR_SHAPE"
+    assert f(M=-1) == "MOE_ERR_SHAPE"
+    assert f(k=0) == "MOE_ERR_SHAPE"
+    assert f(E=0) == "MOE_ERR_SHAPE"
+    assert f(E=1025) == "MOE_ERR_UNSUPPORTED"
+    assert f(K=(1 << 20) + 8) == "MOE_ERR_UNSUPPORTED"
+    assert f(bm=24) == "MOE_ERR_UNSUPPORTED"
+    assert f(bm=256) == "MOE_ERR_UNSUPPORTED"
+    assert f(sc=120) == "MOE_ERR_SHAPE"
+    assert f(M=1 << 30, k=2) == "MOE_ERR_SHAPE"
+    assert f(sc=1 << 31) == "MOE_ERR_SHAPE"
+    assert f(dt=2) == "MOE_ERR_SHAPE"
+    assert f(ldx=56) == "MOE_ERR_SHAPE"
+    assert f(ldy=24) == "MOE_ERR_SHAPE"
+    assert f(ldx=68) == "MOE_ERR_ALIGN"
+    assert f(ldy=36) == "MOE_ERR_ALIGN"
+    for n in ("x", "w", "y"):
+        assert f(**{n: None}) == "MOE_ERR_NULL"
+        assert f(**{n: ctypes.c_void_p(0x10008)}) == "MOE_ERR_ALIGN"
+    for n in ("s", "e", "n"):
+        assert f(**{n: None}) == "MOE_ERR_NULL"
+        assert f(**{n: ctypes.c_void_p(0x10002)}) == "MOE_ERR_ALIGN"
+
+
+def test_group_types_and_workspace():
+    assert _dw(dwt=1) == "MOE_ERR_SHAPE"                # FP16 dw of BF16 operands
+    assert _dw(dt=1, dwt=0) == "MOE_ERR_SHAPE"
+    need = moe.moe_group_mm_workspace_size(moe.MOE_GMM_DX, 4, 64, 32, 8, 2, 16, 128)
+    assert need > 0
+    assert _dx(wsb=need - 1) == "MOE_ERR_CAPACITY"
+    assert _dx(ws=None) == "MOE_ERR_NULL"
+    assert _dx(ws=ctypes.c_void_p(0x10010)) == "MOE_ERR_ALIGN"
+    # the size query rejects what the calls reject
+    for bad in (dict(op=3), dict(K=60), dict(E=1025), dict(bm=24), dict(sc=120), dict(M=1 << 30)):
+        a = dict(op=1, M=4, K=64, N=32, E=8, k=2, bm=16, sc=128)
+        a.update(bad)
+        assert moe.moe_group_mm_workspace_size(a["op"], a["M"], a["K"], a["N"], a["E"], a["k"], a["bm"],
+                                               a["sc"]) == 0
+    # nothing to do: no pointer is needed (dx of tokens without a plan is written, so it is)
+    assert _fwd(M=0, x=None, w=None, y=None) == "MOE_OK"
+    assert _dx(M=0, x=None, w=None, y=None) == "MOE_OK"
+    assert _dw(M=0, acc=1, x=None, w=None, y=None) == "MOE_OK"
+    assert _dw(M=0, w=None) == "MOE_ERR_NULL"
+    assert _dx(sc=0, x=None) == "MOE_ERR_NULL"
+
+
+LIN = dict(M=4, N=96, K=256, act=0, xq=FAKE, xs=FAKE, w=FAKE, ws=FAKE, b=FAKE, r=None, ldr=0, out=FAKE,
+           ldo=96, wk=FAKE, wkb=BIG)
+
+
+def _lin(**kw):
+    a = dict(LIN, **kw)
+    return _err(moe._c["moe_fp8_linear"](a["xq"], a["xs"], a["w"], a["ws"], a["b"], a["r"], a["ldr"], a["M"],
+                                         a["N"], a["K"], a["act"], a["out"], a["ldo"], a["wk"], a["wkb"],
+                                         None))
+
+
+def test_linear_refusals():
+    assert _lin(K=200) == "MOE_ERR_SHAPE"
+    assert _lin(K=0) == "MOE_ERR_SHAPE"
+    assert _lin(N=0) == "MOE_ERR_SHAPE"
+    assert _lin(M=-1) == "MOE_ERR_SHAPE"
+    assert _lin(M=1 << 31) == "MOE_ERR_SHAPE"
+    assert _lin(act=4) == "MOE_ERR_SHAPE"
+    assert _lin(act=-1) == "MOE_ERR_SHAPE"
+    assert _lin(act=3, N=95) == "MOE_ERR_SHAPE"         # SwiGLU of an odd number of rows
+    assert _lin(N=(1 << 20) + 1) == "MOE_ERR_UNSUPPORTED"
+    assert _lin(ldo=95) == "MOE_ERR_SHAPE"
+    assert _lin(r=ctypes.c_void_p(0x20000), ldr=95) == "MOE_ERR_SHAPE"
+    assert _lin(r=FAKE, ldr=104) == "MOE_ERR_SHAPE"     # residual is out, other leading dimension
+    for n in ("xq", "xs", "w", "ws", "out"):
+        assert _lin(**{n: None}) == "MOE_ERR_NULL"
+    for n, p in (("xq", 0x10008), ("w", 0x10008), ("xs", 0x10002), ("ws", 0x10002), ("b", 0x10002),
+                 ("out", 0x10001)):
+        assert _lin(**{n: ctypes.c_void_p(p)}) == "MOE_ERR_ALIGN"
+    assert _lin(M=0, xq=None, w=None, out=None) == "MOE_OK"
+    assert moe.moe_fp8_linear_workspace_size(4, 96, 200) == 0
+    assert moe.moe_fp8_linear_workspace_size(4, 95, 256, moe.MOE_ACT_SWIGLU) == 0
+
+
+def _plan(n=128, blocks=8):
+    return (torch.zeros(n, dtype=torch.int32), torch.zeros(blocks, dtype=torch.int32),
+            torch.zeros(1, dtype=torch.int32))
+
+
+def _refused(f, *a, **kw):
+    with pytest.raises(moe.MoeError) as ei:
+        f(*a, **kw)
+    assert ei.value.status == moe.MOE_ERR_SHAPE
+    return str(ei.value)
+
+
+def test_binding_refusals():
+    bf, hf = torch.bfloat16, torch.float16
+    x, w, y = torch.zeros(4, 64, dtype=bf), torch.zeros(8, 32, 64, dtype=bf), torch.zeros(8, 32, dtype=bf)
+    f = moe.moe_group_mm
+    assert "GPU" in _refused(f, x, w, *_plan(), 2, 16, y)               # CPU tensors
+    assert "x must be" in _refused(f, x.to(hf), w, *_plan(), 2, 16, y)
+    assert "w must be" in _refused(f, x, w.float(), *_plan(), 2, 16, y)
+    assert "w must be" in _refused(f, x, w[:, :, :32], *_plan(), 2, 16, y)
+    assert "columns" in _refused(f, x[:, :32], w, *_plan(), 2, 16, y)
+    assert "unit column stride" in _refused(f, torch.zeros(64, 4, dtype=bf).t(), w, *_plan(), 2, 16, y)
+    assert "one row per" in _refused(f, x[:3], w, *_plan(), 2, 16, y)
+    assert "no multiple" in _refused(f, x, w, *_plan(), 3, 16, y)
+    assert "int32" in _refused(f, x, w, _plan()[0].long(), *_plan()[1:], 2, 16, y)
+    assert "shorter" in _refused(f, x, w, *_plan(128, 7), 2, 16, y)
+    assert "overlap" in _refused(f, x[:1].expand(4, 64), w, *_plan(), 2, 16, y)
+    g = moe.moe_group_mm_dw
+    assert "dw must be" in _refused(g, y, x, *_plan(), 2, 16, w.to(hf))
+    assert "x must be" in _refused(g, y, x.float(), *_plan(), 2, 16, w)
+    h = moe.moe_group_mm_dx
+    assert "dx must be" in _refused(h, y, w, *_plan(), 2, 16, x.to(hf))
+    assert "one row per" in _refused(h, y, w, *_plan(), 2, 16, x[:2])
+
+    q, s = torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(4, 2)
+    lw, ls = torch.zeros(96, 256, dtype=torch.uint8), torch.zeros(1, 2)
+    out = torch.zeros(4, 96, dtype=bf)
+    lin = moe.moe_fp8_linear
+    assert "GPU" in _refused(lin, q, s, lw, ls, out)
+    assert "w_s must be" in _refused(lin, q, s, lw, torch.zeros(2, 2), out)
+    assert "x_s must be" in _refused(lin, q, torch.zeros(4, 3), lw, ls, out)
+    assert "disagree on K" in _refused(lin, q, s, lw[:, :128].contiguous(), ls, out)
+    assert "bias" in _refused(lin, q, s, lw, ls, out, bias=torch.zeros(95))
+    assert "out must" in _refused(lin, q, s, lw, ls, out, act=moe.MOE_ACT_SWIGLU)
+    assert "residual must" in _refused(lin, q, s, lw, ls, out, residual=out.float())
