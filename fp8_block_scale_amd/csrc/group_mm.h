@@ -23,9 +23,22 @@ struct GroupMmArgs {
     int64_t ld_x, ld_dy, ld_out;
     int K, N, E, top_k, block_m;
     void *out;               // y [R, ld_out], dx [M or R, ld_out] or dw [E, N, K]
-    // workspace (group_mm_workspace)
-    int32_t *rpos;           // [R] plan row of each route, -1 if masked (dx summed over routes)
-    float *part;             // [R, K] FP32 rows of the routes (dx summed over routes)
+    // the schedule and the workspace (group_mm_workspace)
+    int tile_rows;           // rows of a row tile (forward, dx)
+    int max_tiles;           // most row tiles that any routing gives
+    int dw_tile;             // output tile of dw: 128 or 256 squared
+    int nsplit;              // dw: parts that an expert's rows are cut into
+    uint32_t div_m;          // r / top_k
+    int div_s;
+    int32_t *meta;           // [1] row tiles
+    int2 *segs;              // [E] {first plan row, valid rows} of each expert
+    int4 *tiles;             // [max_tiles] {first plan row, rows, expert, 0}
+    int32_t *rpos;           // [R] -1 if the route is masked (dx summed over routes)
+    float *part;             // FP32 rows [R, K] (dx summed over routes) or [nsplit, E, N, K] (dw)
+
+    __host__ __device__ int token_of(int r) const {
+        return (int)(((uint64_t)(uint32_t)r * div_m) >> (31 + div_s));
+    }
 };
 
 // Lays the workspace out at ws (NULL: sizes only) and returns its bytes.

@@ -5,7 +5,23 @@
 // over the routes r that the plan lists for each expert e; t(r) = r / top_k
 // (token rows) or r (one row per route).
 //
-// One 64 x 64 output tile per workgroup, both operands staged through LDS.
+// One kernel form serves all three.  A work item is a TQ x TP output tile:
+// TP output columns (contiguous in memory: n, k, k) from operand P, the A
+// side of the MFMA, and TQ output rows (routes, routes, n) from operand Q,
+// the B side.  A stage holds 64 of the contraction for both operands, 128
+// bytes per row, in LDS; it is filled by 16-byte global -> LDS copies, S - 1
+// stages ahead of the MFMAs.  An operand whose memory runs along the
+// contraction (x, dy in dx, w in forward) is staged as [row][64] and read by
+// 16-byte LDS reads; one whose memory runs along the output (w in dx, x and
+// dy in dw) as [64][columns] and read by the transposing LDS read
+// (ds_read_b64_tr_b16), so no operand is ever re-laid out in memory and rows
+// are gathered by the plan on the way in.
+//
+// The kernel is persistent: a workgroup walks its items, and the copies for
+// the next item's first stages are in flight while the current item's last
+// stages are multiplied and its tile is stored (weight gradients have only a
+// few stages per tile).  The items of one row tile are adjacent and on one
+// XCD, so its gathered rows come from that XCD's L2 after the first fetch.
 #include "common.h"
 #include "group_mm.h"
 
@@ -14,6 +30,7 @@ namespace moe {
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 
 template <bool F16>
 __device__ __forceinline__ v4f mfma32(const u32x4 &a, const u32x4 &b, const v4f &c) {
@@ -26,183 +43,536 @@ __device__ __forceinline__ v4f mfma32(const u32x4 &a, const u32x4 &b, const v4f 
 }
 
 template <bool F16>
-__device__ __forceinline__ uint16_t to16(float v) {
+__device__ __forceinline__ uint32_t to16(float v) {
     if constexpr (F16) return __builtin_bit_cast(uint16_t, (_Float16)v);
-    else return (uint16_t)f32_to_bf16_bits(v);
+    else return f32_to_bf16_bits(v);
 }
 
 template <bool F16>
-__device__ __forceinline__ float from16(uint16_t v) {
-    if constexpr (F16) return (float)__builtin_bit_cast(_Float16, v);
-    else return bf16_bits_to_f32(v);
+__device__ __forceinline__ float from16(uint32_t v) {
+    if constexpr (F16) return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
+    else return bf16_bits_to_f32(v & 0xffffu);
 }
 
-// first block in [0, nb) whose expert is >= e (expert ids never decrease)
-__device__ __forceinline__ int first_block(const int32_t *eids, int nb, int e) {
-    int lo = 0, hi = nb;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (eids[mid] < e) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
+// What the copies of contraction values past the end read: zeros on both
+// operands (0 * garbage could be NaN).
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
 
-constexpr int kLd = 40;    // LDS row of 32 contraction values, padded
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <bool F16>
-__device__ __forceinline__ void tile_step(const uint16_t (*p)[kLd], const uint16_t (*q)[kLd], int wp, int wq,
-                                          v4f (&acc)[2][2]) {
-    const int l = threadIdx.x & 63;
-    u32x4 a[2], b[2];
-    for (int i = 0; i < 2; ++i) {
-        a[i] = *(const u32x4 *)&p[wp * 32 + i * 16 + (l & 15)][(l >> 4) * 8];
-        b[i] = *(const u32x4 *)&q[wq * 32 + i * 16 + (l & 15)][(l >> 4) * 8];
-    }
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32<F16>(a[i], b[j], acc[i][j]);
-}
+// ------------------------------------------------------------ set-up launch
 
-template <bool F16, int OP>
-__global__ void __launch_bounds__(256)
-group_mm_kernel(GroupMmArgs g) {
-    __shared__ uint16_t p[64][kLd], q[64][kLd];
-    __shared__ int rid[64];
-    const int tid = threadIdx.x, l = tid & 63, w = tid >> 6, wp = w & 1, wq = w >> 1;
-    const int bm = g.block_m;
-    int P = g.ntp ? *g.ntp : 0;
-    P = P < g.sorted_cap ? P : (int)g.sorted_cap;
-    const int nb = P / bm;
-    int e, row0 = 0, rows, nred;
-    const int p0 = (OP == kGmmDw ? blockIdx.x : blockIdx.y) * 64;
-    if (OP == kGmmDw) {
-        e = blockIdx.z;
-        const int b0 = first_block(g.eids, nb, e), b1 = first_block(g.eids, nb, e + 1);
-        row0 = b0 * bm;
-        nred = (b1 - b0) * bm;
-        rows = 0;
-    } else {
-        const int b = blockIdx.x;
-        if (b >= nb) return;
-        e = g.eids[b];
-        if (e < 0 || e >= g.E) return;
-        row0 = b * bm + blockIdx.z * 64;
-        rows = bm - (int)blockIdx.z * 64;
-        rows = rows < 64 ? rows : 64;
-        nred = OP == kGmmFwd ? g.K : g.N;
-        if (tid < 64) rid[tid] = tid < rows ? g.sorted[row0 + tid] : (int)g.R;
-        __syncthreads();
-    }
-    const int np = OP == kGmmFwd ? g.N : g.K;          // output columns
-    const uint16_t *we = g.w + (int64_t)e * g.N * g.K;
-    v4f acc[2][2] = {};
-    for (int k0 = 0; k0 < nred; k0 += 32) {
-        __syncthreads();
-        for (int i = tid; i < 64 * 32; i += 256) {
-            uint16_t vp = 0, vq = 0;
-            if (OP == kGmmDw) {
-                const int c = i & 63, k = k0 + (i >> 6);
-                const int r = k < nred ? g.sorted[row0 + k] : -1;
-                if (r >= 0 && r < g.R) {
-                    const int64_t xr = g.per_route ? r : r / g.top_k;
-                    if (p0 + c < g.K) vp = g.x[xr * g.ld_x + p0 + c];
-                    if ((int)blockIdx.y * 64 + c < g.N) vq = g.dy[(int64_t)r * g.ld_dy + blockIdx.y * 64 + c];
-                }
-                p[c][i >> 6] = vp;
-                q[c][i >> 6] = vq;
-            } else if (OP == kGmmFwd) {
-                const int c = i >> 5, k = k0 + (i & 31);
-                const int r = rid[c];
-                if (k < nred) {
-                    if (p0 + c < np) vp = we[(int64_t)(p0 + c) * g.K + k];
-                    if (r >= 0 && r < g.R) vq = g.x[(int64_t)(g.per_route ? r : r / g.top_k) * g.ld_x + k];
-                }
-                p[c][i & 31] = vp;
-                q[c][i & 31] = vq;
-            } else {
-                const int c = i & 63, k = k0 + (i >> 6);
-                if (k < nred && p0 + c < np) vp = we[(int64_t)k * g.K + p0 + c];
-                p[c][i >> 6] = vp;
-                const int c2 = i >> 5, k2 = k0 + (i & 31);
-                const int r = rid[c2];
-                if (k2 < nred && r >= 0 && r < g.R) vq = g.dy[(int64_t)r * g.ld_dy + k2];
-                q[c2][i & 31] = vq;
-            }
-        }
-        __syncthreads();
-        tile_step<F16>(p, q, wp, wq, acc);
-    }
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2; ++j)
-            for (int v = 0; v < 4; ++v) {
-                const int c = p0 + wp * 32 + i * 16 + 4 * (l >> 4) + v;
-                const int qr = wq * 32 + j * 16 + (l & 15);
-                if (c >= np) continue;
-                if (OP == kGmmDw) {
-                    const int n = blockIdx.y * 64 + qr;
-                    if (n >= g.N) continue;
-                    const int64_t o = ((int64_t)e * g.N + n) * g.K + c;
-                    float s = acc[i][j][v];
-                    if (g.out_f32) {
-                        float *d = (float *)g.out + o;
-                        *d = g.accumulate ? *d + s : s;
-                    } else {
-                        uint16_t *d = (uint16_t *)g.out + o;
-                        *d = to16<F16>(g.accumulate ? from16<F16>(*d) + s : s);
-                    }
-                } else {
-                    const int r = rid[qr];
-                    if (r < 0 || r >= g.R) continue;
-                    if (OP == kGmmDx && !g.per_route) g.part[(int64_t)r * g.K + c] = acc[i][j][v];
-                    else ((uint16_t *)g.out)[(int64_t)r * g.ld_out + c] = to16<F16>(acc[i][j][v]);
-                }
-            }
-}
+// Workgroup 0 finds every expert's rows in the plan, segs[e] = {first plan
+// row, valid rows} (its sentinels, all at the end, cut off by a binary search
+// of its last block), and cuts them into row tiles of tile_rows, listed as
+// {first row, rows, expert, 0} with their count in meta[0].  The other
+// workgroups set rpos[0, R) = -1 for the sum over a token's routes.
+constexpr int kPrepThreads = 1024;
 
-__global__ void __launch_bounds__(256)
-group_mark_kernel(GroupMmArgs g) {
+__global__ void __launch_bounds__(kPrepThreads)
+group_prep_kernel(GroupMmArgs g, int tile_rows) {
+    const int tid = threadIdx.x;
+    if (blockIdx.x > 0) {
+        const int64_t stride = (int64_t)(gridDim.x - 1) * kPrepThreads;
+        for (int64_t i = (int64_t)(blockIdx.x - 1) * kPrepThreads + tid; i < g.R; i += stride) g.rpos[i] = -1;
+        return;
+    }
+    __shared__ int first[1024], last[1024], pre[1025], wsum[16];
     int P = *g.ntp;
     P = P < g.sorted_cap ? P : (int)g.sorted_cap;
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < P; i += gridDim.x * 256) {
-        const int r = g.sorted[i];
-        if (r >= 0 && r < g.R) g.rpos[r] = i;
+    const int bm = g.block_m, nb = P > 0 ? P / bm : 0;
+    first[tid] = last[tid] = 0;
+    __syncthreads();
+    for (int b = tid; b < nb; b += kPrepThreads) {
+        const int e = g.eids[b];
+        if (e < 0 || e >= g.E) continue;
+        if (b == 0 || g.eids[b - 1] != e) first[e] = b;
+        if (b == nb - 1 || g.eids[b + 1] != e) last[e] = b + 1;
+    }
+    __syncthreads();
+    int rows = 0;
+    if (last[tid] > first[tid]) {
+        int lo = (last[tid] - 1) * bm, hi = last[tid] * bm;
+        while (lo < hi) {                       // first sentinel of the last block
+            const int mid = (lo + hi) >> 1;
+            const int r = g.sorted[mid];
+            if (r >= 0 && r < g.R) lo = mid + 1;
+            else hi = mid;
+        }
+        rows = lo - first[tid] * bm;
+    }
+    if (tid < g.E) g.segs[tid] = make_int2(first[tid] * bm, rows);
+    const int cnt = (rows + tile_rows - 1) / tile_rows;
+    int incl = cnt;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(incl, d, 64);
+        if ((tid & 63) >= d) incl += v;
+    }
+    if ((tid & 63) == 63) wsum[tid >> 6] = incl;
+    __syncthreads();
+    for (int q = 0; q < (tid >> 6); ++q) incl += wsum[q];
+    pre[tid + 1] = incl;
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+    const int n = pre[1024];
+    if (tid == 0) g.meta[0] = n;
+    last[tid] = rows;
+    __syncthreads();
+    for (int i = tid; i < n && i < g.max_tiles; i += kPrepThreads) {
+        int lo = 0, hi = 1023;                  // the expert e with pre[e] <= i < pre[e + 1]
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid + 1] <= i) lo = mid + 1;
+            else hi = mid;
+        }
+        const int off = (i - pre[lo]) * tile_rows;
+        const int rem = last[lo] - off;
+        g.tiles[i] = make_int4(first[lo] * bm + off, rem < tile_rows ? rem : tile_rows, lo, 0);
     }
 }
 
+// ------------------------------------------------------------- tile kernel
+
+// Columns of MFMA tile pair t: row i of tile 2 t + h is column
+// 32 t + 8 (i / 4) + 4 h + i % 4, so that a lane's results of the pair
+// (rows 4 (l / 16) + v of either) are 8 consecutive columns.
+template <bool F16, int OP, int TP, int TQ, int WP, int WQ, int S>
+struct Tile {
+    static constexpr int NW = WP * WQ;
+    static constexpr bool PKS = OP != kGmmFwd;      // operand memory runs along the output
+    static constexpr bool QKS = OP == kGmmDw;
+    static constexpr int PB = TP * 128, QB = TQ * 128, Stage = PB + QB;
+    static constexpr int JP = PB / 1024 / NW;       // 1-KB copies per wave and stage
+    static constexpr int JQ = (QB / 1024 + NW - 1) / NW;
+    static constexpr int Ahead = (S - 2) * (JP + QB / 1024 / NW);   // copies that may be in flight
+    static constexpr int NP = TP / WP / 16, NQ = TQ / WQ / 16;
+    static constexpr size_t Smem = (size_t)S * Stage + (QKS ? 0 : S * TQ * 4);
+    static_assert(NP % 2 == 0 && JP >= 1 && Smem <= 160 * 1024, "tile");
+    static_assert(!QKS || (TP == TQ && NQ % 2 == 0), "dw tile");
+};
+
+__device__ __forceinline__ u32x4 lds_read_tr(const uint8_t *p, int second) {
+    typedef __attribute__((address_space(3))) v4s *lp;
+    const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)p);
+    const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p + second));
+    const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
+    return u32x4{x.x, x.y, y.x, y.y};
+}
+
+template <bool F16, int OP, int TP, int TQ, int WP, int WQ, int S>
+__global__ void __launch_bounds__(64 * WP * WQ)
+group_tile_kernel(GroupMmArgs g) {
+    using T = Tile<F16, OP, TP, TQ, WP, WQ, S>;
+    constexpr int NW = T::NW, JP = T::JP, JQ = T::JQ, NP = T::NP, NQ = T::NQ;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    int *rids = reinterpret_cast<int *>(smem + (size_t)S * T::Stage);   // [S][TQ] routes of an item's rows
+
+    const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6);
+    const int wp = w % WP, wq = w / WP;
+    const int np = OP == kGmmFwd ? g.N : g.K;                 // output columns
+    const int nct = (np + TP - 1) / TP;
+
+    // ---- the items of this workgroup: a contiguous range per XCD
+    int n_items, qtiles = 1;
+    if (OP == kGmmDw) {
+        qtiles = (g.N + TQ - 1) / TQ;
+        n_items = g.E * qtiles * nct * g.nsplit;
+    } else {
+        int nt = uni(g.meta[0]);
+        nt = nt < g.max_tiles ? nt : g.max_tiles;
+        n_items = nt * nct;
+    }
+    const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+    const int end = (int)((int64_t)(xcd + 1) * n_items / 8);
+    int lit = (int)((int64_t)xcd * n_items / 8) + (blockIdx.x >> 3);     // load cursor
+    int cit = lit;                                                        // compute cursor
+    if (cit >= end) return;
+
+    // ---- load side: state of the item being loaded
+    const uint8_t *pbase = nullptr;          // uniform; advances along the contraction
+    uint32_t poff[JP];
+    const uint8_t *qptr[JQ];
+    const uint8_t *xcol = nullptr, *dycol = nullptr;      // dw: this lane's columns
+    int lkt = 0, lnk = 0, lord = 0;          // stage in the item, its stages, its ordinal
+    int lrow = 0, lrows = 0;                 // dw: first plan row, rows
+    int nid[JQ];                             // dw: routes of the next stage's rows
+    const int nred = OP == kGmmFwd ? g.K : g.N;
+
+    auto kr_of = [&](int j) { return (j * NW + w) * (1024 / (TP * 2)) + l / (TP / 8); };   // KS row in stage
+    // copies of the KC layout: lane l copies row 8 (j NW + w) + l / 8, chunk position l % 8
+    const int kc_p = ((l & 7) ^ (((l >> 3) & 3) | ((w & 1) << 2)));     // global chunk (P swizzle)
+    const int kc_q = ((l & 7) ^ (l >> 3));                              // global chunk (Q swizzle)
+    static_assert(NW % 2 == 0, "the swizzles assume an even wave count");
+
+    auto ids_ahead = [&](int kt) {
+        for (int j = 0; j < JQ; ++j) {
+            const int p = kt * 64 + kr_of(j);
+            nid[j] = p < lrows ? g.sorted[lrow + p] : -1;
+        }
+    };
+
+    auto load_setup = [&]() {
+        if (OP == kGmmDw) {
+            int i = lit;
+            const int sp = i % g.nsplit;
+            i /= g.nsplit;
+            const int ct = i % nct;
+            i /= nct;
+            const int qt = i % qtiles, e = i / qtiles;
+            const int2 sg = g.segs[e];
+            const int per = ((sg.y + 64 * g.nsplit - 1) / (64 * g.nsplit)) * 64;   // rows per split
+            const int r0 = sp * per;
+            int rows = sg.y - r0;
+            rows = rows < 0 ? 0 : (rows < per ? rows : per);
+            lrow = uni(sg.x) + uni(r0);
+            lrows = uni(rows);
+            lnk = lrows > 0 ? (lrows + 63) / 64 : 1;
+            const int ch = (l % (TP / 8)) ^ ((kr_of(0) & 3) << 2);
+            const int pc = ct * TP + ch * 8, qc = qt * TQ + ch * 8;
+            xcol = reinterpret_cast<const uint8_t *>(g.x + (pc < g.K ? pc : 0));
+            dycol = reinterpret_cast<const uint8_t *>(g.dy + (qc < g.N ? qc : 0));
+            ids_ahead(0);
+        } else {
+            const int4 t = g.tiles[lit / nct];
+            const int ct = lit % nct, p0 = ct * TP;
+            const int e = uni(t.z), row0 = uni(t.x), rows = uni(t.y);
+            lnk = (nred + 63) / 64;
+            const uint8_t *we = reinterpret_cast<const uint8_t *>(g.w + (int64_t)e * g.N * g.K);
+            if (T::PKS) {
+                pbase = we + (int64_t)p0 * 2;
+                for (int j = 0; j < JP; ++j) {
+                    const int kr = kr_of(j);
+                    int c = ((l % (TP / 8)) ^ ((kr & 3) << 2)) * 8;
+                    c = p0 + c < g.K ? c : 0;
+                    poff[j] = (uint32_t)kr * (uint32_t)g.K * 2u + (uint32_t)c * 2u;
+                }
+            } else {
+                pbase = we + (int64_t)p0 * g.K * 2;
+                for (int j = 0; j < JP; ++j) {
+                    int row = 8 * (j * NW + w) + (l >> 3);
+                    row = p0 + row < g.N ? row : g.N - 1 - p0;
+                    poff[j] = (uint32_t)row * (uint32_t)g.K * 2u + (uint32_t)kc_p * 16u;
+                }
+            }
+            const uint16_t *src = OP == kGmmFwd ? g.x : g.dy;
+            const int64_t ld = OP == kGmmFwd ? g.ld_x : g.ld_dy;
+            for (int j = 0; j < JQ; ++j) {
+                const int row = 8 * (j * NW + w) + (l >> 3);
+                int r = row < rows ? g.sorted[row0 + row] : -1;
+                if (r >= g.R) r = -1;
+                if (row < TQ && (l & 7) == 0) rids[(lord % S) * TQ + row] = r;
+                int64_t xr = r < 0 ? 0 : (OP == kGmmFwd && !g.per_route ? g.token_of(r) : r);
+                qptr[j] = reinterpret_cast<const uint8_t *>(src + xr * ld) + kc_q * 16;
+            }
+        }
+        lkt = 0;
+    };
+
+    // one stage of copies into slot
+    auto issue = [&](int slot) {
+        uint8_t *sp = smem + slot * T::Stage;
+        uint8_t *sq = sp + T::PB;
+        if (OP == kGmmDw) {
+            int id[JQ];
+            for (int j = 0; j < JQ; ++j) id[j] = nid[j];
+            if (lkt + 1 < lnk) ids_ahead(lkt + 1);
+            for (int j = 0; j < JQ; ++j) {
+                const int r = id[j];
+                const bool ok = r >= 0 && r < g.R;
+                const int64_t xr = g.per_route ? r : g.token_of(r);
+                const void *zp = kZeros;
+                lds_dma16(ok ? (const void *)(xcol + xr * g.ld_x * 2) : zp, sp + (j * NW + w) * 1024);
+                lds_dma16(ok ? (const void *)(dycol + (int64_t)r * g.ld_dy * 2) : zp, sq + (j * NW + w) * 1024);
+            }
+        } else {
+            const int k0 = lkt * 64;
+            const bool tail = k0 + 64 > nred;
+            const uint8_t *pb = pbase + (T::PKS ? (int64_t)k0 * g.K * 2 : (int64_t)k0 * 2);
+            for (int j = 0; j < JP; ++j) {
+                const void *p = pb + poff[j];
+                if (tail && k0 + (T::PKS ? kr_of(j) : kc_p * 8) >= nred) p = kZeros;
+                lds_dma16(p, sp + (j * NW + w) * 1024);
+            }
+            for (int j = 0; j < JQ; ++j) {
+                if ((j + 1) * NW > T::QB / 1024 && j * NW + w >= T::QB / 1024) continue;
+                const void *p = qptr[j] + (int64_t)k0 * 2;
+                if (tail && k0 + kc_q * 8 >= nred) p = kZeros;
+                lds_dma16(p, sq + (j * NW + w) * 1024);
+            }
+        }
+        if (++lkt == lnk) {
+            lit += step;
+            ++lord;
+            if (lit < end) load_setup();
+        }
+    };
+
+    // ---- compute side
+    const int i16 = l & 15, grp = l >> 4;
+    v4f acc[NP][NQ];
+    auto clear = [&]() {
+        for (int a = 0; a < NP; ++a)
+            for (int b = 0; b < NQ; ++b) acc[a][b] = v4f{0.f, 0.f, 0.f, 0.f};
+    };
+    // LDS offsets of this lane's operand reads
+    const int pf = (i16 & 3) | (((i16 >> 2) & 1) << 2);
+    const int p_kc = (wp * (TP / WP) + 8 * (i16 >> 2) + (i16 & 3)) * 128 + ((grp ^ pf) << 4);
+    const int q_kc = (wq * (TQ / WQ) + i16) * 128 + ((grp ^ (i16 & 7)) << 4);
+    const int ks_row = 8 * grp + (i16 >> 2);
+    const int ks_x = (i16 >> 2) & 3;
+
+    auto compute = [&](int slot) {
+        const uint8_t *sp = smem + slot * T::Stage;
+        const uint8_t *sq = sp + T::PB;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            u32x4 a[NP], b[NQ];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                if constexpr (T::PKS) {
+                    const int ch = (wp * (TP / WP) / 8 + 4 * (n >> 1) + (i16 & 3)) ^ (ks_x << 2);
+                    a[n] = lds_read_tr(sp + (kk * 32 + ks_row) * (TP * 2) + ch * 16 + (n & 1) * 8, 4 * TP * 2);
+                } else {
+                    a[n] = lds_read16(sp + (p_kc ^ (kk << 6)) + (n >> 1) * 32 * 128 + (n & 1) * 4 * 128);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                if constexpr (T::QKS) {
+                    const int ch = (wq * (TQ / WQ) / 8 + 4 * (n >> 1) + (i16 & 3)) ^ (ks_x << 2);
+                    b[n] = lds_read_tr(sq + (kk * 32 + ks_row) * (TQ * 2) + ch * 16 + (n & 1) * 8, 4 * TQ * 2);
+                } else {
+                    b[n] = lds_read16(sq + (q_kc ^ (kk << 6)) + n * 16 * 128);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) acc[m][n] = mfma32<F16>(a[m], b[n], acc[m][n]);
+        }
+    };
+
+    auto store8 = [&](uint16_t *d, const v4f &x, const v4f &y) {
+        u32x4 o;
+        o.x = to16<F16>(x[0]) | (to16<F16>(x[1]) << 16);
+        o.y = to16<F16>(x[2]) | (to16<F16>(x[3]) << 16);
+        o.z = to16<F16>(y[0]) | (to16<F16>(y[1]) << 16);
+        o.w = to16<F16>(y[2]) | (to16<F16>(y[3]) << 16);
+        *reinterpret_cast<u32x4 *>(d) = o;
+    };
+
+    auto epilogue = [&](int ord) {
+        int i = cit;
+        int sp = 0, qt = 0, e = 0, ct;
+        if (OP == kGmmDw) {
+            sp = i % g.nsplit;
+            i /= g.nsplit;
+            ct = i % nct;
+            i /= nct;
+            qt = i % qtiles;
+            e = i / qtiles;
+        } else {
+            ct = i % nct;
+        }
+        const int c0 = ct * TP + wp * (TP / WP) + 8 * grp;
+        for (int n = 0; n < NQ; ++n) {
+            const int q = wq * (TQ / WQ) + (T::QKS ? 32 * (n >> 1) + 8 * (i16 >> 2) + 4 * (n & 1) + (i16 & 3)
+                                                   : 16 * n + i16);
+            if (OP == kGmmDw) {
+                const int row = qt * TQ + q;
+                if (row >= g.N) continue;
+                const int64_t o = ((int64_t)e * g.N + row) * g.K;
+                for (int m = 0; m < NP / 2; ++m) {
+                    const int c = c0 + 32 * m;
+                    if (c >= g.K) continue;
+                    v4f x = acc[2 * m][n], y = acc[2 * m + 1][n];
+                    if (g.nsplit > 1) {
+                        float *d = g.part + (int64_t)sp * g.E * g.N * g.K + o + c;
+                        *reinterpret_cast<v4f *>(d) = x;
+                        *reinterpret_cast<v4f *>(d + 4) = y;
+                    } else if (g.out_f32) {
+                        float *d = (float *)g.out + o + c;
+                        if (g.accumulate) {
+                            x += *reinterpret_cast<v4f *>(d);
+                            y += *reinterpret_cast<v4f *>(d + 4);
+                        }
+                        *reinterpret_cast<v4f *>(d) = x;
+                        *reinterpret_cast<v4f *>(d + 4) = y;
+                    } else {
+                        uint16_t *d = (uint16_t *)g.out + o + c;
+                        if (g.accumulate) {
+                            const u32x4 old = *reinterpret_cast<const u32x4 *>(d);
+                            for (int v = 0; v < 2; ++v) {
+                                x[2 * v] += from16<F16>(old[v]);
+                                x[2 * v + 1] += from16<F16>(old[v] >> 16);
+                                y[2 * v] += from16<F16>(old[2 + v]);
+                                y[2 * v + 1] += from16<F16>(old[2 + v] >> 16);
+                            }
+                        }
+                        store8(d, x, y);
+                    }
+                }
+            } else {
+                const int r = rids[(ord % S) * TQ + q];
+                if (r < 0) continue;
+                if (OP == kGmmDx && !g.per_route) {
+                    if (ct == 0 && wp == 0 && grp == 0) g.rpos[r] = 0;
+                    float *d = g.part + (int64_t)r * g.K + c0;
+                    for (int m = 0; m < NP / 2; ++m) {
+                        if (c0 + 32 * m >= np) continue;
+                        *reinterpret_cast<v4f *>(d + 32 * m) = acc[2 * m][n];
+                        *reinterpret_cast<v4f *>(d + 32 * m + 4) = acc[2 * m + 1][n];
+                    }
+                } else {
+                    uint16_t *d = (uint16_t *)g.out + (int64_t)r * g.ld_out + c0;
+                    for (int m = 0; m < NP / 2; ++m)
+                        if (c0 + 32 * m < np) store8(d + 32 * m, acc[2 * m][n], acc[2 * m + 1][n]);
+                }
+            }
+        }
+    };
+
+    // ---- the pipeline
+    load_setup();
+    int issued = 0, done = 0;                // stages issued and multiplied so far
+    int cnk = lnk, ckt = 0, cord = 0;
+    int nks[S];                              // stages of the items between the two cursors
+    for (int s = 0; s < S; ++s) nks[s] = 0;
+    nks[0] = lnk;
+    auto issue_next = [&]() {
+        if (lit >= end) return;
+        const int o = lord;
+        issue(issued % S);
+        ++issued;
+        if (lord != o && lit < end)
+            for (int s = 0; s < S; ++s)
+                if (s == lord % S) nks[s] = lnk;
+    };
+    for (int s = 0; s < S - 1; ++s) issue_next();
+    clear();
+    while (true) {
+        // this wave's copies of the stage have landed, then everyone's; all
+        // reads of the slot that the next copies overwrite are complete
+        if (S > 2 && issued - done == S - 1) wait_vmcnt<(T::Ahead < 63 ? T::Ahead : 63)>();
+        else wait_vmcnt<0>();
+        __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0)
+        stage_barrier();
+        issue_next();
+        compute(done % S);
+        ++done;
+        if (++ckt == cnk) {
+            epilogue(cord);
+            cit += step;
+            if (cit >= end) break;
+            clear();
+            ++cord;
+            ckt = 0;
+            for (int s = 0; s < S; ++s)
+                if (s == cord % S) cnk = nks[s];
+        }
+    }
+}
+
+// ------------------------------------------------------------ joining sums
+
+// dx[t] = the sum of the token's routes' FP32 rows, in route order.
 template <bool F16>
 __global__ void __launch_bounds__(256)
 group_sum_kernel(GroupMmArgs g) {
-    const int64_t t = blockIdx.x;
-    for (int c = threadIdx.x; c < g.K; c += 256) {
-        float s = 0.f;
-        for (int j = 0; j < g.top_k; ++j) {
-            const int64_t r = t * g.top_k + j;
-            if (g.rpos[r] >= 0) s += g.part[r * g.K + c];
+    const int per = (g.K / 8 + 255) / 256;
+    const int64_t t = blockIdx.x / per;
+    const int c = ((int)(blockIdx.x % per) * 256 + threadIdx.x) * 8;
+    if (c >= g.K) return;
+    v4f x = {0.f, 0.f, 0.f, 0.f}, y = x;
+    for (int j = 0; j < g.top_k; ++j) {
+        const int64_t r = t * g.top_k + j;
+        if (g.rpos[r] < 0) continue;
+        x += *reinterpret_cast<const v4f *>(g.part + r * g.K + c);
+        y += *reinterpret_cast<const v4f *>(g.part + r * g.K + c + 4);
+    }
+    u32x4 o;
+    o.x = to16<F16>(x[0]) | (to16<F16>(x[1]) << 16);
+    o.y = to16<F16>(x[2]) | (to16<F16>(x[3]) << 16);
+    o.z = to16<F16>(y[0]) | (to16<F16>(y[1]) << 16);
+    o.w = to16<F16>(y[2]) | (to16<F16>(y[3]) << 16);
+    *reinterpret_cast<u32x4 *>((uint16_t *)g.out + t * g.ld_out + c) = o;
+}
+
+// dw = the sum of the splits' FP32 tiles, in split order.
+template <bool F16>
+__global__ void __launch_bounds__(256)
+group_join_kernel(GroupMmArgs g) {
+    const int64_t n = (int64_t)g.E * g.N * g.K;
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    v4f s = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < g.nsplit; ++k) s += *reinterpret_cast<const v4f *>(g.part + k * n + i);
+    if (g.out_f32) {
+        v4f *d = reinterpret_cast<v4f *>((float *)g.out + i);
+        *d = g.accumulate ? *d + s : s;
+    } else {
+        uint2 *d = reinterpret_cast<uint2 *>((uint16_t *)g.out + i);
+        if (g.accumulate) {
+            const uint2 o = *d;
+            s[0] += from16<F16>(o.x);
+            s[1] += from16<F16>(o.x >> 16);
+            s[2] += from16<F16>(o.y);
+            s[3] += from16<F16>(o.y >> 16);
         }
-        ((uint16_t *)g.out)[t * g.ld_out + c] = to16<F16>(s);
+        *d = uint2{to16<F16>(s[0]) | (to16<F16>(s[1]) << 16), to16<F16>(s[2]) | (to16<F16>(s[3]) << 16)};
+    }
+}
+
+// ----------------------------------------------------------------- launch
+
+template <bool F16, int OP, int TP, int TQ, int WP, int WQ, int S>
+hipError_t launch_tile(const GroupMmArgs &g, int64_t max_items, hipStream_t st) {
+    using T = Tile<F16, OP, TP, TQ, WP, WQ, S>;
+    static std::atomic<uint64_t> done{0};
+    auto fn = group_tile_kernel<F16, OP, TP, TQ, WP, WQ, S>;
+    hipError_t e = raise_lds_limit(done, (const void *)fn, (int)T::Smem);
+    if (e != hipSuccess) return e;
+    const int64_t per_cu = (160 * 1024) / (int64_t)T::Smem;
+    int64_t grid = (int64_t)device_cu_count() * (per_cu < 2 ? 1 : 2);
+    if (grid > max_items) grid = max_items;
+    grid = (grid + 7) / 8 * 8;
+    fn<<<(unsigned)grid, 64 * WP * WQ, T::Smem, st>>>(g);
+    return hipGetLastError();
+}
+
+template <bool F16, int OP>
+hipError_t launch_rows(const GroupMmArgs &g, hipStream_t st) {
+    const int np = OP == kGmmFwd ? g.N : g.K;
+    const int64_t items = (int64_t)g.max_tiles * ((np + 255) / 256);
+    switch (g.tile_rows) {
+        case 256: return launch_tile<F16, OP, 256, 256, 4, 2, 2>(g, items, st);
+        case 128: return launch_tile<F16, OP, 256, 128, 4, 2, 3>(g, items, st);
+        case 64: return launch_tile<F16, OP, 256, 64, 4, 2, 3>(g, items, st);
+        default: return launch_tile<F16, OP, 256, 32, 8, 1, 4>(g, items, st);
     }
 }
 
 template <bool F16>
 hipError_t launch(const GroupMmArgs &g, hipStream_t st) {
-    const unsigned blocks = (unsigned)(g.sorted_cap / g.block_m);
+    const bool summed = g.op == kGmmDx && !g.per_route;
+    const int64_t fill = summed ? (g.R + 8 * kPrepThreads - 1) / (8 * kPrepThreads) : 0;
+    group_prep_kernel<<<(unsigned)(1 + (fill < 255 ? fill : 255)), kPrepThreads, 0, st>>>(g, g.tile_rows);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     if (g.op == kGmmDw) {
-        dim3 grid((g.K + 63) / 64, (g.N + 63) / 64, g.E);
-        group_mm_kernel<F16, kGmmDw><<<grid, 256, 0, st>>>(g);
+        const int64_t t = g.dw_tile;
+        const int64_t items = (int64_t)g.E * ((g.N + t - 1) / t) * ((g.K + t - 1) / t) * g.nsplit;
+        e = t == 256 ? launch_tile<F16, kGmmDw, 256, 256, 4, 2, 2>(g, items, st)
+                     : launch_tile<F16, kGmmDw, 128, 128, 2, 2, 2>(g, items, st);
+        if (e != hipSuccess || g.nsplit == 1) return e;
+        const int64_t n = (int64_t)g.E * g.N * g.K / 4;
+        group_join_kernel<F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
         return hipGetLastError();
     }
-    const int sub = (g.block_m + 63) / 64;
-    if (g.op == kGmmFwd) {
-        group_mm_kernel<F16, kGmmFwd><<<dim3(blocks, (g.N + 63) / 64, sub), 256, 0, st>>>(g);
-        return hipGetLastError();
-    }
-    if (!g.per_route) {
-        hipError_t e = launch_fill((uint32_t *)g.rpos, (size_t)g.R, 0xffffffffu, st);
-        if (e != hipSuccess) return e;
-        group_mark_kernel<<<256, 256, 0, st>>>(g);
-    }
-    group_mm_kernel<F16, kGmmDx><<<dim3(blocks, (g.K + 63) / 64, sub), 256, 0, st>>>(g);
-    if (!g.per_route) group_sum_kernel<F16><<<(unsigned)g.M, 256, 0, st>>>(g);
+    e = g.op == kGmmFwd ? launch_rows<F16, kGmmFwd>(g, st) : launch_rows<F16, kGmmDx>(g, st);
+    if (e != hipSuccess || !summed) return e;
+    const int64_t per = (g.K / 8 + 255) / 256;
+    group_sum_kernel<F16><<<(unsigned)(g.M * per), 256, 0, st>>>(g);
     return hipGetLastError();
 }
 
@@ -213,14 +583,46 @@ hipError_t launch_group_mm(const GroupMmArgs &g, hipStream_t st) {
 }
 
 size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
+    // r / top_k for 0 <= r < 2^31 by one high product: with s the least
+    // number with 2^s >= top_k and m = floor(2^(31 + s) / top_k) + 1 (below
+    // 2^32), m top_k exceeds 2^(31 + s) by at most top_k <= 2^s, so
+    // floor(r m / 2^(31 + s)) is the quotient.
+    int s = 0;
+    while (((int64_t)1 << s) < g.top_k) ++s;
+    g.div_m = (uint32_t)((((uint64_t)1 << (31 + s)) / (uint64_t)g.top_k) + 1);
+    g.div_s = s;
+
+    const int64_t rpe = g.R / g.E;
+    g.tile_rows = rpe > 128 ? 256 : rpe > 48 ? 128 : rpe > 24 ? 64 : 32;
+    g.max_tiles = (int)(g.R / g.tile_rows + (g.E < g.R ? g.E : g.R));
+    g.nsplit = 1;
+    g.dw_tile = 256;
+    if (g.op == kGmmDw) {
+        int64_t tiles = (int64_t)g.E * ((g.N + 255) / 256) * ((g.K + 255) / 256);
+        if (tiles < 256) {
+            g.dw_tile = 128;
+            tiles = (int64_t)g.E * ((g.N + 127) / 128) * ((g.K + 127) / 128);
+        }
+        int64_t sp = 256 / tiles;                      // tiles < 256: cut the rows
+        if (sp > rpe / 128) sp = rpe / 128;
+        if (sp > 64) sp = 64;
+        if (sp > 1) g.nsplit = (int)sp;
+    }
     uint8_t *base = (uint8_t *)ws;
     size_t off = 0;
+    auto take = [&](size_t n) {
+        uint8_t *p = base + off;
+        off += (n + 255) & ~size_t(255);
+        return p;
+    };
+    g.meta = (int32_t *)take(4);
+    g.segs = (int2 *)take((size_t)g.E * 8);
+    g.tiles = (int4 *)take((size_t)g.max_tiles * 16);
     if (g.op == kGmmDx && !g.per_route) {
-        g.rpos = (int32_t *)(base + off);
-        off += ((size_t)g.R * 4 + 255) & ~size_t(255);
-        g.part = (float *)(base + off);
-        off += ((size_t)g.R * g.K * 4 + 255) & ~size_t(255);
+        g.rpos = (int32_t *)take((size_t)g.R * 4);
+        g.part = (float *)take((size_t)g.R * g.K * 4);
     }
+    if (g.nsplit > 1) g.part = (float *)take((size_t)g.nsplit * g.E * g.N * g.K * 4);
     return off;
 }
 
