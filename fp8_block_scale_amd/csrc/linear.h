@@ -7,6 +7,8 @@ namespace moe {
 
 enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActSwiglu = 3 };
 
+enum { kLinStream1 = 0, kLinStream2, kLinStream4, kLinTile64, kLinTile128, kLinTile256 };
+
 struct LinearArgs {
     const uint8_t *xq;       // [M, K] E4M3
     const float *xs;         // [M, K / 128]
@@ -18,9 +20,15 @@ struct LinearArgs {
     int64_t M, ld_res, ld_out;
     int K, N, n_out;         // n_out = N, or N / 2 with SwiGLU
     int act;
-    float *part;             // workspace
+    // the schedule and the workspace (linear_workspace)
+    int form;                // kernel form
+    int nsplit;              // parts that K is cut into (tile forms)
+    int ld_part;             // row of the partial sums
+    float *part;             // [nsplit, M, ld_part] FP32
 };
 
+// Chooses the schedule, lays the workspace out at ws (NULL: sizes only) and
+// returns its bytes.
 size_t linear_workspace(LinearArgs &a, void *ws);
 hipError_t launch_linear(const LinearArgs &a, hipStream_t st);
 
