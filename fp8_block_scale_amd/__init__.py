@@ -440,43 +440,52 @@ def _need(cond, where, what):
         raise MoeError(MOE_ERR_SHAPE, where, what)
 
 
-def _on_device(where, stream, first, *rest):
-    """All tensors on one GPU, and the stream (default: that GPU's current
-    one) on it too; returns (device, stream)."""
-    dev = first.device
-    _need(dev.type == "cuda", where, "tensors must be on a GPU")
-    for t in rest:
-        _need(t is None or t.device == dev, where, "tensors are on different devices")
+def _launch(where, stream, tensors, *args):
+    """Calls the entry point on the stream given (default: the current one of
+    the tensors' device) after a check that all tensors (None: absent) and the
+    stream are on one GPU; that GPU is the current device during the call."""
+    dev = tensors[0].get_device()
+    _need(dev >= 0, where, "tensors must be on a GPU")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise MoeError(MOE_ERR_SHAPE, where, "tensors are on different devices")
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-    _need(stream.device == dev, where, "the stream is on another device than the tensors")
-    return dev, stream
+    _need(stream.device_index == dev, where, "the stream is on another device than the tensors")
+    if torch.cuda.current_device() == dev:
+        _check(_c[where](*args, stream.cuda_stream), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(_c[where](*args, stream.cuda_stream), where)
 
 
-def _rows_arg(where, name, t, dtype, cols=None):
+def _rows_arg(where, name, t, dtype, cols):
     """A 2-d operand with unit column stride: (pointer, leading dimension)."""
-    _need(t.dim() == 2 and t.dtype == dtype, where, f"{name} must be a 2-d {dtype} tensor")
-    _need(cols is None or t.shape[1] == cols, where, f"{name} must have {cols} columns")
-    _need(t.shape[1] == 1 or t.stride(1) == 1, where, f"{name} must have unit column stride")
-    # a single row may carry any stride; below, rows must not overlap
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    _need(ld >= t.shape[1], where, f"rows of {name} overlap")
-    return _ptr(t), ld
+    if t.dim() != 2 or t.dtype != dtype:
+        raise MoeError(MOE_ERR_SHAPE, where, f"{name} must be a 2-d {dtype} tensor")
+    rows, n = t.shape
+    if n != cols:
+        raise MoeError(MOE_ERR_SHAPE, where, f"{name} must have {cols} columns")
+    ld, unit = t.stride()
+    _need(n == 1 or unit == 1, where, f"{name} must have unit column stride")
+    if rows <= 1:                       # a single row may carry any stride
+        return t.data_ptr(), n
+    _need(ld >= n, where, f"rows of {name} overlap")
+    return t.data_ptr(), ld
 
 
 def _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m):
-    for n, t in (("sorted_token_ids", sorted_token_ids), ("expert_ids", expert_ids),
-                 ("num_tokens_post_padded", num_tokens_post_padded)):
-        _need(t.dtype == torch.int32 and t.is_contiguous(), where, f"{n} must be contiguous int32")
+    for t in (sorted_token_ids, expert_ids, num_tokens_post_padded):
+        _need(t.dtype == torch.int32 and t.is_contiguous(), where, "the plan must be contiguous int32")
     _need(num_tokens_post_padded.numel() >= 1, where, "num_tokens_post_padded is empty")
-    _need(top_k >= 1 and R % top_k == 0, where, f"{R} routes are no multiple of top_k ({top_k})")
+    _need(top_k >= 1 and R % top_k == 0, where, "the routes are no multiple of top_k")
     # blocks past the plan's length are never read: P / block_m is at most
-    # the plan's block capacity and at most sorted_cap / block_m
-    need = sorted_token_ids.numel() // block_m if block_m > 0 else 0
-    if R > 0:
-        need = min(need, moe_plan_capacity(R // top_k, top_k, E, block_m)[1])
-    _need(expert_ids.numel() >= need, where, "expert_ids shorter than the plan can need")
-    return _ptr(sorted_token_ids), _ptr(expert_ids), _ptr(num_tokens_post_padded)
+    # sorted_cap / block_m, and at most the capacity that any routing needs
+    if block_m > 0:
+        need = min(sorted_token_ids.numel() // block_m,
+                   -(-(R + min(E, R) * (block_m - 1)) // block_m))
+        _need(expert_ids.numel() >= need, where, "expert_ids shorter than the plan can need")
+    return sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr()
 
 
 def _x_rows(where, name, t, R, top_k, per_route):
@@ -485,12 +494,12 @@ def _x_rows(where, name, t, R, top_k, per_route):
     if per_route is None:
         per_route = t.shape[0] * top_k != R
     _need(t.shape[0] == (R if per_route else R // top_k), where,
-          f"{name} must have one row per token or per route")
+          name + " must have one row per token or per route")
     return int(bool(per_route))
 
 
 def _ws(workspace):
-    return (_ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
 
 
 def moe_group_mm_workspace_size(op, M, K, N, E, top_k, block_m, sorted_cap, x_per_route=False):
@@ -513,12 +522,9 @@ def moe_group_mm(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, top
     R = out.shape[0]
     plan = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
     per_route = _x_rows(where, "x", x, R, top_k, x_per_route)
-    dev, stream = _on_device(where, stream, x, w, out, sorted_token_ids, expert_ids,
-                             num_tokens_post_padded, workspace)
-    with torch.cuda.device(dev):
-        _check(_c[where](xp, ld_x, per_route, _ptr(w), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k,
-                         block_m, sorted_token_ids.numel(), yp, ld_y, *_ws(workspace),
-                         _stream(stream)), where)
+    _launch(where, stream, (x, w, out, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace),
+            xp, ld_x, per_route, w.data_ptr(), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
+            sorted_token_ids.numel(), yp, ld_y, *_ws(workspace))
 
 
 def moe_group_mm_dx(dy, w, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, dx,
@@ -535,12 +541,9 @@ def moe_group_mm_dx(dy, w, sorted_token_ids, expert_ids, num_tokens_post_padded,
     R = dy.shape[0]
     plan = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
     per_route = _x_rows(where, "dx", dx, R, top_k, x_per_route)
-    dev, stream = _on_device(where, stream, dy, w, dx, sorted_token_ids, expert_ids,
-                             num_tokens_post_padded, workspace)
-    with torch.cuda.device(dev):
-        _check(_c[where](yp, ld_y, _ptr(w), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
-                         sorted_token_ids.numel(), xp, ld_x, per_route, *_ws(workspace),
-                         _stream(stream)), where)
+    _launch(where, stream, (dy, w, dx, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace),
+            yp, ld_y, w.data_ptr(), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
+            sorted_token_ids.numel(), xp, ld_x, per_route, *_ws(workspace))
 
 
 def moe_group_mm_dw(dy, x, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, dw,
@@ -558,12 +561,10 @@ def moe_group_mm_dw(dy, x, sorted_token_ids, expert_ids, num_tokens_post_padded,
     R = dy.shape[0]
     plan = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
     per_route = _x_rows(where, "x", x, R, top_k, x_per_route)
-    dev, stream = _on_device(where, stream, dy, x, dw, sorted_token_ids, expert_ids,
-                             num_tokens_post_padded, workspace)
-    with torch.cuda.device(dev):
-        _check(_c[where](yp, ld_y, xp, ld_x, per_route, _DT[dy.dtype], *plan, R // top_k, K, N, E,
-                         top_k, block_m, sorted_token_ids.numel(), _ptr(dw), _DT[dw.dtype],
-                         int(bool(accumulate)), *_ws(workspace), _stream(stream)), where)
+    _launch(where, stream, (dy, x, dw, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace),
+            yp, ld_y, xp, ld_x, per_route, _DT[dy.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
+            sorted_token_ids.numel(), dw.data_ptr(), _DT[dw.dtype], int(bool(accumulate)),
+            *_ws(workspace))
 
 
 # --------------------------------------------------------- dense product --
@@ -582,8 +583,8 @@ def moe_fp8_linear(x_q, x_s, w, w_s, out, bias=None, residual=None, act=MOE_ACT_
     where = "moe_fp8_linear"
     for n, t, dt in (("x_q", x_q, torch.uint8), ("x_s", x_s, torch.float32), ("w", w, torch.uint8),
                      ("w_s", w_s, torch.float32)):
-        _need(t.dim() == 2 and t.dtype == dt and t.is_contiguous(), where,
-              f"{n} must be a contiguous 2-d {dt} tensor")
+        if t.dim() != 2 or t.dtype != dt or not t.is_contiguous():
+            raise MoeError(MOE_ERR_SHAPE, where, f"{n} must be a contiguous 2-d {dt} tensor")
     M, K = x_q.shape
     N = w.shape[0]
     _need(w.shape[1] == K, where, "w and x_q disagree on K")
@@ -598,10 +599,9 @@ def moe_fp8_linear(x_q, x_s, w, w_s, out, bias=None, residual=None, act=MOE_ACT_
     if residual is not None:
         rp, ld_res = _rows_arg(where, "residual", residual, torch.bfloat16, n_out)
         _need(residual.shape[0] == M, where, "residual and x_q disagree on M")
-    dev, stream = _on_device(where, stream, x_q, x_s, w, w_s, out, bias, residual, workspace)
-    with torch.cuda.device(dev):
-        _check(_c[where](_ptr(x_q), _ptr(x_s), _ptr(w), _ptr(w_s), _ptr(bias), rp, ld_res, M, N, K, act,
-                         op, ld_out, *_ws(workspace), _stream(stream)), where)
+    _launch(where, stream, (x_q, x_s, w, w_s, out, bias, residual, workspace), x_q.data_ptr(),
+            x_s.data_ptr(), w.data_ptr(), w_s.data_ptr(), None if bias is None else bias.data_ptr(), rp,
+            ld_res, M, N, K, act, op, ld_out, *_ws(workspace))
 
 
 def moe_status_str(status):

@@ -473,6 +473,93 @@ group_tile_kernel(GroupMmArgs g) {
     }
 }
 
+// --------------------------------------------------- few rows: the forward
+
+// The forward product where experts hold a few rows each (decoded tokens):
+// the time is that of reading the touched experts' weights once.  A workgroup
+// takes 16 weight rows of one plan block; its NW waves split K, load weights
+// and x rows straight into registers (no LDS ring and no set-up launch to
+// wait for) U steps of 64 at a time, and add up in LDS.  Plan blocks with more than 16 NQ
+// routes go through the weights again for each further 16 NQ.
+template <bool F16, int NQ, int NW, int U>
+__global__ void __launch_bounds__(64 * NW)
+group_stream_kernel(GroupMmArgs g) {
+    __shared__ float red[NW][NQ][16][17];
+    const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6), i16 = l & 15, grp = l >> 4;
+    int P = *g.ntp;
+    P = P < g.sorted_cap ? P : (int)g.sorted_cap;
+    const int b = blockIdx.y, bm = g.block_m;
+    if ((b + 1) * bm > P) return;
+    const int e = uni(g.eids[b]);
+    if (e < 0 || e >= g.E) return;
+    const int c0 = blockIdx.x * 16;
+    const int c = c0 + i16 < g.N ? c0 + i16 : g.N - 1;
+    const uint16_t *ap = g.w + ((int64_t)e * g.N + c) * g.K;
+    const int nk = (g.K + 63) / 64;
+
+    for (int row0 = b * bm; row0 < (b + 1) * bm; row0 += 16 * NQ) {
+        const int r0 = uni(g.sorted[row0]);
+        if (r0 < 0 || r0 >= g.R) break;                 // sentinels end the segment
+        const uint16_t *bp[NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            const int i = 16 * n + i16;
+            int r = i < bm ? g.sorted[row0 + i] : r0;
+            if (r < 0 || r >= g.R) r = r0;              // results of these lanes are not stored
+            bp[n] = g.x + (int64_t)(g.per_route ? r : g.token_of(r)) * g.ld_x;
+        }
+        v4f acc[NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) acc[n] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int k0 = w; k0 < nk; k0 += NW * U) {
+            u32x4 a[U][2], x[U][NQ][2];
+            bool ok[U][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    int k = (k0 + u * NW) * 64 + 32 * h + 8 * grp;
+                    ok[u][h] = k < g.K;
+                    k = ok[u][h] ? k : 0;
+                    a[u][h] = __builtin_nontemporal_load((const u32x4 *)(ap + k));
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) x[u][n][h] = *(const u32x4 *)(bp[n] + k);
+                }
+            __builtin_amdgcn_sched_barrier(0);          // every load above is issued first
+            const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // past the end of K: zeros on both sides
+                    const u32x4 av = ok[u][h] ? a[u][h] : zero;
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+                        acc[n] = mfma32<F16>(av, ok[u][h] ? x[u][n][h] : zero, acc[n]);
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) red[w][n][i16][4 * grp + v] = acc[n][v];
+        __syncthreads();
+        for (int i = tid; i < 16 * NQ * 8; i += 64 * NW) {
+            const int cc = (i & 7) * 2, q = i >> 3;
+            if (q >= bm || c0 + cc >= g.N) continue;
+            const int r = g.sorted[row0 + q];
+            if (r < 0 || r >= g.R) continue;
+            float z0 = 0.f, z1 = 0.f;
+            for (int k = 0; k < NW; ++k) {
+                z0 += red[k][q >> 4][q & 15][cc];
+                z1 += red[k][q >> 4][q & 15][cc + 1];
+            }
+            *reinterpret_cast<uint32_t *>((uint16_t *)g.out + (int64_t)r * g.ld_out + c0 + cc) =
+                to16<F16>(z0) | (to16<F16>(z1) << 16);
+        }
+        __syncthreads();
+    }
+}
+
 // ------------------------------------------------------------ joining sums
 
 // dx[t] = the sum of the token's routes' FP32 rows, in route order.
@@ -554,6 +641,11 @@ hipError_t launch_rows(const GroupMmArgs &g, hipStream_t st) {
 
 template <bool F16>
 hipError_t launch(const GroupMmArgs &g, hipStream_t st) {
+    if (g.stream) {
+        const dim3 grid((g.N + 15) / 16, (unsigned)(g.sorted_cap / g.block_m));
+        group_stream_kernel<F16, 1, 8, 7><<<grid, 512, 0, st>>>(g);
+        return hipGetLastError();
+    }
     const bool summed = g.op == kGmmDx && !g.per_route;
     const int64_t fill = summed ? (g.R + 8 * kPrepThreads - 1) / (8 * kPrepThreads) : 0;
     group_prep_kernel<<<(unsigned)(1 + (fill < 255 ? fill : 255)), kPrepThreads, 0, st>>>(g, g.tile_rows);
@@ -593,6 +685,8 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
     g.div_s = s;
 
     const int64_t rpe = g.R / g.E;
+    g.stream = g.op == kGmmFwd && rpe <= 2 && g.sorted_cap / g.block_m <= 65535;
+    if (g.stream) return 0;
     g.tile_rows = rpe > 128 ? 256 : rpe > 48 ? 128 : rpe > 24 ? 64 : 32;
     g.max_tiles = (int)(g.R / g.tile_rows + (g.E < g.R ? g.E : g.R));
     g.nsplit = 1;
