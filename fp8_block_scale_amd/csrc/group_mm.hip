@@ -20,8 +20,8 @@
 // The kernel is persistent: a workgroup walks its items, and the copies for
 // the next item's first stages are in flight while the current item's last
 // stages are multiplied and its tile is stored (weight gradients have only a
-// few stages per tile).  The items of one row tile are adjacent and on one
-// XCD, so its gathered rows come from that XCD's L2 after the first fetch.
+// few stages per tile).  Neighbouring items, which share rows or weights, run
+// on one XCD at the same time (panel_tile).
 #include "common.h"
 #include "group_mm.h"
 
@@ -173,14 +173,14 @@ group_tile_kernel(GroupMmArgs g) {
     const int nct = (np + TP - 1) / TP;
 
     // ---- the items of this workgroup: a contiguous range per XCD
-    int n_items, qtiles = 1;
+    int n_items, qtiles = 1, ntiles = 0;
     if (OP == kGmmDw) {
         qtiles = (g.N + TQ - 1) / TQ;
         n_items = g.E * qtiles * nct * g.nsplit;
     } else {
-        int nt = uni(g.meta[0]);
-        nt = nt < g.max_tiles ? nt : g.max_tiles;
-        n_items = nt * nct;
+        ntiles = uni(g.meta[0]);
+        ntiles = ntiles < g.max_tiles ? ntiles : g.max_tiles;
+        n_items = ntiles * nct;
     }
     const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
     const int end = (int)((int64_t)(xcd + 1) * n_items / 8);
@@ -233,8 +233,10 @@ group_tile_kernel(GroupMmArgs g) {
             dycol = reinterpret_cast<const uint8_t *>(g.dy + (qc < g.N ? qc : 0));
             ids_ahead(0);
         } else {
-            const int4 t = g.tiles[lit / nct];
-            const int ct = lit % nct, p0 = ct * TP;
+            int rt, ct;
+            panel_tile<4>(lit, ntiles, nct, rt, ct);
+            const int4 t = g.tiles[rt];
+            const int p0 = ct * TP;
             const int e = uni(t.z), row0 = uni(t.x), rows = uni(t.y);
             lnk = (nred + 63) / 64;
             const uint8_t *we = reinterpret_cast<const uint8_t *>(g.w + (int64_t)e * g.N * g.K);
@@ -372,7 +374,8 @@ group_tile_kernel(GroupMmArgs g) {
             qt = i % qtiles;
             e = i / qtiles;
         } else {
-            ct = i % nct;
+            int rt;
+            panel_tile<4>(i, ntiles, nct, rt, ct);
         }
         const int c0 = ct * TP + wp * (TP / WP) + 8 * grp;
         for (int n = 0; n < NQ; ++n) {

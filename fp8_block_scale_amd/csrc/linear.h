@@ -7,7 +7,7 @@ namespace moe {
 
 enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActSwiglu = 3 };
 
-enum { kLinStream1 = 0, kLinStream2, kLinStream4, kLinTile64, kLinTile128, kLinTile256 };
+enum { kLinStream = 0, kLinTile64, kLinTile128, kLinTile256 };
 
 struct LinearArgs {
     const uint8_t *xq;       // [M, K] E4M3
@@ -23,8 +23,7 @@ struct LinearArgs {
     // the schedule and the workspace (linear_workspace)
     int form;                // kernel form
     int nsplit;              // parts that K is cut into (tile forms)
-    int ld_part;             // row of the partial sums
-    float *part;             // [nsplit, M, ld_part] FP32
+    float *part;             // FP32 sums of every (tile, split)
 };
 
 // Chooses the schedule, lays the workspace out at ws (NULL: sizes only) and

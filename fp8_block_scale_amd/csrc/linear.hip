@@ -55,7 +55,6 @@ linear_stream_kernel(LinearArgs g) {
     const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6), i16 = l & 15, grp = l >> 4;
     const int nkb = g.K >> 7;
     const int c0 = blockIdx.x * (SW ? 8 : 16);
-    const int64_t m0 = (int64_t)blockIdx.y * (16 * NQ);
 
     auto wrow = [&](int i) {                     // weight row of MFMA row i
         const int c = c0 + (SW ? i & 7 : i);
@@ -64,9 +63,9 @@ linear_stream_kernel(LinearArgs g) {
     const uint8_t *ap = g.w + (int64_t)wrow(i16) * g.K + grp * 16;
     const uint8_t *bp[NQ];
     const float *xp[NQ];
+#pragma unroll
     for (int n = 0; n < NQ; ++n) {
-        int64_t m = m0 + 16 * n + i16;
-        m = m < g.M ? m : g.M - 1;
+        const int64_t m = 16 * n + i16 < g.M ? 16 * n + i16 : g.M - 1;
         bp[n] = g.xq + m * g.K + grp * 16;
         xp[n] = g.xs + m * nkb;
     }
@@ -76,6 +75,7 @@ linear_stream_kernel(LinearArgs g) {
     for (int v = 0; v < 4; ++v) wp[v] = g.ws + (int64_t)(wrow(4 * grp + v) >> 7) * nkb;
 
     v4f acc[NQ];
+#pragma unroll
     for (int n = 0; n < NQ; ++n) acc[n] = v4f{0.f, 0.f, 0.f, 0.f};
     for (int kb0 = w; kb0 < nkb; kb0 += NW * U) {
         u32x4 a[U][2], b[U][NQ][2];
@@ -117,7 +117,7 @@ linear_stream_kernel(LinearArgs g) {
     constexpr int COLS = SW ? 8 : 16;
     for (int i = tid; i < 16 * NQ * COLS; i += 64 * NW) {
         const int c = i % COLS, r = i / COLS;
-        const int64_t m = m0 + r;
+        const int64_t m = r;
         const int col = c0 + c;
         if (m >= g.M || col >= g.n_out) continue;
         float z = 0.f, u = 0.f;
@@ -143,56 +143,54 @@ linear_stream_kernel(LinearArgs g) {
 template <int TP, int TQ, int WP, int WQ, int S>
 struct LTile {
     static constexpr int NW = WP * WQ;
-    static constexpr int PB = TP * 128, QB = TQ * 128, XB = TQ * 4, Stage = PB + QB + XB;
+    static constexpr int PB = TP * 128, QB = TQ * 128, XB = TQ * 4, WB = 256, Stage = PB + QB + XB + WB;
     static constexpr int JP = PB / 1024 / NW, JQ = QB / 1024 / NW;
-    static constexpr int XW = TQ / 64;                    // waves that copy 64 scales each
+    static constexpr int XW = TQ / 64;                    // waves that copy 64 scales of x each; the last wave
+                                                          // copies the weights'
     static constexpr int NP = TP / WP / 16, NQ = TQ / WQ / 16;
     static constexpr size_t Smem = (size_t)S * Stage;
-    static_assert(NP % 4 == 0 && JP >= 1 && JQ >= 1 && XW <= NW && Smem <= 160 * 1024, "tile");
+    static_assert(NP % 4 == 0 && JP >= 1 && JQ >= 1 && XW < NW && Smem <= 160 * 1024, "tile");
 };
 
-// The lane's results of a column group: 8 consecutive columns of one row.
-struct Store8 {
-    const LinearArgs &g;
-    bool vec;                                    // 16-byte accesses are aligned
-    __device__ __forceinline__ void operator()(int64_t m, int col, float (&z)[8]) const {
-        const int n = g.n_out - col;             // valid columns from here
-        if (g.res) {
-            const uint16_t *r = g.res + m * g.ld_res + col;
-            if (vec && n >= 8) {
-                const u32x4 o = *reinterpret_cast<const u32x4 *>(r);
+// Stores a lane's results of a column group, 8 consecutive columns of one
+// row, by one 16-byte access (which global memory takes at any alignment:
+// rows of an odd number of columns are 2-byte aligned only).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+__device__ __forceinline__ void store8(const LinearArgs &g, int64_t m, int col, float (&z)[8]) {
+    const int n = g.n_out - col;                 // valid columns from here
+    if (g.res) {
+        const uint16_t *r = g.res + m * g.ld_res + col;
+        if (n >= 8) {
+            const u32x4 o = *reinterpret_cast<const u32x4_any *>(r);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    z[2 * v] += bf16_bits_to_f32(o[v] & 0xffffu);
-                    z[2 * v + 1] += bf16_bits_to_f32(o[v] >> 16);
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < 8; ++v)
-                    if (v < n) z[v] += bf16_bits_to_f32(r[v]);
+            for (int v = 0; v < 4; ++v) {
+                z[2 * v] += bf16_bits_to_f32(o[v] & 0xffffu);
+                z[2 * v + 1] += bf16_bits_to_f32(o[v] >> 16);
             }
-        }
-        uint16_t *d = g.out + m * g.ld_out + col;
-        if (vec && n >= 8) {
-            u32x4 o;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) o[v] = f32_to_bf16_bits(z[2 * v]) | (f32_to_bf16_bits(z[2 * v + 1]) << 16);
-            *reinterpret_cast<u32x4 *>(d) = o;
         } else {
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-                if (v < n) d[v] = (uint16_t)f32_to_bf16_bits(z[v]);
+                if (v < n) z[v] += bf16_bits_to_f32(r[v]);
         }
     }
-};
-
-__device__ __forceinline__ bool vec_ok(const LinearArgs &g) {
-    return (((uintptr_t)g.out | (uintptr_t)g.res) & 15u) == 0 && ((g.ld_out | (g.res ? g.ld_res : 0)) & 7) == 0;
+    uint16_t *d = g.out + m * g.ld_out + col;
+    if (n >= 8) {
+        u32x4 o;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] = f32_to_bf16_bits(z[2 * v]) | (f32_to_bf16_bits(z[2 * v + 1]) << 16);
+        *reinterpret_cast<u32x4_any *>(d) = o;
+    } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            if (v < n) d[v] = (uint16_t)f32_to_bf16_bits(z[v]);
+    }
 }
 
 // GLU: 0 no SwiGLU; 1 SwiGLU; 2 SwiGLU whose up rows in a wave may straddle
 // two blocks of 128 weight rows (N / 2 no multiple of 32).
-template <int TP, int TQ, int WP, int WQ, int S, int GLU>
+// SPLIT: the K-blocks of a tile may be cut over several items.
+template <int TP, int TQ, int WP, int WQ, int S, int GLU, bool SPLIT>
 __global__ void __launch_bounds__(64 * WP * WQ)
 linear_tile_kernel(LinearArgs g) {
     using T = LTile<TP, TQ, WP, WQ, S>;
@@ -204,58 +202,92 @@ linear_tile_kernel(LinearArgs g) {
     const int wp = w % WP, wq = w / WP, i16 = l & 15, grp = l >> 4;
     const int nkb = g.K >> 7;
     const int nct = (g.n_out + TC - 1) / TC;
-    const int n_items = (int)((g.M + TQ - 1) / TQ) * nct * g.nsplit;
+    const int nrt = (int)((g.M + TQ - 1) / TQ);
+    const int n_items = nrt * nct * (SPLIT ? g.nsplit : 1);
     const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
     const int end = (int)((int64_t)(xcd + 1) * n_items / 8);
     int lit = (int)((int64_t)xcd * n_items / 8) + (blockIdx.x >> 3), cit = lit;
     if (cit >= end) return;
-    const int per = (nkb + g.nsplit - 1) / g.nsplit;      // K-blocks per split (none empty)
+    const int nsp = SPLIT ? g.nsplit : 1;
+    const int per = (nkb + nsp - 1) / nsp;                // K-blocks per split (none empty)
 
-    // ---- load side
-    const uint8_t *pbase = nullptr, *qbase = nullptr;
+    // ---- load side.  A 16-byte copy instruction of a wave fills 8 rows of a
+    // tile (8 lanes a row): its first row is uniform, so an address is a
+    // scalar base, stepped from copy to copy, and one lane offset, which all
+    // copies share; only tiles that reach past the last row clamp row by row.
+    const uint8_t *pbase = nullptr, *qbase = nullptr;     // the wave's first copy, K-block lkb
     const float *xbase = nullptr;
-    uint32_t poff[JP], qoff[JQ], xoff = 0;
-    int lkb = 0, lkend = 0;
-    const int kc_p = (l & 7) ^ (((l >> 3) & 3) | ((w & 1) << 2));
-    const int kc_q = (l & 7) ^ (l >> 3);
+    uint32_t xoff = 0;                                    // of x's or the weights' scales
+    int lkb = 0, lkend = 0, pleft = 0, qleft = 0;         // pleft, qleft: the tile's rows that exist
+    const int lrow = l >> 3;
+    const uint32_t poff = (uint32_t)lrow * (uint32_t)g.K + (uint32_t)((l & 7) ^ ((lrow & 3) | ((w & 1) << 2))) * 16u;
+    const uint32_t qoff = (uint32_t)lrow * (uint32_t)g.K + (uint32_t)((l & 7) ^ lrow) * 16u;
+    // LDS row 8 (j NW + w) of the weights' tile: its column within the tile
+    // and whether it is an up row; scalar steps from copy to copy
+    auto pcol = [&](int j) {
+        const int rho = 8 * (j * NW + w);
+        return SW ? (rho >> 6) * 32 + (rho & 31) : rho;
+    };
+    const int64_t up = SW ? (int64_t)g.n_out * g.K : 0;
+    static_assert(NW == 8 || NW == 4, "the steps below");
+    const int64_t pstep0 = !SW ? (int64_t)(8 * NW) * g.K : NW == 8 ? (int64_t)32 * g.K : up;
+    const int64_t pstep1 = SW && NW == 4 ? (int64_t)32 * g.K - up : pstep0;
+    const int64_t qstep = (int64_t)(8 * NW) * g.K;
     auto load_setup = [&]() {
         int i = lit;
-        const int sp = i % g.nsplit;
-        i /= g.nsplit;
-        const int ct = i % nct;
-        const int64_t m0 = (int64_t)(i / nct) * TQ;
+        const int sp = i % nsp;
+        i /= nsp;
+        int rt, ct;
+        panel_tile<8>(i, nrt, nct, rt, ct);
+        const int64_t m0 = (int64_t)rt * TQ;
         lkb = sp * per;
         lkend = min(lkb + per, nkb);
         const int c0 = ct * TC;
-        pbase = g.w + (int64_t)c0 * g.K;
-#pragma unroll
-        for (int j = 0; j < JP; ++j) {
-            const int rho = 8 * (j * NW + w) + (l >> 3);
-            int c = SW ? (rho >> 6) * 32 + (rho & 31) : rho;
-            c = c0 + c < g.n_out ? c : g.n_out - 1 - c0;
-            // an up row lies N / 2 rows further: up to 2^39 bytes, so its
-            // offset is taken in 16-byte units
-            poff[j] = (uint32_t)(((int64_t)(c + (SW && (rho & 32) ? g.n_out : 0)) * g.K) >> 4) + (uint32_t)kc_p;
+        pbase = g.w + (int64_t)(c0 + pcol(0)) * g.K + (NW == 8 && w >= 4 ? up : 0) + (int64_t)lkb * 128;
+        pleft = min(TC, g.n_out - c0);
+        qbase = g.xq + (m0 + 8 * w) * g.K + (int64_t)lkb * 128;
+        qleft = (int)min((int64_t)TQ, g.M - m0);
+        if (w < T::XW) {
+            xbase = g.xs + m0 * nkb + lkb;
+            xoff = (uint32_t)min(w * 64 + l, qleft - 1) * (uint32_t)nkb;
+        } else {
+            // the weights' scales, from the tile's first block on; with SwiGLU
+            // lanes 32.. take the up rows' blocks
+            const int first = (SW && l >= 32 ? c0 + g.n_out : c0) >> 7;
+            const int last = ((SW ? 2 * g.n_out : g.n_out) - 1) >> 7;
+            xbase = g.ws + lkb;
+            xoff = (uint32_t)min(first + (SW ? l & 31 : l), last) * (uint32_t)nkb;
         }
-        qbase = g.xq + m0 * g.K;
-        xbase = g.xs + m0 * nkb;
-        const int rows = (int)min((int64_t)TQ, g.M - m0);
-#pragma unroll
-        for (int j = 0; j < JQ; ++j) {
-            const int row = 8 * (j * NW + w) + (l >> 3);
-            qoff[j] = (uint32_t)(row < rows ? row : rows - 1) * (uint32_t)g.K + (uint32_t)kc_q * 16u;
-        }
-        const int row = (w % T::XW) * 64 + l;
-        xoff = (uint32_t)(row < rows ? row : rows - 1) * (uint32_t)nkb;
     };
-    auto issue = [&](int slot) {
-        uint8_t *sp = smem + slot * T::Stage, *sq = sp + T::PB, *sx = sq + T::QB;
-        const int64_t k0 = (int64_t)lkb * 128;
-#pragma unroll
-        for (int j = 0; j < JP; ++j) lds_dma16(pbase + k0 + ((uint64_t)poff[j] << 4), sp + (j * NW + w) * 1024);
-#pragma unroll
-        for (int j = 0; j < JQ; ++j) lds_dma16(qbase + k0 + qoff[j], sq + (j * NW + w) * 1024);
-        if (w < T::XW) lds_dma4(xbase + lkb + xoff, sx + w * 256);
+    // Copy c of a stage (JP of the weights, JQ of x, one of scales) into slot.
+    // Rows past the last read the last one: the copy's first row r moves back
+    // to it (uniform), then each lane by what its own row exceeds it, at most
+    // lrow (24-bit products: below 2^8 times K <= 2^20), so that the lane
+    // offset never goes below zero.
+    constexpr int kCopies = JP + JQ + 1;
+    auto copy8 = [&](const uint8_t *base, int r, int last, uint32_t off, uint8_t *dst) {
+        const int back = max(r - last, 0);
+        const int over = max(r - back + lrow - last, 0);
+        lds_dma16(base - (int64_t)(back * g.K) + (off - __umul24(over, g.K)), dst);
+    };
+    auto issue_copy = [&](int c, int slot) {
+        uint8_t *sp = smem + slot * T::Stage;
+        if (c < JP) {
+            const int64_t st = (int64_t)((c + 1) / 2) * pstep0 + (int64_t)(c / 2) * pstep1;
+            copy8(pbase + st, pcol(c), pleft - 1, poff, sp + (c * NW + w) * 1024);
+        } else if (c < JP + JQ) {
+            const int j = c - JP;
+            copy8(qbase + j * qstep, 8 * (j * NW + w), qleft - 1, qoff, sp + T::PB + (j * NW + w) * 1024);
+        } else if (w < T::XW) {
+            lds_dma4(xbase + xoff, sp + T::PB + T::QB + w * 256);
+        } else if (w == NW - 1) {
+            lds_dma4(xbase + xoff, sp + T::PB + T::QB + T::XB);
+        }
+    };
+    auto stage_issued = [&]() {
+        pbase += 128;
+        qbase += 128;
+        xbase += 1;
         if (++lkb == lkend) {
             lit += step;
             if (lit < end) load_setup();
@@ -273,78 +305,94 @@ linear_tile_kernel(LinearArgs g) {
     const int pf = (i16 & 3) | (((i16 >> 2) & 1) << 2);
     const int p_off = (wp * (TP / WP) + 8 * (i16 >> 2) + (i16 & 3)) * 128 + ((grp ^ pf) << 4);
     const int q_off = (wq * (TQ / WQ) + i16) * 128 + ((grp ^ (i16 & 7)) << 4);
-    int ckb = 0, ckend = 0, cc0 = 0, csp = 0;
-    int64_t cm0 = 0;
     // weight scales: one block of 128 rows per 64-row wave slice (gate and up
-    // apart); where its up rows straddle two, rows from `cut` on take the second
-    const float *w0 = nullptr, *w1 = nullptr, *w2 = nullptr;
-    int cut = 1 << 30;
-    auto comp_setup = [&]() {
-        int i = cit;
-        csp = i % g.nsplit;
-        i /= g.nsplit;
-        cc0 = (i % nct) * TC;
-        cm0 = (int64_t)(i / nct) * TQ;
-        ckb = csp * per;
-        ckend = min(ckb + per, nkb);
+    // apart: b0, b1, counted from the tile's first); where its up rows
+    // straddle two, rows from `cut` on take the second
+    struct Item {
+        int c0, kb, kend, b0, b1, cut;
+        int64_t m0;
+    };
+    auto item_of = [&](int i) {
+        Item it;
+        const int csp = i % nsp;
+        i /= nsp;
+        int rt, ct;
+        panel_tile<8>(i, nrt, nct, rt, ct);
+        it.c0 = ct * TC;
+        it.m0 = (int64_t)rt * TQ;
+        it.kb = csp * per;
+        it.kend = min(it.kb + per, nkb);
         static_assert(TP / WP == 64, "a wave's columns lie in one block of 128");
-        const int c = cc0 + wp * (SW ? 32 : 64);
-        const int last = ((SW ? 2 * g.n_out : g.n_out) - 1) >> 7;
-        w0 = g.ws + (int64_t)min(c >> 7, last) * nkb;
+        const int c = it.c0 + wp * (SW ? 32 : 64);
+        it.b0 = (c >> 7) - (it.c0 >> 7);
+        it.b1 = it.cut = 0;
         if (SW) {
             const int b = (c + g.n_out) >> 7;
-            w1 = g.ws + (int64_t)min(b, last) * nkb;
-            w2 = g.ws + (int64_t)min(b + 1, last) * nkb;
-            cut = ((b + 1) << 7) - (c + g.n_out);       // of the wave's 32 up rows
+            it.b1 = 32 + b - ((it.c0 + g.n_out) >> 7);
+            it.cut = ((b + 1) << 7) - (c + g.n_out);      // of the wave's 32 up rows
         }
+        return it;
     };
-    auto compute = [&](int slot) {
-        const uint8_t *sp = smem + slot * T::Stage, *sq = sp + T::PB;
-        const float *sx = reinterpret_cast<const float *>(sq + T::QB);
-        const float s0 = w0[ckb], s1 = SW ? w1[ckb] : 0.f, s2 = GLU == 2 ? w2[ckb] : 0.f;
-        v8i a[NP];
+    // Operands of a step in registers: all of the weights' (a), x's in a ring
+    // of three (b), read from LDS two row tiles ahead of the MFMAs; a row
+    // tile's products (t) are scaled and added while the next one's are formed.
+    v8i a[NP], b[3];
+    float x[3], s0 = 0.f, s1 = 0.f, s2 = 0.f;
+    v4f t[2][NP];
+    auto read_b = [&](int slot, int n) {
+        const uint8_t *sq = smem + slot * T::Stage + T::PB;
+        b[n % 3] = join8(lds_read16(sq + q_off + n * 2048), lds_read16(sq + (q_off ^ 64) + n * 2048));
+        x[n % 3] = reinterpret_cast<const float *>(sq + T::QB)[wq * (TQ / WQ) + n * 16 + i16];
+    };
+    auto read_head = [&](int slot, const Item &it) {
+        const uint8_t *sp = smem + slot * T::Stage;
+        const float *sw = reinterpret_cast<const float *>(sp + T::PB + T::QB + T::XB);
 #pragma unroll
         for (int m = 0; m < NP; ++m) {
             const int o = (m >> 1) * 32 * 128 + (m & 1) * 4 * 128;
             a[m] = join8(lds_read16(sp + p_off + o), lds_read16(sp + (p_off ^ 64) + o));
         }
+        read_b(slot, 0);
+        read_b(slot, 1);
+        s0 = sw[it.b0];
+        if (SW) s1 = sw[it.b1];
+        if (GLU == 2) s2 = sw[it.b1 + 1];
+    };
+    auto add = [&](int n, float xn, float f0, float f1, float f2, int cut) {
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            const v8i b = join8(lds_read16(sq + q_off + n * 2048), lds_read16(sq + (q_off ^ 64) + n * 2048));
-            const float x = sx[wq * (TQ / WQ) + n * 16 + i16];
+        for (int m = 0; m < NP; ++m) {
+            if (GLU == 2 && m >= 2) {
+                const int r = 8 * grp + 4 * (m & 1);      // the lane's first up row of four
 #pragma unroll
-            for (int m = 0; m < NP; ++m) {
-                const v4f t = mfma16x16x128(a[m], b);
-                if (GLU == 2 && m >= 2) {
-                    const int r = 8 * grp + 4 * (m & 1);         // the lane's first up row of four
+                for (int v = 0; v < 4; ++v) acc[m][n][v] += t[n & 1][m][v] * (xn * (r + v < cut ? f1 : f2));
+            } else {
+                const float f = xn * (SW && m >= 2 ? f1 : f0);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[m][n][v] += t[v] * (x * (r + v < cut ? s1 : s2));
-                } else {
-                    const float s = x * (SW && m >= 2 ? s1 : s0);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[m][n][v] += t[v] * s;
-                }
+                for (int v = 0; v < 4; ++v) acc[m][n][v] += t[n & 1][m][v] * f;
             }
+            // keeps the additions here: the compiler would gather them behind
+            // the last MFMA and spill the products until then
+            asm volatile("" : "+v"(acc[m][n]));
         }
     };
-    const Store8 store{g, vec_ok(g)};
-    auto epilogue = [&]() {
-        const int cw = cc0 + wp * (SW ? 32 : 64) + 8 * grp;
+    auto epilogue = [&](const Item &it) {
+        if (SPLIT && g.nsplit > 1) {             // FP32 sums, 1 KB per wave and MFMA tile
+            float *d = g.part + ((int64_t)cit * NW + w) * (NP * NQ * 256) + l * 4;
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) *reinterpret_cast<v4f *>(d + (m * NQ + n) * 256) = acc[m][n];
+            return;
+        }
+        const int cw = it.c0 + wp * (SW ? 32 : 64) + 8 * grp;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            const int64_t m = cm0 + wq * (TQ / WQ) + 16 * n + i16;
+            const int64_t m = it.m0 + wq * (TQ / WQ) + 16 * n + i16;
             if (m >= g.M) continue;
 #pragma unroll
             for (int p = 0; p < NP / 2; ++p) {
                 const int c = cw + (SW ? 0 : 32 * p);
                 if (c >= g.n_out) continue;
-                if (g.nsplit > 1) {              // FP32 partial of z, columns as the weight rows
-                    float *d = g.part + ((int64_t)csp * g.M + m) * g.ld_part + c + (SW && p ? g.n_out : 0);
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        if (c + v < g.n_out) d[v] = acc[2 * p + (v >> 2)][n][v & 3];
-                    continue;
-                }
                 if (SW && p) continue;
                 float z[8];
 #pragma unroll
@@ -357,78 +405,134 @@ linear_tile_kernel(LinearArgs g) {
                     }
                     z[v] = SW ? silu(z[v]) * u : act1(z[v], g.act);
                 }
-                store(m, c, z);
+                store8(g, m, c, z);
             }
         }
     };
 
     load_setup();
-    comp_setup();
+    Item cur = item_of(cit);
+    int ckb = cur.kb;
     clear();
-    int issued = 0, done = 0;
-    auto issue_next = [&]() {
-        if (lit >= end) return;
-        issue(issued % S);
-        ++issued;
-    };
-    for (int s = 0; s < S - 1; ++s) issue_next();
-    while (true) {
-        // the stage's copies have landed for this wave, then for all; every
-        // read of the slot the next copies overwrite is complete
+    int issued = 0, done = 0, islot = 0, slot = 0;        // stages issued and multiplied, their slots
+    // The stage's copies have landed for this wave, then for all; every read
+    // of the slot that the next copies overwrite is complete.
+    auto next_stage = [&]() {
         constexpr int ahead = (S - 2) * (JP + JQ);
         if (S > 2 && issued - done == S - 1) wait_vmcnt<(ahead < 63 ? ahead : 63)>();
         else wait_vmcnt<0>();
         __builtin_amdgcn_s_waitcnt(0xC07F);               // lgkmcnt(0)
         stage_barrier();
-        issue_next();
-        compute(done % S);
+    };
+    for (int s = 0; s < S - 1 && lit < end; ++s) {
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) issue_copy(c, islot);
+        stage_issued();
+        ++issued;
+        islot = islot + 1 == S ? 0 : islot + 1;
+    }
+    next_stage();
+    while (true) {
+        // The products of this step, and beside them the copies of the stage
+        // S - 1 steps ahead, a few per row tile: copies all issued at once
+        // would hold every wave up before its first MFMA.
+        read_head(slot, cur);
+        const bool load = lit < end;
+        constexpr int kPer = (2 * kCopies + NQ - 1) / NQ;
+        float xp = 0.f;
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            if (n + 2 < NQ) read_b(slot, n + 2);
+            if (load) {
+#pragma unroll
+                for (int c = n * kPer; c < (n + 1) * kPer && c < kCopies; ++c) issue_copy(c, islot);
+            }
+#pragma unroll
+            for (int m = 0; m < NP; ++m) t[n & 1][m] = mfma16x16x128(a[m], b[n % 3]);
+            if (n > 0) add(n - 1, xp, s0, s1, s2, cur.cut);
+            xp = x[n % 3];
+            // reads ahead, then each MFMA beside a quarter of the previous row
+            // tile's additions
+            __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+            for (int m = 0; m < NP; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        add(NQ - 1, xp, s0, s1, s2, cur.cut);
+        if (load) {
+            stage_issued();
+            ++issued;
+            islot = islot + 1 == S ? 0 : islot + 1;
+        }
         ++done;
-        if (++ckb == ckend) {
-            epilogue();
+        slot = slot + 1 == S ? 0 : slot + 1;
+        if (issued > done) next_stage();
+        if (++ckb == cur.kend) {
+            epilogue(cur);
             cit += step;
             if (cit >= end) break;
-            comp_setup();
             clear();
+            cur = item_of(cit);
+            ckb = cur.kb;
         }
     }
 }
 
-// Adds the splits of z in order, then the epilogue; 8 columns per thread.
+// Adds the splits' sums in order, then the epilogue: a thread takes the 8
+// columns of one row that a lane of the tile kernel held.
+template <int TP, int TQ, int WP, int WQ, int GLU>
 __global__ void __launch_bounds__(256)
 linear_join_kernel(LinearArgs g) {
-    const int per = (g.n_out + 7) / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= g.M * per) return;
-    const int64_t m = i / per;
-    const int c = (int)(i - m * per) * 8;
-    const bool sw = g.act == kActSwiglu;
-    float z[8], u[8];
-    for (int v = 0; v < 8; ++v) z[v] = u[v] = 0.f;
+    constexpr int NW = WP * WQ, NP = TP / WP / 16, NQ = TQ / WQ / 16, TC = GLU ? TP / 2 : TP;
+    constexpr int NG = GLU ? 1 : NP / 2;                  // column groups of a wave
+    const int l = threadIdx.x & 63;
+    int i = (int)(((int64_t)blockIdx.x * 256 + threadIdx.x) >> 6);
+    const int n = i % NQ;
+    i /= NQ;
+    const int p = i % NG;
+    i /= NG;
+    const int w = i % NW, tile = i / NW;
+    const int nct = (g.n_out + TC - 1) / TC;
+    const int wp = w % WP, wq = w / WP;
+    int rt, ct;
+    panel_tile<8>(tile, (int)((g.M + TQ - 1) / TQ), nct, rt, ct);
+    const int64_t m = (int64_t)rt * TQ + wq * (TQ / WQ) + 16 * n + (l & 15);
+    const int c = ct * TC + wp * (GLU ? 32 : 64) + 32 * p + 8 * (l >> 4);
+    if (m >= g.M || c >= g.n_out) return;
+    v4f z[2], u[2];
+    for (int h = 0; h < 2; ++h) z[h] = u[h] = v4f{0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < g.nsplit; ++s) {
-        const float *p = g.part + ((int64_t)s * g.M + m) * g.ld_part + c;
-        for (int v = 0; v < 8; ++v)
-            if (c + v < g.n_out) {
-                z[v] += p[v];
-                if (sw) u[v] += p[v + g.n_out];
-            }
-    }
-    for (int v = 0; v < 8; ++v) {
-        if (g.bias && c + v < g.n_out) {
-            z[v] += g.bias[c + v];
-            if (sw) u[v] += g.bias[c + v + g.n_out];
+        const float *d = g.part + (((int64_t)tile * g.nsplit + s) * NW + w) * (NP * NQ * 256) + l * 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            z[h] += *reinterpret_cast<const v4f *>(d + ((2 * p + h) * NQ + n) * 256);
+            if (GLU) u[h] += *reinterpret_cast<const v4f *>(d + ((2 + h) * NQ + n) * 256);
         }
-        z[v] = sw ? silu(z[v]) * u[v] : act1(z[v], g.act);
     }
-    Store8{g, vec_ok(g)}(m, c, z);
+    float o[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        o[v] = z[v >> 2][v & 3];
+        float y = GLU ? u[v >> 2][v & 3] : 0.f;
+        if (g.bias && c + v < g.n_out) {
+            o[v] += g.bias[c + v];
+            if (GLU) y += g.bias[c + v + g.n_out];
+        }
+        o[v] = GLU ? silu(o[v]) * y : act1(o[v], g.act);
+    }
+    store8(g, m, c, o);
 }
 
 // ----------------------------------------------------------------- launch
 
-template <int TP, int TQ, int WP, int WQ, int S, int GLU>
+template <int TP, int TQ, int WP, int WQ, int S, int GLU, bool SPLIT>
 hipError_t launch_tile(const LinearArgs &g, hipStream_t st) {
     using T = LTile<TP, TQ, WP, WQ, S>;
     static std::atomic<uint64_t> done{0};
-    auto fn = linear_tile_kernel<TP, TQ, WP, WQ, S, GLU>;
+    auto fn = linear_tile_kernel<TP, TQ, WP, WQ, S, GLU, SPLIT>;
     hipError_t e = raise_lds_limit(done, (const void *)fn, (int)T::Smem);
     if (e != hipSuccess) return e;
     const int tc = GLU ? TP / 2 : TP;
@@ -438,9 +542,9 @@ hipError_t launch_tile(const LinearArgs &g, hipStream_t st) {
     grid = (grid + 7) / 8 * 8;
     fn<<<(unsigned)grid, 64 * WP * WQ, T::Smem, st>>>(g);
     e = hipGetLastError();
-    if (e != hipSuccess || g.nsplit == 1) return e;
-    const int64_t n = g.M * ((g.n_out + 7) / 8);
-    linear_join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
+    if (e != hipSuccess || !SPLIT || g.nsplit == 1) return e;
+    const int64_t waves = items / g.nsplit * (WP * WQ) * (GLU ? 1 : T::NP / 2) * T::NQ;
+    linear_join_kernel<TP, TQ, WP, WQ, GLU><<<(unsigned)((waves + 3) / 4), 256, 0, st>>>(g);
     return hipGetLastError();
 }
 
@@ -448,21 +552,21 @@ template <int GLU>
 hipError_t launch(const LinearArgs &g, hipStream_t st) {
     constexpr bool SW = GLU != 0;
     switch (g.form) {
-        case kLinStream1:
-        case kLinStream2:
-        case kLinStream4: {
-            const int nq = g.form == kLinStream1 ? 1 : g.form == kLinStream2 ? 2 : 4;
-            const dim3 grid((g.n_out + (SW ? 7 : 15)) / (SW ? 8 : 16), (unsigned)((g.M + 16 * nq - 1) / (16 * nq)));
-            if (nq == 1) linear_stream_kernel<1, 8, 7, SW><<<grid, 512, 0, st>>>(g);
-            else if (nq == 2) linear_stream_kernel<2, 8, 4, SW><<<grid, 512, 0, st>>>(g);
-            else linear_stream_kernel<4, 8, 2, SW><<<grid, 512, 0, st>>>(g);
+        case kLinStream: {
+            const unsigned grid = (unsigned)((g.n_out + (SW ? 7 : 15)) / (SW ? 8 : 16));
+            if (g.M > 48) linear_stream_kernel<4, 16, 1, SW><<<grid, 1024, 0, st>>>(g);
+            else if (g.M > 32) linear_stream_kernel<3, 16, 2, SW><<<grid, 1024, 0, st>>>(g);
+            else if (g.M > 16) linear_stream_kernel<2, 8, 3, SW><<<grid, 512, 0, st>>>(g);
+            else if (g.K > 32 * 128 && (int)grid <= device_cu_count())
+                linear_stream_kernel<1, 8, 7, SW><<<grid, 512, 0, st>>>(g);
+            else linear_stream_kernel<1, 8, 4, SW><<<grid, 512, 0, st>>>(g);
             return hipGetLastError();
         }
         case kLinTile256:
-            if constexpr (GLU < 2) return launch_tile<256, 256, 4, 2, 2, GLU>(g, st);
+            if constexpr (GLU < 2) return launch_tile<256, 256, 4, 2, 2, GLU, false>(g, st);
             [[fallthrough]];
-        case kLinTile128: return launch_tile<256, 128, 4, 2, 3, GLU>(g, st);
-        default: return launch_tile<128, 64, 2, 2, 3, GLU>(g, st);
+        case kLinTile128: return launch_tile<256, 128, 4, 2, 3, GLU, false>(g, st);
+        default: return launch_tile<128, 64, 2, 2, 6, GLU, true>(g, st);
     }
 }
 
@@ -475,24 +579,23 @@ size_t linear_workspace(LinearArgs &a, void *ws) {
     a.nsplit = 1;
     a.part = nullptr;
     if (a.M <= 64) {
-        a.form = a.M <= 16 ? kLinStream1 : a.M <= 32 ? kLinStream2 : kLinStream4;
+        a.form = kLinStream;
         return 0;
     }
     if (items(256, 256) >= 200) a.form = kLinTile256;
     else if (items(256, 128) >= 200) a.form = kLinTile128;
     else {
         a.form = kLinTile64;
-        int64_t s = 512 / items(128, 64);
+        int64_t s = 256 / items(128, 64);
         if (s > nkb / 4) s = nkb / 4;
         if (s > 1) {
             const int per = (int)((nkb + s - 1) / s);
             a.nsplit = (nkb + per - 1) / per;                      // none empty
         }
     }
-    a.ld_part = (n + 3) / 4 * 4;
     if (a.nsplit == 1) return 0;
     a.part = (float *)ws;
-    return (size_t)a.nsplit * a.M * a.ld_part * 4;
+    return (size_t)a.nsplit * items(128, 64) * (128 * 64 * 4);
 }
 
 hipError_t launch_linear(const LinearArgs &a, hipStream_t st) {
