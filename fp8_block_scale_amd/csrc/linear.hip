@@ -152,38 +152,63 @@ struct LTile {
     static_assert(NP % 4 == 0 && JP >= 1 && JQ >= 1 && XW < NW && Smem <= 160 * 1024, "tile");
 };
 
-// Stores a lane's results of a column group, 8 consecutive columns of one
-// row, by one 16-byte access (which global memory takes at any alignment:
-// rows of an odd number of columns are 2-byte aligned only).
+// A lane's results of a column group are 8 consecutive columns of one row.
+// Rows of an odd number of columns are 2-byte aligned only: global memory
+// takes 16-byte accesses at any alignment.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef v4f v4f_any __attribute__((aligned(4)));
 
-__device__ __forceinline__ void store8(const LinearArgs &g, int64_t m, int col, float (&z)[8]) {
-    const int n = g.n_out - col;                 // valid columns from here
-    if (g.res) {
-        const uint16_t *r = g.res + m * g.ld_res + col;
-        if (n >= 8) {
-            const u32x4 o = *reinterpret_cast<const u32x4_any *>(r);
+// b[0, 8) = bias[c, c + 8), 0 past n (and without a bias)
+__device__ __forceinline__ void load_bias8(const float *bias, int c, int n, float (&b)[8]) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                z[2 * v] += bf16_bits_to_f32(o[v] & 0xffffu);
-                z[2 * v + 1] += bf16_bits_to_f32(o[v] >> 16);
-            }
-        } else {
+    for (int v = 0; v < 8; ++v) b[v] = 0.f;
+    if (!bias) return;
+    if (c + 8 <= n) {
+        const v4f lo = *reinterpret_cast<const v4f_any *>(bias + c), hi = *reinterpret_cast<const v4f_any *>(bias + c + 4);
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-                if (v < n) z[v] += bf16_bits_to_f32(r[v]);
+        for (int v = 0; v < 4; ++v) {
+            b[v] = lo[v];
+            b[4 + v] = hi[v];
         }
+    } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            if (c + v < n) b[v] = bias[c + v];
     }
+}
+
+__device__ __forceinline__ void act8(float (&z)[8], int act) {
+    if (act == kActSilu) {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) z[v] = silu(z[v]);
+    } else if (act == kActGelu) {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) z[v] = gelu(z[v]);
+    }
+}
+
+// z += residual, out = bf16(z) at row m, columns [col, col + 8); `res` holds
+// the residual's 8 values where all 8 columns exist.
+__device__ __forceinline__ void store8(const LinearArgs &g, int64_t m, int col, float (&z)[8], const u32x4 &res) {
     uint16_t *d = g.out + m * g.ld_out + col;
-    if (n >= 8) {
+    if (col + 8 <= g.n_out) {
         u32x4 o;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) o[v] = f32_to_bf16_bits(z[2 * v]) | (f32_to_bf16_bits(z[2 * v + 1]) << 16);
+        for (int v = 0; v < 4; ++v) {
+            if (g.res) {
+                z[2 * v] += bf16_bits_to_f32(res[v] & 0xffffu);
+                z[2 * v + 1] += bf16_bits_to_f32(res[v] >> 16);
+            }
+            o[v] = f32_to_bf16_bits(z[2 * v]) | (f32_to_bf16_bits(z[2 * v + 1]) << 16);
+        }
         *reinterpret_cast<u32x4_any *>(d) = o;
     } else {
 #pragma unroll
         for (int v = 0; v < 8; ++v)
-            if (v < n) d[v] = (uint16_t)f32_to_bf16_bits(z[v]);
+            if (col + v < g.n_out) {
+                if (g.res) z[v] += bf16_bits_to_f32(g.res[m * g.ld_res + col + v]);
+                d[v] = (uint16_t)f32_to_bf16_bits(z[v]);
+            }
     }
 }
 
@@ -384,28 +409,41 @@ linear_tile_kernel(LinearArgs g) {
                 for (int n = 0; n < NQ; ++n) *reinterpret_cast<v4f *>(d + (m * NQ + n) * 256) = acc[m][n];
             return;
         }
-        const int cw = it.c0 + wp * (SW ? 32 : 64) + 8 * grp;
+        // The residual's reads of NB row tiles go out together: one wait for
+        // memory per NB tiles instead of one per tile.
+        constexpr int NB = NQ < 4 ? NQ : 4;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            const int64_t m = it.m0 + wq * (TQ / WQ) + 16 * n + i16;
-            if (m >= g.M) continue;
+        for (int p = 0; p < (SW ? 1 : NP / 2); ++p) {
+            const int c = it.c0 + wp * (SW ? 32 : 64) + 8 * grp + 32 * p;
+            if (c >= g.n_out) continue;
+            float bz[8], bu[8];
+            load_bias8(g.bias, c, g.n_out, bz);
+            if (SW) load_bias8(g.bias ? g.bias + g.n_out : nullptr, c, g.n_out, bu);
 #pragma unroll
-            for (int p = 0; p < NP / 2; ++p) {
-                const int c = cw + (SW ? 0 : 32 * p);
-                if (c >= g.n_out) continue;
-                if (SW && p) continue;
-                float z[8];
+            for (int n0 = 0; n0 < NQ; n0 += NB) {
+                u32x4 r[NB];
 #pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                    z[v] = acc[2 * p + (v >> 2)][n][v & 3];
-                    float u = SW ? acc[2 + (v >> 2)][n][v & 3] : 0.f;
-                    if (g.bias && c + v < g.n_out) {
-                        z[v] += g.bias[c + v];
-                        if (SW) u += g.bias[c + v + g.n_out];
-                    }
-                    z[v] = SW ? silu(z[v]) * u : act1(z[v], g.act);
+                for (int n = 0; n < NB; ++n) {
+                    r[n] = u32x4{0u, 0u, 0u, 0u};
+                    const int64_t m = it.m0 + wq * (TQ / WQ) + 16 * (n0 + n) + i16;
+                    if (g.res && c + 8 <= g.n_out && m < g.M)
+                        r[n] = *reinterpret_cast<const u32x4_any *>(g.res + m * g.ld_res + c);
                 }
-                store8(g, m, c, z);
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const int64_t m = it.m0 + wq * (TQ / WQ) + 16 * (n0 + n) + i16;
+                    if (m >= g.M) continue;
+                    float z[8];
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) z[v] = acc[2 * p + (v >> 2)][n0 + n][v & 3] + bz[v];
+                    if (SW) {
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) z[v] = silu(z[v]) * (acc[2 + (v >> 2)][n0 + n][v & 3] + bu[v]);
+                    } else {
+                        act8(z, g.act);
+                    }
+                    store8(g, m, c, z, r[n]);
+                }
             }
         }
     };
@@ -512,18 +550,18 @@ linear_join_kernel(LinearArgs g) {
             if (GLU) u[h] += *reinterpret_cast<const v4f *>(d + ((2 + h) * NQ + n) * 256);
         }
     }
-    float o[8];
+    float o[8], bz[8], bu[8];
+    u32x4 r = {0u, 0u, 0u, 0u};
+    load_bias8(g.bias, c, g.n_out, bz);
+    if (GLU) load_bias8(g.bias ? g.bias + g.n_out : nullptr, c, g.n_out, bu);
+    if (g.res && c + 8 <= g.n_out) r = *reinterpret_cast<const u32x4_any *>(g.res + m * g.ld_res + c);
 #pragma unroll
     for (int v = 0; v < 8; ++v) {
-        o[v] = z[v >> 2][v & 3];
-        float y = GLU ? u[v >> 2][v & 3] : 0.f;
-        if (g.bias && c + v < g.n_out) {
-            o[v] += g.bias[c + v];
-            if (GLU) y += g.bias[c + v + g.n_out];
-        }
-        o[v] = GLU ? silu(o[v]) * y : act1(o[v], g.act);
+        o[v] = z[v >> 2][v & 3] + bz[v];
+        if (GLU) o[v] = silu(o[v]) * (u[v >> 2][v & 3] + bu[v]);
     }
-    store8(g, m, c, o);
+    if (!GLU) act8(o, g.act);
+    store8(g, m, c, o, r);
 }
 
 // ----------------------------------------------------------------- launch
