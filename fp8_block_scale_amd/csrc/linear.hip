@@ -620,17 +620,36 @@ size_t linear_workspace(LinearArgs &a, void *ws) {
         a.form = kLinStream;
         return 0;
     }
-    if (items(256, 256) >= 200) a.form = kLinTile256;
-    else if (items(256, 128) >= 200) a.form = kLinTile128;
-    else {
-        a.form = kLinTile64;
-        int64_t s = 256 / items(128, 64);
-        if (s > nkb / 4) s = nkb / 4;
-        if (s > 1) {
-            const int per = (int)((nkb + s - 1) / s);
-            a.nsplit = (nkb + per - 1) / per;                      // none empty
+    // Tile form by estimated time: rounds of tiles over the CUs, each nkb
+    // steps and a fill and store of the tile.  Per step and per tile, measured
+    // with every CU busy: 256 x 256 2.0 and 10 us, 256 x 128 1.1 and 6 us,
+    // 128 x 64 0.67 and 3 us.  (The larger tile does the most per step, the
+    // smaller ones lose less to a last, partly filled round.)
+    const int64_t cus = 256;
+    auto est = [&](int64_t it, int steps, double step, double tile) {
+        return (double)((it + cus - 1) / cus) * (steps * step + tile);
+    };
+    const double t256 = est(items(256, 256), nkb, 2.0, 10.0), t128 = est(items(256, 128), nkb, 1.1, 6.0);
+    // the small tile may split K over the idle CUs (at least 4 steps each);
+    // joining the parts costs about 4 us
+    const int64_t it64 = items(128, 64);
+    int64_t sp = cus / it64 < nkb / 4 ? cus / it64 : nkb / 4;
+    double t64 = est(it64, nkb, 0.67, 3.0);
+    if (sp > 1) {
+        const int per = (int)((nkb + sp - 1) / sp);
+        sp = (nkb + per - 1) / per;                                // none empty
+        const double t = est(it64 * sp, per, 0.67, 3.0) + 4.0;
+        if (t < t64) {
+            t64 = t;
+            a.nsplit = (int)sp;
         }
     }
+    // SwiGLU with straddling blocks has no 256 x 256 form (registers)
+    const bool no256 = a.act == kActSwiglu && a.n_out % 32 != 0;
+    a.form = kLinTile64;
+    if (t128 < t64) a.form = kLinTile128;
+    if (!no256 && t256 < (t128 < t64 ? t128 : t64)) a.form = kLinTile256;
+    if (a.form != kLinTile64) a.nsplit = 1;
     if (a.nsplit == 1) return 0;
     a.part = (float *)ws;
     return (size_t)a.nsplit * items(128, 64) * (128 * 64 * 4);
