@@ -146,9 +146,12 @@ struct Tile {
     static constexpr int JQ = (QB / 1024 + NW - 1) / NW;
     static constexpr int Ahead = (S - 2) * (JP + QB / 1024 / NW);   // copies that may be in flight
     static constexpr int NP = TP / WP / 16, NQ = TQ / WQ / 16;
-    static constexpr size_t Smem = (size_t)S * Stage + (QKS ? 0 : S * TQ * 4);
-    static_assert(NP % 2 == 0 && JP >= 1 && Smem <= 160 * 1024, "tile");
-    static_assert(!QKS || (TP == TQ && NQ % 2 == 0), "dw tile");
+    // behind the stages: the routes of an item's rows (forward, dx; a ring of
+    // S items), or the routes of a stage's rows (two) and all experts' rows (dw)
+    static constexpr int Tail = QKS ? 2 * 256 : S * TQ * 4;
+    static constexpr size_t Smem = (size_t)S * Stage + Tail;
+    static_assert(NP % 2 == 0 && JP >= 1 && NW % 2 == 0 && Smem <= 160 * 1024, "tile");
+    static_assert(!QKS || (TP == TQ && NQ % 2 == 0 && S == 2), "dw tile");
 };
 
 __device__ __forceinline__ u32x4 lds_read_tr(const uint8_t *p, int second) {
@@ -164,8 +167,11 @@ __global__ void __launch_bounds__(64 * WP * WQ)
 group_tile_kernel(GroupMmArgs g) {
     using T = Tile<F16, OP, TP, TQ, WP, WQ, S>;
     constexpr int NW = T::NW, JP = T::JP, JQ = T::JQ, NP = T::NP, NQ = T::NQ;
+    constexpr bool DW = OP == kGmmDw;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    int *rids = reinterpret_cast<int *>(smem + (size_t)S * T::Stage);   // [S][TQ] routes of an item's rows
+    int *rids = reinterpret_cast<int *>(smem + (size_t)S * T::Stage);          // [S][TQ] (forward, dx)
+    int *sids = rids;                                                          // [2][64] (dw)
+    int2 *segs = reinterpret_cast<int2 *>(smem + (size_t)S * T::Stage + 512);  // [E] (dw)
 
     const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6);
     const int wp = w % WP, wq = w / WP;
@@ -174,7 +180,7 @@ group_tile_kernel(GroupMmArgs g) {
 
     // ---- the items of this workgroup: a contiguous range per XCD
     int n_items, qtiles = 1, ntiles = 0;
-    if (OP == kGmmDw) {
+    if (DW) {
         qtiles = (g.N + TQ - 1) / TQ;
         n_items = g.E * qtiles * nct * g.nsplit;
     } else {
@@ -187,125 +193,157 @@ group_tile_kernel(GroupMmArgs g) {
     int lit = (int)((int64_t)xcd * n_items / 8) + (blockIdx.x >> 3);     // load cursor
     int cit = lit;                                                        // compute cursor
     if (cit >= end) return;
+    if (DW) {
+        for (int i = tid; i < g.E; i += 64 * NW) segs[i] = g.segs[i];
+        __syncthreads();
+    }
 
-    // ---- load side: state of the item being loaded
-    const uint8_t *pbase = nullptr;          // uniform; advances along the contraction
-    uint32_t poff[JP];
-    const uint8_t *qptr[JQ];
-    const uint8_t *xcol = nullptr, *dycol = nullptr;      // dw: this lane's columns
-    int lkt = 0, lnk = 0, lord = 0;          // stage in the item, its stages, its ordinal
-    int lrow = 0, lrows = 0;                 // dw: first plan row, rows
-    int nid[JQ];                             // dw: routes of the next stage's rows
-    const int nred = OP == kGmmFwd ? g.K : g.N;
-
-    auto kr_of = [&](int j) { return (j * NW + w) * (1024 / (TP * 2)) + l / (TP / 8); };   // KS row in stage
-    // copies of the KC layout: lane l copies row 8 (j NW + w) + l / 8, chunk position l % 8
-    const int kc_p = ((l & 7) ^ (((l >> 3) & 3) | ((w & 1) << 2)));     // global chunk (P swizzle)
-    const int kc_q = ((l & 7) ^ (l >> 3));                              // global chunk (Q swizzle)
-    static_assert(NW % 2 == 0, "the swizzles assume an even wave count");
-
-    auto ids_ahead = [&](int kt) {
-        for (int j = 0; j < JQ; ++j) {
-            const int p = kt * 64 + kr_of(j);
-            nid[j] = p < lrows ? g.sorted[lrow + p] : -1;
-        }
+    struct Item {
+        int e, ct, qt, sp;           // expert, column tile, row tile and split (dw)
+        int row0, rows;              // its plan rows
     };
+    auto item_of = [&](int i) {
+        Item it = {};
+        if (DW) {
+            it.sp = i % g.nsplit;
+            i /= g.nsplit;
+            int rt;
+            const int per_e = qtiles * nct;
+            it.e = i / per_e;
+            panel_tile<4>(i - it.e * per_e, qtiles, nct, rt, it.ct);
+            it.qt = rt;
+            const int2 sg = segs[it.e];
+            const int seg_rows = uni(sg.y);
+            const int per = (seg_rows + 64 * g.nsplit - 1) / (64 * g.nsplit) * 64;   // rows per split
+            const int r0 = it.sp * per;
+            const int left = seg_rows - r0;
+            it.row0 = uni(sg.x) + (left > 0 ? r0 : 0);
+            it.rows = left < 0 ? 0 : left < per ? left : per;
+        } else {
+            int rt;
+            panel_tile<4>(i, ntiles, nct, rt, it.ct);
+            const int4 t = g.tiles[rt];
+            it.row0 = uni(t.x);
+            it.rows = uni(t.y);
+            it.e = uni(t.z);
+        }
+        return it;
+    };
+    const int nred = OP == kGmmFwd ? g.K : g.N;               // the contraction (forward, dx)
+    auto stages_of = [&](const Item &it) {
+        return DW ? (it.rows > 0 ? (it.rows + 63) / 64 : 1) : (nred + 63) / 64;
+    };
+
+    // ---- load side.  A copy instruction of a wave fills 1 KB of a tile: 8
+    // rows of 128 bytes, or 2 (TP = 256) or 4 rows of the output's columns.
+    constexpr int RPI = 1024 / (TP * 2);                     // KS rows per copy
+    const int lrow = l >> 3;
+    const int kc_p = (l & 7) ^ ((lrow & 3) | ((w & 1) << 2));           // KC: global chunk (P swizzle)
+    const int kc_q = (l & 7) ^ lrow;                                    // KC: global chunk (Q swizzle)
+    const int ks_l = l / (TP / 8);                                      // KS: row in the copy
+    const int ks_chunk = (l % (TP / 8)) ^ (((w * RPI + ks_l) & 3) << 2);   // (NW RPI is a multiple of 4)
+    static_assert(!T::PKS || (NW * RPI) % 4 == 0, "the swizzle is the same for all copies");
+    const uint8_t *pbase = nullptr;          // P, uniform: the wave's first copy of the stage
+    uint32_t poff = 0;                       // its lane offset
+    int plast = 0;                           // KC: last row of the tile that exists
+    const uint8_t *qptr[JQ];                 // Q (forward, dx): each copy's row, gathered
+    const uint8_t *xcol = nullptr, *dycol = nullptr;         // dw: the lane's columns
+    const int64_t pstep = T::PKS ? (int64_t)(NW * RPI) * g.K * 2 : (int64_t)(8 * NW) * g.K * 2;
+    const int64_t padv = T::PKS ? (int64_t)64 * g.K * 2 : 128;          // stage to stage
+    Item ld = item_of(lit), ld_next = ld;
+    int lkt = 0, lnk = 0, lord = 0;          // stage in the item, its stages, its ordinal
 
     auto load_setup = [&]() {
-        if (OP == kGmmDw) {
-            int i = lit;
-            const int sp = i % g.nsplit;
-            i /= g.nsplit;
-            const int ct = i % nct;
-            i /= nct;
-            const int qt = i % qtiles, e = i / qtiles;
-            const int2 sg = g.segs[e];
-            const int per = ((sg.y + 64 * g.nsplit - 1) / (64 * g.nsplit)) * 64;   // rows per split
-            const int r0 = sp * per;
-            int rows = sg.y - r0;
-            rows = rows < 0 ? 0 : (rows < per ? rows : per);
-            lrow = uni(sg.x) + uni(r0);
-            lrows = uni(rows);
-            lnk = lrows > 0 ? (lrows + 63) / 64 : 1;
-            const int ch = (l % (TP / 8)) ^ ((kr_of(0) & 3) << 2);
-            const int pc = ct * TP + ch * 8, qc = qt * TQ + ch * 8;
+        lkt = 0;
+        lnk = stages_of(ld);
+        if (DW) {
+            const int pc = ld.ct * TP + ks_chunk * 8, qc = ld.qt * TQ + ks_chunk * 8;
             xcol = reinterpret_cast<const uint8_t *>(g.x + (pc < g.K ? pc : 0));
             dycol = reinterpret_cast<const uint8_t *>(g.dy + (qc < g.N ? qc : 0));
-            ids_ahead(0);
-        } else {
-            int rt, ct;
-            panel_tile<4>(lit, ntiles, nct, rt, ct);
-            const int4 t = g.tiles[rt];
-            const int p0 = ct * TP;
-            const int e = uni(t.z), row0 = uni(t.x), rows = uni(t.y);
-            lnk = (nred + 63) / 64;
-            const uint8_t *we = reinterpret_cast<const uint8_t *>(g.w + (int64_t)e * g.N * g.K);
-            if (T::PKS) {
-                pbase = we + (int64_t)p0 * 2;
-                for (int j = 0; j < JP; ++j) {
-                    const int kr = kr_of(j);
-                    int c = ((l % (TP / 8)) ^ ((kr & 3) << 2)) * 8;
-                    c = p0 + c < g.K ? c : 0;
-                    poff[j] = (uint32_t)kr * (uint32_t)g.K * 2u + (uint32_t)c * 2u;
-                }
-            } else {
-                pbase = we + (int64_t)p0 * g.K * 2;
-                for (int j = 0; j < JP; ++j) {
-                    int row = 8 * (j * NW + w) + (l >> 3);
-                    row = p0 + row < g.N ? row : g.N - 1 - p0;
-                    poff[j] = (uint32_t)row * (uint32_t)g.K * 2u + (uint32_t)kc_p * 16u;
-                }
-            }
-            const uint16_t *src = OP == kGmmFwd ? g.x : g.dy;
-            const int64_t ld = OP == kGmmFwd ? g.ld_x : g.ld_dy;
-            for (int j = 0; j < JQ; ++j) {
-                const int row = 8 * (j * NW + w) + (l >> 3);
-                int r = row < rows ? g.sorted[row0 + row] : -1;
-                if (r >= g.R) r = -1;
-                if (row < TQ && (l & 7) == 0) rids[(lord % S) * TQ + row] = r;
-                int64_t xr = r < 0 ? 0 : (OP == kGmmFwd && !g.per_route ? g.token_of(r) : r);
-                qptr[j] = reinterpret_cast<const uint8_t *>(src + xr * ld) + kc_q * 16;
-            }
+            if (lit + step < end) ld_next = item_of(lit + step);
+            return;
         }
-        lkt = 0;
+        const int p0 = ld.ct * TP;
+        const uint8_t *we = reinterpret_cast<const uint8_t *>(g.w + (int64_t)ld.e * g.N * g.K);
+        if (T::PKS) {
+            pbase = we + ((int64_t)(w * RPI) * g.K + p0) * 2;
+            const int c = p0 + ks_chunk * 8 < g.K ? ks_chunk * 8 : 0;
+            poff = ((uint32_t)ks_l * (uint32_t)g.K + (uint32_t)c) * 2u;
+        } else {
+            pbase = we + (int64_t)(p0 + 8 * w) * g.K * 2;
+            poff = (uint32_t)lrow * (uint32_t)g.K * 2u + (uint32_t)kc_p * 16u;
+            plast = min(TP, g.N - p0) - 1;
+        }
+        const uint16_t *src = OP == kGmmFwd ? g.x : g.dy;
+        const int64_t ldq = OP == kGmmFwd ? g.ld_x : g.ld_dy;
+#pragma unroll
+        for (int j = 0; j < JQ; ++j) {
+            const int row = 8 * (j * NW + w) + lrow;
+            int r = row < ld.rows ? g.sorted[ld.row0 + row] : -1;
+            if (r >= g.R) r = -1;
+            if (row < TQ && (l & 7) == 0) rids[(lord % S) * TQ + row] = r;
+            const int64_t xr = r < 0 ? 0 : (OP == kGmmFwd && !g.per_route ? g.token_of(r) : r);
+            qptr[j] = reinterpret_cast<const uint8_t *>(src + xr * ldq) + kc_q * 16;
+        }
     };
 
-    // one stage of copies into slot
-    auto issue = [&](int slot) {
-        uint8_t *sp = smem + slot * T::Stage;
+    // dw: the routes of stage kt of item it, 64 of them, into ids
+    auto fetch_ids = [&](const Item &it, int kt, int *ids) {
+        if (w != 0) return;
+        const int last = it.rows > 0 ? it.rows - 1 : 0;
+        const int i = kt * 64 + l < last ? kt * 64 + l : last;
+        lds_dma4(g.sorted + it.row0 + i, ids);
+    };
+
+    // Copy c of the next stage into the slot at sp: P's JP copies, then Q's
+    // JQ; in dw P's and Q's c-th together, as they share their rows (whose
+    // routes are at ids).  `tail`: the stage reaches past the end of the
+    // contraction, where both operands are read as zeros.
+    constexpr int kCopies = DW ? JP : JP + JQ;
+    auto issue_copy = [&](int c, uint8_t *sp, const int *ids, bool tail) {
         uint8_t *sq = sp + T::PB;
-        if (OP == kGmmDw) {
-            int id[JQ];
-            for (int j = 0; j < JQ; ++j) id[j] = nid[j];
-            if (lkt + 1 < lnk) ids_ahead(lkt + 1);
-            for (int j = 0; j < JQ; ++j) {
-                const int r = id[j];
-                const bool ok = r >= 0 && r < g.R;
-                const int64_t xr = g.per_route ? r : g.token_of(r);
-                const void *zp = kZeros;
-                lds_dma16(ok ? (const void *)(xcol + xr * g.ld_x * 2) : zp, sp + (j * NW + w) * 1024);
-                lds_dma16(ok ? (const void *)(dycol + (int64_t)r * g.ld_dy * 2) : zp, sq + (j * NW + w) * 1024);
+        const void *zero = kZeros;
+        if (DW) {
+            const int kr = (c * NW + w) * RPI + ks_l;
+            const int r = ids[kr];
+            const bool ok = lkt * 64 + kr < ld.rows && r >= 0 && r < g.R;
+            const int64_t xr = g.per_route ? r : g.token_of(r);
+            lds_dma16(ok ? (const void *)(xcol + xr * g.ld_x * 2) : zero, sp + (c * NW + w) * 1024);
+            lds_dma16(ok ? (const void *)(dycol + (int64_t)r * g.ld_dy * 2) : zero, sq + (c * NW + w) * 1024);
+        } else if (c < JP) {
+            const int left = nred - lkt * 64;              // of the contraction
+            const uint8_t *base = pbase + c * pstep;
+            if (T::PKS) {
+                const void *p = base + poff;
+                if (tail && (c * NW + w) * RPI + ks_l >= left) p = zero;
+                lds_dma16(p, sp + (c * NW + w) * 1024);
+            } else {
+                // rows past the last read the last one: first the copy's
+                // first row moves back (uniform), then each lane by what its
+                // own row exceeds it (at most lrow: the offset stays >= 0)
+                const int r = 8 * (c * NW + w), back = max(r - plast, 0);
+                const int over = max(r - back + lrow - plast, 0);
+                const void *p = base - (int64_t)back * g.K * 2 + (poff - __umul24(over, 2 * g.K));
+                if (tail && kc_p * 8 >= left) p = zero;
+                lds_dma16(p, sp + (c * NW + w) * 1024);
             }
         } else {
-            const int k0 = lkt * 64;
-            const bool tail = k0 + 64 > nred;
-            const uint8_t *pb = pbase + (T::PKS ? (int64_t)k0 * g.K * 2 : (int64_t)k0 * 2);
-            for (int j = 0; j < JP; ++j) {
-                const void *p = pb + poff[j];
-                if (tail && k0 + (T::PKS ? kr_of(j) : kc_p * 8) >= nred) p = kZeros;
-                lds_dma16(p, sp + (j * NW + w) * 1024);
-            }
-            for (int j = 0; j < JQ; ++j) {
-                if ((j + 1) * NW > T::QB / 1024 && j * NW + w >= T::QB / 1024) continue;
-                const void *p = qptr[j] + (int64_t)k0 * 2;
-                if (tail && k0 + kc_q * 8 >= nred) p = kZeros;
-                lds_dma16(p, sq + (j * NW + w) * 1024);
-            }
+            const int j = c - JP;
+            if ((j + 1) * NW > T::QB / 1024 && j * NW + w >= T::QB / 1024) return;
+            const void *p = qptr[j] + (int64_t)lkt * 128;
+            if (tail && kc_q * 8 >= nred - lkt * 64) p = zero;
+            lds_dma16(p, sq + (j * NW + w) * 1024);
         }
+    };
+    auto stage_issued = [&]() {
+        pbase += padv;
         if (++lkt == lnk) {
             lit += step;
             ++lord;
-            if (lit < end) load_setup();
+            if (lit < end) {
+                ld = DW ? ld_next : item_of(lit);
+                load_setup();
+            }
         }
     };
 
@@ -313,7 +351,9 @@ group_tile_kernel(GroupMmArgs g) {
     const int i16 = l & 15, grp = l >> 4;
     v4f acc[NP][NQ];
     auto clear = [&]() {
+#pragma unroll
         for (int a = 0; a < NP; ++a)
+#pragma unroll
             for (int b = 0; b < NQ; ++b) acc[a][b] = v4f{0.f, 0.f, 0.f, 0.f};
     };
     // LDS offsets of this lane's operand reads
@@ -321,36 +361,31 @@ group_tile_kernel(GroupMmArgs g) {
     const int p_kc = (wp * (TP / WP) + 8 * (i16 >> 2) + (i16 & 3)) * 128 + ((grp ^ pf) << 4);
     const int q_kc = (wq * (TQ / WQ) + i16) * 128 + ((grp ^ (i16 & 7)) << 4);
     const int ks_row = 8 * grp + (i16 >> 2);
-    const int ks_x = (i16 >> 2) & 3;
+    const int ks_x = ((i16 >> 2) & 3) << 2;
 
-    auto compute = [&](int slot) {
-        const uint8_t *sp = smem + slot * T::Stage;
+    // A step is 2 NQ units, (contraction half kk, row tile n) in turn.  The
+    // columns' operand (a) of a half and the rows' operand (b) of the units
+    // ahead are read from LDS while earlier units are multiplied.
+    u32x4 a[2][NP], b[4];
+    auto read_a = [&](const uint8_t *sp, int kk) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            if constexpr (T::PKS) {
+                const int ch = (wp * (TP / WP) / 8 + 4 * (n >> 1) + (i16 & 3)) ^ ks_x;
+                a[kk][n] = lds_read_tr(sp + (kk * 32 + ks_row) * (TP * 2) + ch * 16 + (n & 1) * 8, 4 * TP * 2);
+            } else {
+                a[kk][n] = lds_read16(sp + (p_kc ^ (kk << 6)) + (n >> 1) * 32 * 128 + (n & 1) * 4 * 128);
+            }
+        }
+    };
+    auto read_b = [&](const uint8_t *sp, int u) {
         const uint8_t *sq = sp + T::PB;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            u32x4 a[NP], b[NQ];
-#pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                if constexpr (T::PKS) {
-                    const int ch = (wp * (TP / WP) / 8 + 4 * (n >> 1) + (i16 & 3)) ^ (ks_x << 2);
-                    a[n] = lds_read_tr(sp + (kk * 32 + ks_row) * (TP * 2) + ch * 16 + (n & 1) * 8, 4 * TP * 2);
-                } else {
-                    a[n] = lds_read16(sp + (p_kc ^ (kk << 6)) + (n >> 1) * 32 * 128 + (n & 1) * 4 * 128);
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                if constexpr (T::QKS) {
-                    const int ch = (wq * (TQ / WQ) / 8 + 4 * (n >> 1) + (i16 & 3)) ^ (ks_x << 2);
-                    b[n] = lds_read_tr(sq + (kk * 32 + ks_row) * (TQ * 2) + ch * 16 + (n & 1) * 8, 4 * TQ * 2);
-                } else {
-                    b[n] = lds_read16(sq + (q_kc ^ (kk << 6)) + n * 16 * 128);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < NP; ++m)
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) acc[m][n] = mfma32<F16>(a[m], b[n], acc[m][n]);
+        const int kk = u / NQ, n = u % NQ;
+        if constexpr (T::QKS) {
+            const int ch = (wq * (TQ / WQ) / 8 + 4 * (n >> 1) + (i16 & 3)) ^ ks_x;
+            b[u & 3] = lds_read_tr(sq + (kk * 32 + ks_row) * (TQ * 2) + ch * 16 + (n & 1) * 8, 4 * TQ * 2);
+        } else {
+            b[u & 3] = lds_read16(sq + (q_kc ^ (kk << 6)) + n * 16 * 128);
         }
     };
 
@@ -363,34 +398,23 @@ group_tile_kernel(GroupMmArgs g) {
         *reinterpret_cast<u32x4 *>(d) = o;
     };
 
-    auto epilogue = [&](int ord) {
-        int i = cit;
-        int sp = 0, qt = 0, e = 0, ct;
-        if (OP == kGmmDw) {
-            sp = i % g.nsplit;
-            i /= g.nsplit;
-            ct = i % nct;
-            i /= nct;
-            qt = i % qtiles;
-            e = i / qtiles;
-        } else {
-            int rt;
-            panel_tile<4>(i, ntiles, nct, rt, ct);
-        }
-        const int c0 = ct * TP + wp * (TP / WP) + 8 * grp;
+    auto epilogue = [&](const Item &it, int ord) {
+        const int c0 = it.ct * TP + wp * (TP / WP) + 8 * grp;
+#pragma unroll
         for (int n = 0; n < NQ; ++n) {
             const int q = wq * (TQ / WQ) + (T::QKS ? 32 * (n >> 1) + 8 * (i16 >> 2) + 4 * (n & 1) + (i16 & 3)
                                                    : 16 * n + i16);
-            if (OP == kGmmDw) {
-                const int row = qt * TQ + q;
+            if (DW) {
+                const int row = it.qt * TQ + q;
                 if (row >= g.N) continue;
-                const int64_t o = ((int64_t)e * g.N + row) * g.K;
+                const int64_t o = ((int64_t)it.e * g.N + row) * g.K;
+#pragma unroll
                 for (int m = 0; m < NP / 2; ++m) {
                     const int c = c0 + 32 * m;
                     if (c >= g.K) continue;
                     v4f x = acc[2 * m][n], y = acc[2 * m + 1][n];
                     if (g.nsplit > 1) {
-                        float *d = g.part + (int64_t)sp * g.E * g.N * g.K + o + c;
+                        float *d = g.part + (int64_t)it.sp * g.E * g.N * g.K + o + c;
                         *reinterpret_cast<v4f *>(d) = x;
                         *reinterpret_cast<v4f *>(d + 4) = y;
                     } else if (g.out_f32) {
@@ -405,6 +429,7 @@ group_tile_kernel(GroupMmArgs g) {
                         uint16_t *d = (uint16_t *)g.out + o + c;
                         if (g.accumulate) {
                             const u32x4 old = *reinterpret_cast<const u32x4 *>(d);
+#pragma unroll
                             for (int v = 0; v < 2; ++v) {
                                 x[2 * v] += from16<F16>(old[v]);
                                 x[2 * v + 1] += from16<F16>(old[v] >> 16);
@@ -419,8 +444,9 @@ group_tile_kernel(GroupMmArgs g) {
                 const int r = rids[(ord % S) * TQ + q];
                 if (r < 0) continue;
                 if (OP == kGmmDx && !g.per_route) {
-                    if (ct == 0 && wp == 0 && grp == 0) g.rpos[r] = 0;
+                    if (it.ct == 0 && wp == 0 && grp == 0) g.rpos[r] = 0;
                     float *d = g.part + (int64_t)r * g.K + c0;
+#pragma unroll
                     for (int m = 0; m < NP / 2; ++m) {
                         if (c0 + 32 * m >= np) continue;
                         *reinterpret_cast<v4f *>(d + 32 * m) = acc[2 * m][n];
@@ -428,6 +454,7 @@ group_tile_kernel(GroupMmArgs g) {
                     }
                 } else {
                     uint16_t *d = (uint16_t *)g.out + (int64_t)r * g.ld_out + c0;
+#pragma unroll
                     for (int m = 0; m < NP / 2; ++m)
                         if (c0 + 32 * m < np) store8(d + 32 * m, acc[2 * m][n], acc[2 * m + 1][n]);
                 }
@@ -436,42 +463,89 @@ group_tile_kernel(GroupMmArgs g) {
     };
 
     // ---- the pipeline
-    load_setup();
-    int issued = 0, done = 0;                // stages issued and multiplied so far
-    int cnk = lnk, ckt = 0, cord = 0;
-    int nks[S];                              // stages of the items between the two cursors
-    for (int s = 0; s < S; ++s) nks[s] = 0;
-    nks[0] = lnk;
-    auto issue_next = [&]() {
-        if (lit >= end) return;
-        const int o = lord;
-        issue(issued % S);
-        ++issued;
-        if (lord != o && lit < end)
-            for (int s = 0; s < S; ++s)
-                if (s == lord % S) nks[s] = lnk;
-    };
-    for (int s = 0; s < S - 1; ++s) issue_next();
-    clear();
-    while (true) {
-        // this wave's copies of the stage have landed, then everyone's; all
-        // reads of the slot that the next copies overwrite are complete
+    int issued = 0, done = 0, islot = 0, slot = 0;       // stages issued and multiplied, their slots
+    // This wave's copies of the stage have landed, then everyone's; all reads
+    // of the slot that the next copies overwrite are complete.
+    auto next_stage = [&]() {
         if (S > 2 && issued - done == S - 1) wait_vmcnt<(T::Ahead < 63 ? T::Ahead : 63)>();
         else wait_vmcnt<0>();
         __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0)
         stage_barrier();
-        issue_next();
-        compute(done % S);
+    };
+    // dw: what follows stage lkt of ld, to fetch its routes along
+    auto fetch_next = [&](int *ids) {
+        if (lkt + 1 < lnk) fetch_ids(ld, lkt + 1, ids);
+        else if (lit + step < end) fetch_ids(ld_next, 0, ids);
+    };
+    auto advance = [&]() {
+        stage_issued();
+        ++issued;
+        islot = islot + 1 == S ? 0 : islot + 1;
+    };
+    // The products of the stage at rd, and beside the first units' the copies
+    // of the stage S - 1 steps ahead into wr (all at once they would hold
+    // every wave up).  The pointers do not alias: rd, wr are different slots,
+    // idr, idw different halves of sids; without that the compiler would wait
+    // for all copies in flight before each transposing read.
+    auto multiply = [&](const uint8_t *__restrict__ rd, uint8_t *__restrict__ wr, const int *__restrict__ idr,
+                        int *__restrict__ idw, bool load) __attribute__((always_inline)) {
+        read_a(rd, 0);
+#pragma unroll
+        for (int u = 0; u < 3 && u < 2 * NQ; ++u) read_b(rd, u);
+        const bool tail = !DW && load && (lkt + 1) * 64 > nred;
+        if (tail) {
+#pragma unroll
+            for (int c = 0; c < kCopies; ++c) issue_copy(c, wr, idr, true);
+        }
+        const bool fast = load && !tail;
+        if (DW && load) fetch_next(idw);
+        constexpr int kPer = (2 * kCopies + 2 * NQ - 1) / (2 * NQ);
+#pragma unroll
+        for (int u = 0; u < 2 * NQ; ++u) {
+            if (u == 0) read_a(rd, 1);
+            if (u + 3 < 2 * NQ) read_b(rd, u + 3);
+            if (fast) {
+#pragma unroll
+                for (int c = u * kPer; c < (u + 1) * kPer && c < kCopies; ++c) issue_copy(c, wr, idr, false);
+            }
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+                acc[m][u % NQ] = mfma32<F16>(a[u / NQ][m], b[u & 3], acc[m][u % NQ]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    Item cur = ld;
+    int ckt = 0, cnk = stages_of(cur), cord = 0;
+    load_setup();
+    if (DW) {
+        fetch_ids(ld, 0, sids);
+        wait_vmcnt<0>();
+        __syncthreads();
+    }
+    for (int s = 0; s < S - 1 && lit < end; ++s) {
+        if (DW) fetch_next(sids + 64);
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) issue_copy(c, smem + islot * T::Stage, sids, true);
+        advance();
+    }
+    clear();
+    next_stage();
+    while (true) {
+        const bool load = lit < end;
+        multiply(smem + slot * T::Stage, smem + islot * T::Stage, sids + islot * 64, sids + (islot ^ 1) * 64, load);
+        if (load) advance();
         ++done;
+        slot = slot + 1 == S ? 0 : slot + 1;
+        if (issued > done) next_stage();
         if (++ckt == cnk) {
-            epilogue(cord);
+            epilogue(cur, cord);
             cit += step;
             if (cit >= end) break;
             clear();
-            ++cord;
+            cur = item_of(cit);
             ckt = 0;
-            for (int s = 0; s < S; ++s)
-                if (s == cord % S) cnk = nks[s];
+            cnk = stages_of(cur);
+            ++cord;
         }
     }
 }
@@ -620,13 +694,14 @@ hipError_t launch_tile(const GroupMmArgs &g, int64_t max_items, hipStream_t st) 
     using T = Tile<F16, OP, TP, TQ, WP, WQ, S>;
     static std::atomic<uint64_t> done{0};
     auto fn = group_tile_kernel<F16, OP, TP, TQ, WP, WQ, S>;
-    hipError_t e = raise_lds_limit(done, (const void *)fn, (int)T::Smem);
+    const size_t smem = T::Smem + (OP == kGmmDw ? (size_t)g.E * 8 : 0);
+    hipError_t e = raise_lds_limit(done, (const void *)fn, (int)(T::Smem + (OP == kGmmDw ? 1024 * 8 : 0)));
     if (e != hipSuccess) return e;
-    const int64_t per_cu = (160 * 1024) / (int64_t)T::Smem;
+    const int64_t per_cu = (160 * 1024) / (int64_t)smem;
     int64_t grid = (int64_t)device_cu_count() * (per_cu < 2 ? 1 : 2);
     if (grid > max_items) grid = max_items;
     grid = (grid + 7) / 8 * 8;
-    fn<<<(unsigned)grid, 64 * WP * WQ, T::Smem, st>>>(g);
+    fn<<<(unsigned)grid, 64 * WP * WQ, smem, st>>>(g);
     return hipGetLastError();
 }
 
