@@ -42,10 +42,14 @@ __device__ __forceinline__ v4f mfma32(const u32x4 &a, const u32x4 &b, const v4f 
                                                        __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
+// Two values at once (one packed conversion, round to nearest even).
 template <bool F16>
-__device__ __forceinline__ uint32_t to16(float v) {
-    if constexpr (F16) return __builtin_bit_cast(uint16_t, (_Float16)v);
-    else return f32_to_bf16_bits(v);
+__device__ __forceinline__ uint32_t to16x2(float lo, float hi) {
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    const v2f v = {lo, hi};
+    if constexpr (F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2h));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2bf));
 }
 
 template <bool F16>
@@ -300,12 +304,13 @@ group_tile_kernel(GroupMmArgs g) {
     // routes are at ids).  `tail`: the stage reaches past the end of the
     // contraction, where both operands are read as zeros.
     constexpr int kCopies = DW ? JP : JP + JQ;
+    int rid[JP];                             // dw: routes of the lane's rows in the stage being copied
     auto issue_copy = [&](int c, uint8_t *sp, const int *ids, bool tail) {
         uint8_t *sq = sp + T::PB;
         const void *zero = kZeros;
         if (DW) {
             const int kr = (c * NW + w) * RPI + ks_l;
-            const int r = ids[kr];
+            const int r = tail ? ids[kr] : rid[c];
             const bool ok = lkt * 64 + kr < ld.rows && r >= 0 && r < g.R;
             const int64_t xr = g.per_route ? r : g.token_of(r);
             lds_dma16(ok ? (const void *)(xcol + xr * g.ld_x * 2) : zero, sp + (c * NW + w) * 1024);
@@ -365,8 +370,12 @@ group_tile_kernel(GroupMmArgs g) {
 
     // A step is 2 NQ units, (contraction half kk, row tile n) in turn.  The
     // columns' operand (a) of a half and the rows' operand (b) of the units
-    // ahead are read from LDS while earlier units are multiplied.
-    u32x4 a[2][NP], b[4];
+    // ahead are read from LDS while earlier units are multiplied; the first
+    // reads of a stage go out before the last kLast units of the stage before,
+    // whose operands are in registers by then, so that neither the barrier
+    // between the stages nor the reads' latency leaves the MFMAs idle.
+    constexpr int kUnits = 2 * NQ, kAhead = NQ < 3 ? NQ : 3, kLast = kAhead;   // (the last units: second half)
+    u32x4 a[2][NP], b[kUnits], head[kAhead];
     auto read_a = [&](const uint8_t *sp, int kk) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
@@ -378,23 +387,23 @@ group_tile_kernel(GroupMmArgs g) {
             }
         }
     };
-    auto read_b = [&](const uint8_t *sp, int u) {
+    auto read_b = [&](const uint8_t *sp, int u, u32x4 &bu) {
         const uint8_t *sq = sp + T::PB;
         const int kk = u / NQ, n = u % NQ;
         if constexpr (T::QKS) {
             const int ch = (wq * (TQ / WQ) / 8 + 4 * (n >> 1) + (i16 & 3)) ^ ks_x;
-            b[u & 3] = lds_read_tr(sq + (kk * 32 + ks_row) * (TQ * 2) + ch * 16 + (n & 1) * 8, 4 * TQ * 2);
+            bu = lds_read_tr(sq + (kk * 32 + ks_row) * (TQ * 2) + ch * 16 + (n & 1) * 8, 4 * TQ * 2);
         } else {
-            b[u & 3] = lds_read16(sq + (q_kc ^ (kk << 6)) + n * 16 * 128);
+            bu = lds_read16(sq + (q_kc ^ (kk << 6)) + n * 16 * 128);
         }
     };
 
     auto store8 = [&](uint16_t *d, const v4f &x, const v4f &y) {
         u32x4 o;
-        o.x = to16<F16>(x[0]) | (to16<F16>(x[1]) << 16);
-        o.y = to16<F16>(x[2]) | (to16<F16>(x[3]) << 16);
-        o.z = to16<F16>(y[0]) | (to16<F16>(y[1]) << 16);
-        o.w = to16<F16>(y[2]) | (to16<F16>(y[3]) << 16);
+        o.x = to16x2<F16>(x[0], x[1]);
+        o.y = to16x2<F16>(x[2], x[3]);
+        o.z = to16x2<F16>(y[0], y[1]);
+        o.w = to16x2<F16>(y[2], y[3]);
         *reinterpret_cast<u32x4 *>(d) = o;
     };
 
@@ -482,36 +491,60 @@ group_tile_kernel(GroupMmArgs g) {
         ++issued;
         islot = islot + 1 == S ? 0 : islot + 1;
     };
-    // The products of the stage at rd, and beside the first units' the copies
-    // of the stage S - 1 steps ahead into wr (all at once they would hold
-    // every wave up).  The pointers do not alias: rd, wr are different slots,
-    // idr, idw different halves of sids; without that the compiler would wait
-    // for all copies in flight before each transposing read.
+    // The products of the stage at rd but for the last units, and beside the
+    // first units' the copies of the stage S - 1 steps ahead into wr (all at
+    // once they would hold every wave up).  The pointers do not alias: rd, wr
+    // are different slots, idr, idw different halves of sids; without that the
+    // compiler would wait for all copies in flight before each transposing read.
+    auto products = [&](int u) {
+#pragma unroll
+        for (int m = 0; m < NP; ++m) acc[m][u % NQ] = mfma32<F16>(a[u / NQ][m], b[u], acc[m][u % NQ]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
     auto multiply = [&](const uint8_t *__restrict__ rd, uint8_t *__restrict__ wr, const int *__restrict__ idr,
                         int *__restrict__ idw, bool load) __attribute__((always_inline)) {
-        read_a(rd, 0);
-#pragma unroll
-        for (int u = 0; u < 3 && u < 2 * NQ; ++u) read_b(rd, u);
         const bool tail = !DW && load && (lkt + 1) * 64 > nred;
         if (tail) {
 #pragma unroll
             for (int c = 0; c < kCopies; ++c) issue_copy(c, wr, idr, true);
         }
         const bool fast = load && !tail;
-        if (DW && load) fetch_next(idw);
-        constexpr int kPer = (2 * kCopies + 2 * NQ - 1) / (2 * NQ);
+        if (DW && load) {
+            fetch_next(idw);
 #pragma unroll
-        for (int u = 0; u < 2 * NQ; ++u) {
+            for (int c = 0; c < JP; ++c) rid[c] = idr[(c * NW + w) * RPI + ks_l];
+        }
+        constexpr int kIssue = kUnits - kLast < kUnits / 2 ? kUnits - kLast : kUnits / 2;
+        constexpr int kPer = (kCopies + kIssue - 1) / kIssue;       // copies go out in kIssue units
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) b[u] = head[u];
+#pragma unroll
+        for (int u = 0; u < kUnits - kLast; ++u) {
             if (u == 0) read_a(rd, 1);
-            if (u + 3 < 2 * NQ) read_b(rd, u + 3);
+            read_b(rd, u + kAhead, b[u + kAhead]);
             if (fast) {
 #pragma unroll
                 for (int c = u * kPer; c < (u + 1) * kPer && c < kCopies; ++c) issue_copy(c, wr, idr, false);
             }
+            products(u);
+        }
+    };
+    // the first reads of the stage at rd
+    auto read_head = [&](const uint8_t *rd) {
+        read_a(rd, 0);
 #pragma unroll
-            for (int m = 0; m < NP; ++m)
-                acc[m][u % NQ] = mfma32<F16>(a[u / NQ][m], b[u & 3], acc[m][u % NQ]);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int u = 0; u < kAhead; ++u) read_b(rd, u, head[u]);
+    };
+    // For more than two stages, with the next stage's first reads in the same
+    // scope as the copies that they must not wait for.
+    auto multiply_head = [&](const uint8_t *__restrict__ rd, uint8_t *__restrict__ wr,
+                             const uint8_t *__restrict__ nx, bool load) __attribute__((always_inline)) {
+        multiply(rd, wr, sids, sids, load);
+        if (load) advance();
+        ++done;
+        if (issued > done) {
+            next_stage();
+            read_head(nx);
         }
     };
     Item cur = ld;
@@ -530,13 +563,26 @@ group_tile_kernel(GroupMmArgs g) {
     }
     clear();
     next_stage();
+    read_head(smem);
     while (true) {
         const bool load = lit < end;
-        multiply(smem + slot * T::Stage, smem + islot * T::Stage, sids + islot * 64, sids + (islot ^ 1) * 64, load);
-        if (load) advance();
-        ++done;
-        slot = slot + 1 == S ? 0 : slot + 1;
-        if (issued > done) next_stage();
+        const int nslot = slot + 1 == S ? 0 : slot + 1;
+        const uint8_t *rd = smem + slot * T::Stage, *nx = smem + nslot * T::Stage;
+        uint8_t *wr = smem + islot * T::Stage;
+        if constexpr (S > 2) {
+            multiply_head(rd, wr, nx, load);
+        } else {
+            multiply(rd, wr, sids + islot * 64, sids + (islot ^ 1) * 64, load);
+            if (load) advance();
+            ++done;
+            if (issued > done) {
+                next_stage();
+                read_head(nx);
+            }
+        }
+#pragma unroll
+        for (int u = kUnits - kLast; u < kUnits; ++u) products(u);
+        slot = nslot;
         if (++ckt == cnk) {
             epilogue(cur, cord);
             cit += step;
@@ -631,7 +677,7 @@ group_stream_kernel(GroupMmArgs g) {
                 z1 += red[k][q >> 4][q & 15][cc + 1];
             }
             *reinterpret_cast<uint32_t *>((uint16_t *)g.out + (int64_t)r * g.ld_out + c0 + cc) =
-                to16<F16>(z0) | (to16<F16>(z1) << 16);
+                to16x2<F16>(z0, z1);
         }
         __syncthreads();
     }
@@ -655,10 +701,10 @@ group_sum_kernel(GroupMmArgs g) {
         y += *reinterpret_cast<const v4f *>(g.part + r * g.K + c + 4);
     }
     u32x4 o;
-    o.x = to16<F16>(x[0]) | (to16<F16>(x[1]) << 16);
-    o.y = to16<F16>(x[2]) | (to16<F16>(x[3]) << 16);
-    o.z = to16<F16>(y[0]) | (to16<F16>(y[1]) << 16);
-    o.w = to16<F16>(y[2]) | (to16<F16>(y[3]) << 16);
+    o.x = to16x2<F16>(x[0], x[1]);
+    o.y = to16x2<F16>(x[2], x[3]);
+    o.z = to16x2<F16>(y[0], y[1]);
+    o.w = to16x2<F16>(y[2], y[3]);
     *reinterpret_cast<u32x4 *>((uint16_t *)g.out + t * g.ld_out + c) = o;
 }
 
@@ -683,7 +729,7 @@ group_join_kernel(GroupMmArgs g) {
             s[2] += from16<F16>(o.y);
             s[3] += from16<F16>(o.y >> 16);
         }
-        *d = uint2{to16<F16>(s[0]) | (to16<F16>(s[1]) << 16), to16<F16>(s[2]) | (to16<F16>(s[3]) << 16)};
+        *d = uint2{to16x2<F16>(s[0], s[1]), to16x2<F16>(s[2], s[3])};
     }
 }
 
@@ -721,7 +767,7 @@ template <bool F16>
 hipError_t launch(const GroupMmArgs &g, hipStream_t st) {
     if (g.stream) {
         const dim3 grid((g.N + 15) / 16, (unsigned)(g.sorted_cap / g.block_m));
-        group_stream_kernel<F16, 1, 8, 7><<<grid, 512, 0, st>>>(g);
+        group_stream_kernel<F16, 1, 8, 6><<<grid, 512, 0, st>>>(g);
         return hipGetLastError();
     }
     const bool summed = g.op == kGmmDx && !g.per_route;
