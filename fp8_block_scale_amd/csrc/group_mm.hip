@@ -286,8 +286,8 @@ group_tile_kernel(GroupMmArgs g) {
             int r = row < ld.rows ? g.sorted[ld.row0 + row] : -1;
             if (r >= g.R) r = -1;
             if (row < TQ && (l & 7) == 0) rids[(lord % S) * TQ + row] = r;
-            const int64_t xr = r < 0 ? 0 : (OP == kGmmFwd && !g.per_route ? g.token_of(r) : r);
-            qptr[j] = reinterpret_cast<const uint8_t *>(src + xr * ldq) + kc_q * 16;
+            const int64_t xr = OP == kGmmFwd && !g.per_route ? g.token_of(r) : r;
+            qptr[j] = r < 0 ? nullptr : reinterpret_cast<const uint8_t *>(src + xr * ldq) + kc_q * 16;
         }
     };
 
@@ -335,7 +335,8 @@ group_tile_kernel(GroupMmArgs g) {
         } else {
             const int j = c - JP;
             if ((j + 1) * NW > T::QB / 1024 && j * NW + w >= T::QB / 1024) return;
-            const void *p = qptr[j] + (int64_t)lkt * 128;
+            // rows without a route are zeros: multiplying them costs least power
+            const void *p = qptr[j] ? (const void *)(qptr[j] + (int64_t)lkt * 128) : zero;
             if (tail && kc_q * 8 >= nred - lkt * 64) p = zero;
             lds_dma16(p, sq + (j * NW + w) * 1024);
         }
