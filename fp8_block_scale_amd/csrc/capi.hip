@@ -1025,6 +1025,8 @@ moe_status check_rows(const char *name, const void *p, int64_t ld, int64_t cols)
     if (ld < cols)
         return fail(MOE_ERR_SHAPE, "leading dimension of %s (%lld) < %lld", name, (long long)ld,
                     (long long)cols);
+    if (ld > (int64_t)1 << 30)
+        return fail(MOE_ERR_UNSUPPORTED, "leading dimension of %s (%lld) exceeds 2^30", name, (long long)ld);
     if (!p) return fail(MOE_ERR_NULL, "%s is NULL", name);
     if (!aligned16(p) || ld % 8 != 0)
         return fail(MOE_ERR_ALIGN, "%s must be 16-byte aligned, its leading dimension a multiple of 8", name);

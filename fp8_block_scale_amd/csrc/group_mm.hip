@@ -304,17 +304,21 @@ group_tile_kernel(GroupMmArgs g) {
     // routes are at ids).  `tail`: the stage reaches past the end of the
     // contraction, where both operands are read as zeros.
     constexpr int kCopies = DW ? JP : JP + JQ;
+    const bool by_route = g.per_route || g.top_k == 1;
+    const uint32_t ldx2 = (uint32_t)g.ld_x * 2u, ldy2 = (uint32_t)g.ld_dy * 2u;
     int rid[JP];                             // dw: routes of the lane's rows in the stage being copied
     auto issue_copy = [&](int c, uint8_t *sp, const int *ids, bool tail) {
         uint8_t *sq = sp + T::PB;
         const void *zero = kZeros;
         if (DW) {
+            // (32-bit factors: each row address is one multiply-add)
             const int kr = (c * NW + w) * RPI + ks_l;
-            const int r = tail ? ids[kr] : rid[c];
-            const bool ok = lkt * 64 + kr < ld.rows && r >= 0 && r < g.R;
-            const int64_t xr = g.per_route ? r : g.token_of(r);
-            lds_dma16(ok ? (const void *)(xcol + xr * g.ld_x * 2) : zero, sp + (c * NW + w) * 1024);
-            lds_dma16(ok ? (const void *)(dycol + (int64_t)r * g.ld_dy * 2) : zero, sq + (c * NW + w) * 1024);
+            const uint32_t r = (uint32_t)(tail ? ids[kr] : rid[c]);
+            const bool ok = r < (uint32_t)g.R && kr < ld.rows - lkt * 64;
+            const uint32_t xr = by_route ? r : __umulhi(r, g.div_m) >> (g.div_s - 1);
+            const void *px = xcol + (uint64_t)xr * ldx2, *py = dycol + (uint64_t)r * ldy2;
+            lds_dma16(ok ? px : zero, sp + (c * NW + w) * 1024);
+            lds_dma16(ok ? py : zero, sq + (c * NW + w) * 1024);
         } else if (c < JP) {
             const int left = nred - lkt * 64;              // of the contraction
             const uint8_t *base = pbase + c * pstep;
@@ -818,11 +822,11 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
     g.dw_tile = 256;
     if (g.op == kGmmDw) {
         int64_t tiles = (int64_t)g.E * ((g.N + 255) / 256) * ((g.K + 255) / 256);
-        if (tiles < 256) {
+        if (tiles <= 128) {
             g.dw_tile = 128;
             tiles = (int64_t)g.E * ((g.N + 127) / 128) * ((g.K + 127) / 128);
         }
-        int64_t sp = 256 / tiles;                      // tiles < 256: cut the rows
+        int64_t sp = 256 / tiles;                      // fewer tiles than CUs: cut the rows
         if (sp > rpe / 128) sp = rpe / 128;
         if (sp > 64) sp = 64;
         if (sp > 1) g.nsplit = (int)sp;

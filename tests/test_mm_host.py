@@ -61,6 +61,8 @@ def test_group_refusals(f):
     assert f(dt=2) == "MOE_ERR_SHAPE"
     assert f(ldx=56) == "MOE_ERR_SHAPE"
     assert f(ldy=24) == "MOE_ERR_SHAPE"
+    assert f(ldx=(1 << 30) + 8) == "MOE_ERR_UNSUPPORTED"
+    assert f(ldy=(1 << 30) + 8) == "MOE_ERR_UNSUPPORTED"
     assert f(ldx=68) == "MOE_ERR_ALIGN"
     assert f(ldy=36) == "MOE_ERR_ALIGN"
     for n in ("x", "w", "y"):
