@@ -22,6 +22,9 @@
 // stages are multiplied and its tile is stored (weight gradients have only a
 // few stages per tile).  Neighbouring items, which share rows or weights, run
 // on one XCD at the same time (panel_tile).
+#include <algorithm>
+#include <cmath>
+
 #include "common.h"
 #include "group_mm.h"
 
@@ -610,13 +613,17 @@ group_tile_kernel(GroupMmArgs g) {
 // wait for) U steps of 64 at a time, and add up in LDS.  Plan blocks with more than 16 NQ
 // routes go through the weights again for each further 16 NQ.
 template <bool F16, int NQ, int NW, int U>
-__global__ void __launch_bounds__(64 * NW)
+__global__ void __launch_bounds__(64 * NW, 3)
 group_stream_kernel(GroupMmArgs g) {
     __shared__ float red[NW][NQ][16][17];
     const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6), i16 = l & 15, grp = l >> 4;
-    int P = *g.ntp;
-    P = P < g.sorted_cap ? P : (int)g.sorted_cap;
+    // the plan's length and the block's routes are read together (the block
+    // lies within sorted_cap), its expert once the block is known to exist
     const int b = blockIdx.y, bm = g.block_m;
+    int P = *g.ntp, ids[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) ids[n] = g.sorted[b * bm + min(16 * n + i16, bm - 1)];
+    P = P < g.sorted_cap ? P : (int)g.sorted_cap;
     if ((b + 1) * bm > P) return;
     const int e = uni(g.eids[b]);
     if (e < 0 || e >= g.E) return;
@@ -626,13 +633,16 @@ group_stream_kernel(GroupMmArgs g) {
     const int nk = (g.K + 63) / 64;
 
     for (int row0 = b * bm; row0 < (b + 1) * bm; row0 += 16 * NQ) {
-        const int r0 = uni(g.sorted[row0]);
+        if (row0 > b * bm) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) ids[n] = g.sorted[row0 + min(16 * n + i16, bm - 1)];
+        }
+        const int r0 = uni(ids[0]);                     // (lane 0: the first row)
         if (r0 < 0 || r0 >= g.R) break;                 // sentinels end the segment
         const uint16_t *bp[NQ];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            const int i = 16 * n + i16;
-            int r = i < bm ? g.sorted[row0 + i] : r0;
+            int r = ids[n];
             if (r < 0 || r >= g.R) r = r0;              // results of these lanes are not stored
             bp[n] = g.x + (int64_t)(g.per_route ? r : g.token_of(r)) * g.ld_x;
         }
@@ -649,7 +659,7 @@ group_stream_kernel(GroupMmArgs g) {
                     int k = (k0 + u * NW) * 64 + 32 * h + 8 * grp;
                     ok[u][h] = k < g.K;
                     k = ok[u][h] ? k : 0;
-                    a[u][h] = __builtin_nontemporal_load((const u32x4 *)(ap + k));
+                    a[u][h] = *(const u32x4 *)(ap + k);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) x[u][n][h] = *(const u32x4 *)(bp[n] + k);
                 }
@@ -772,7 +782,9 @@ template <bool F16>
 hipError_t launch(const GroupMmArgs &g, hipStream_t st) {
     if (g.stream) {
         const dim3 grid((g.N + 15) / 16, (unsigned)(g.sorted_cap / g.block_m));
-        group_stream_kernel<F16, 1, 8, 6><<<grid, 512, 0, st>>>(g);
+        if (g.stream == 2) group_stream_kernel<F16, 2, 4, 4><<<grid, 256, 0, st>>>(g);
+        else if (g.K >= 4096) group_stream_kernel<F16, 1, 4, 7><<<grid, 256, 0, st>>>(g);
+        else group_stream_kernel<F16, 1, 4, 4><<<grid, 256, 0, st>>>(g);
         return hipGetLastError();
     }
     const bool summed = g.op == kGmmDx && !g.per_route;
@@ -814,7 +826,25 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
     g.div_s = s;
 
     const int64_t rpe = g.R / g.E;
-    g.stream = g.op == kGmmFwd && rpe <= 2 && g.sorted_cap / g.block_m <= 65535;
+    // The few-rows kernel by estimated time (us).  It takes one workgroup per
+    // plan block and 16 columns, about 768 at a time, each some 2 us and 1 us
+    // per 256 of K, again for every 16 (or, from 16 rows per expert, 32) rows
+    // of a block; the tile kernel some 10 us (two launches, fill and store)
+    // and per round of 256-column tiles over the CUs 0.55 us per 64 of K, or
+    // the weights' way from HBM.  Measured (us, few-rows against tile): K =
+    // 7168, N = 512, 9 / 36 / 112 experts hit 19 / 37 / 149 against 69 / 73 /
+    // 147; K = 1024, N = 512, 4 experts of 8 rows 5 against 17; K = 2048, N =
+    // 1024, 32 experts of 8 rows 34 against 28.
+    const double R = (double)g.R, E = (double)g.E;
+    const double hit = E * -std::expm1(R * std::log1p(-1.0 / E - 1e-12));
+    const double rows = R / hit, nq = rows <= 16 ? 1 : 2;
+    const double blocks = std::min(hit + R / g.block_m, (double)(g.sorted_cap / g.block_m));
+    const double passes = std::max(1.0, std::min(rows, (double)g.block_m) / (16 * nq));
+    const double t_few = std::ceil(blocks * ((g.N + 15) / 16) / 768) * passes * (2.0 + g.K / 256.0);
+    const double t_tile = 10.0 + std::max(0.55 * ((g.K + 63) / 64) * std::ceil(hit * ((g.N + 255) / 256) / 256),
+                                          hit * g.N * g.K * 2 / 5.5e6);
+    g.stream = 0;
+    if (g.op == kGmmFwd && t_few < t_tile && g.sorted_cap / g.block_m <= 65535) g.stream = (int)nq;
     if (g.stream) return 0;
     g.tile_rows = rpe > 128 ? 256 : rpe > 48 ? 128 : rpe > 24 ? 64 : 32;
     g.max_tiles = (int)(g.R / g.tile_rows + (g.E < g.R ? g.E : g.R));
