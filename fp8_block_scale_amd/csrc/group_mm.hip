@@ -769,7 +769,8 @@ hipError_t launch_tile(const GroupMmArgs &g, int64_t max_items, hipStream_t st) 
 template <bool F16, int OP>
 hipError_t launch_rows(const GroupMmArgs &g, hipStream_t st) {
     const int np = OP == kGmmFwd ? g.N : g.K;
-    const int64_t items = (int64_t)g.max_tiles * ((np + 255) / 256);
+    const int64_t items = (int64_t)g.max_tiles * ((np + g.tile_cols - 1) / g.tile_cols);
+    if (g.tile_cols == 128) return launch_tile<F16, OP, 128, 64, 2, 2, 6>(g, items, st);
     switch (g.tile_rows) {
         case 256: return launch_tile<F16, OP, 256, 256, 4, 2, 2>(g, items, st);
         case 128: return launch_tile<F16, OP, 256, 128, 4, 2, 3>(g, items, st);
@@ -826,27 +827,61 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
     g.div_s = s;
 
     const int64_t rpe = g.R / g.E;
-    // The few-rows kernel by estimated time (us).  It takes one workgroup per
-    // plan block and 16 columns, about 768 at a time, each some 2 us and 1 us
-    // per 256 of K, again for every 16 (or, from 16 rows per expert, 32) rows
-    // of a block; the tile kernel some 10 us (two launches, fill and store)
-    // and per round of 256-column tiles over the CUs 0.55 us per 64 of K, or
-    // the weights' way from HBM.  Measured (us, few-rows against tile): K =
-    // 7168, N = 512, 9 / 36 / 112 experts hit 19 / 37 / 149 against 69 / 73 /
-    // 147; K = 1024, N = 512, 4 experts of 8 rows 5 against 17; K = 2048, N =
-    // 1024, 32 experts of 8 rows 34 against 28.
     const double R = (double)g.R, E = (double)g.E;
-    const double hit = E * -std::expm1(R * std::log1p(-1.0 / E - 1e-12));
-    const double rows = R / hit, nq = rows <= 16 ? 1 : 2;
+    const double hit = E * -std::expm1(R * std::log1p(-1.0 / E));    // experts with a route
+    const double rows = R / hit;
+    const double wbytes = hit * g.N * g.K * 2;
+
+    // Forward, dx: the tile by estimated time (us), with routes spread evenly
+    // over the experts (rows of one: about normal, variance `rows`).  Per step
+    // of 64 of the contraction, measured with every CU busy, 256 columns x
+    // 256 / 128 / 64 / 32 rows take 2.1 / 0.95 / 0.65 / 0.55 and 128 x 64 takes
+    // 0.72; a tile's fill and store about 4.  Each row tile reads its expert's
+    // weights, at most 5.5 TB/s of them.  Measured at E = 288, K = 4096, N =
+    // 2048 with 14, 28, 56, 113, 227 rows an expert: 256 rows 1271, 1267,
+    // 1214, 1273, 1545; 128: 938, 938, 878, 1057, 1686; 64: 864, 875, 958,
+    // 1313, 2024; 32: 850, 913, 1196, 1692, 3015.
+    const int np = g.op == kGmmFwd ? g.N : g.K, nred = g.op == kGmmFwd ? g.K : g.N;
+    const int steps = (nred + 63) / 64;
+    struct Form {
+        int cols, rows;
+        double step;
+    };
+    static const Form forms[5] = {{256, 256, 2.1}, {256, 128, 0.95}, {256, 64, 0.65}, {256, 32, 0.55}, {128, 64, 0.72}};
+    double t_tile = 1e300;
+    g.tile_cols = 256;
+    g.tile_rows = 32;
+    for (const Form &f : forms) {
+        double per = 0;                                   // row tiles of an expert
+        if (rows > 32.0 * f.rows) per = rows / f.rows + 0.5;
+        else
+            for (int i = 0; i * f.rows < rows + 5 * std::sqrt(rows) + 1; ++i)
+                per += 0.5 * std::erfc((i * f.rows + 0.5 - rows) / std::sqrt(2 * rows));
+        if (per < 1) per = 1;
+        const double rounds = hit * per * ((np + f.cols - 1) / f.cols) / 256;
+        const double busy = (rounds < 4 ? std::ceil(rounds) : rounds + 0.5) * (steps * f.step + 4);
+        const double mem = per * wbytes / 5.5e6;
+        const double t = std::max(busy, mem) + 0.1 * std::min(busy, mem);
+        if (t < t_tile) {
+            t_tile = t;
+            g.tile_cols = f.cols;
+            g.tile_rows = f.rows;
+        }
+    }
+    // The few-rows kernel takes one workgroup per plan block and 16 columns,
+    // about 768 at a time, each some 2 us and 1 us per 256 of K, again for
+    // every 16 (or, from 16 rows per expert, 32) rows of a block; the tile
+    // kernels need a set-up launch, some 8 us.  Measured (us, few-rows against
+    // tile): K = 7168, N = 512, 9 / 36 / 112 experts hit 19 / 37 / 149 against
+    // 69 / 73 / 147; K = 1024, N = 512, 4 experts of 8 rows 5 against 17; K =
+    // 2048, N = 1024, 32 experts of 8 rows 34 against 28.
+    const double nq = rows <= 16 ? 1 : 2;
     const double blocks = std::min(hit + R / g.block_m, (double)(g.sorted_cap / g.block_m));
     const double passes = std::max(1.0, std::min(rows, (double)g.block_m) / (16 * nq));
     const double t_few = std::ceil(blocks * ((g.N + 15) / 16) / 768) * passes * (2.0 + g.K / 256.0);
-    const double t_tile = 10.0 + std::max(0.55 * ((g.K + 63) / 64) * std::ceil(hit * ((g.N + 255) / 256) / 256),
-                                          hit * g.N * g.K * 2 / 5.5e6);
     g.stream = 0;
-    if (g.op == kGmmFwd && t_few < t_tile && g.sorted_cap / g.block_m <= 65535) g.stream = (int)nq;
+    if (g.op == kGmmFwd && t_few < t_tile + 8 && g.sorted_cap / g.block_m <= 65535) g.stream = (int)nq;
     if (g.stream) return 0;
-    g.tile_rows = rpe > 128 ? 256 : rpe > 48 ? 128 : rpe > 24 ? 64 : 32;
     g.max_tiles = (int)(g.R / g.tile_rows + (g.E < g.R ? g.E : g.R));
     g.nsplit = 1;
     g.dw_tile = 256;
