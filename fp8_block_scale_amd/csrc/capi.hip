@@ -996,6 +996,11 @@ moe_status check_group_shape(int64_t M, int64_t K, int64_t N, int32_t E, int32_t
         return fail(MOE_ERR_SHAPE, "sorted_cap must be a non-negative multiple of block_m");
     if (M >= ((int64_t)1 << 31) / top_k || sorted_cap >= (int64_t)1 << 31)
         return fail(MOE_ERR_SHAPE, "M * top_k and sorted_cap must fit in int32");
+    // the kernels number their output tiles (at least 32 routes x 128 columns,
+    // 128 x 128 of a weight) in int32
+    const int64_t n = (N + 127) / 128, k = (K + 127) / 128, rows = M * top_k / 32 + E;
+    if (rows * (n > k ? n : k) >= (int64_t)1 << 31 || E * n * k >= (int64_t)1 << 31)
+        return fail(MOE_ERR_UNSUPPORTED, "more than 2^31 output tiles");
     return MOE_OK;
 }
 
@@ -1040,6 +1045,8 @@ moe_status run_group(moe::GroupMmArgs &g, int32_t dtype, void *workspace, size_t
         return fail(MOE_ERR_NULL, "sorted_token_ids, expert_ids and num_tokens_post_padded are required");
     if (((uintptr_t)g.sorted & 3u) || ((uintptr_t)g.eids & 3u) || ((uintptr_t)g.ntp & 3u))
         return fail(MOE_ERR_ALIGN, "the plan must be 4-byte aligned");
+    if (g.out == g.x || g.out == g.dy || g.out == g.w)
+        return fail(MOE_ERR_SHAPE, "the output is one of the inputs");
     const size_t need = moe::group_mm_workspace(g, nullptr);
     if (need > 0) {
         if (!workspace) return fail(MOE_ERR_NULL, "workspace is required");
@@ -1170,6 +1177,9 @@ moe_status check_linear_shape(int64_t M, int64_t N, int64_t K, int32_t act) {
         return fail(MOE_ERR_SHAPE, "MOE_ACT_SWIGLU needs an even N (%lld)", (long long)N);
     if (K > kMaxDim || N > kMaxDim)
         return fail(MOE_ERR_UNSUPPORTED, "K (%lld) or N (%lld) exceeds 2^20", (long long)K, (long long)N);
+    // the kernel numbers its output tiles (at least 64 rows x 64 columns) in int32
+    if (((M + 63) / 64) * ((N + 63) / 64) >= (int64_t)1 << 31)
+        return fail(MOE_ERR_UNSUPPORTED, "more than 2^31 output tiles");
     return MOE_OK;
 }
 
@@ -1213,6 +1223,8 @@ MOE_API moe_status moe_fp8_linear(const uint8_t *x_q, const float *x_s, const ui
         return fail(MOE_ERR_ALIGN, "x_s, w_s and bias must be 4-byte aligned");
     if (((uintptr_t)residual & 1u) || ((uintptr_t)out_bf16 & 1u))
         return fail(MOE_ERR_ALIGN, "residual and out must be 2-byte aligned");
+    if (out_bf16 == x_q || out_bf16 == w)
+        return fail(MOE_ERR_SHAPE, "out is one of the operands");
     const size_t need = moe::linear_workspace(a, nullptr);
     if (need > 0) {
         if (!workspace) return fail(MOE_ERR_NULL, "workspace is required");

@@ -10,6 +10,7 @@ import torch
 import fp8_block_scale_amd as moe
 
 FAKE = ctypes.c_void_p(0x10000)      # never dereferenced: validation fails first
+FAKE2, FAKE3 = ctypes.c_void_p(0x20000), ctypes.c_void_p(0x30000)
 BIG = 1 << 40
 
 
@@ -17,7 +18,7 @@ def _err(st):
     return moe.STATUS_NAMES[st]
 
 
-GMM = dict(M=4, K=64, N=32, E=8, k=2, bm=16, sc=128, dt=0, x=FAKE, w=FAKE, y=FAKE, ldx=64, ldy=32, pr=0,
+GMM = dict(M=4, K=64, N=32, E=8, k=2, bm=16, sc=128, dt=0, x=FAKE, w=FAKE2, y=FAKE3, ldx=64, ldy=32, pr=0,
            s=FAKE, e=FAKE, n=FAKE, ws=FAKE, wsb=BIG, dwt=0, acc=0)
 
 
@@ -68,9 +69,18 @@ def test_group_refusals(f):
     for n in ("x", "w", "y"):
         assert f(**{n: None}) == "MOE_ERR_NULL"
         assert f(**{n: ctypes.c_void_p(0x10008)}) == "MOE_ERR_ALIGN"
+    # more output tiles than int32 counts
+    assert f(M=1 << 30, k=1, K=1 << 20, N=1 << 20, ldx=1 << 20, ldy=1 << 20) == "MOE_ERR_UNSUPPORTED"
+    assert f(E=1024, K=1 << 20, N=1 << 20, ldx=1 << 20, ldy=1 << 20) == "MOE_ERR_UNSUPPORTED"
     for n in ("s", "e", "n"):
         assert f(**{n: None}) == "MOE_ERR_NULL"
         assert f(**{n: ctypes.c_void_p(0x10002)}) == "MOE_ERR_ALIGN"
+
+
+def test_group_output_is_no_input():
+    assert _fwd(y=FAKE) == _fwd(y=FAKE2) == "MOE_ERR_SHAPE"
+    assert _dx(x=FAKE3) == _dx(x=FAKE2) == "MOE_ERR_SHAPE"
+    assert _dw(w=FAKE3) == _dw(w=FAKE) == "MOE_ERR_SHAPE"
 
 
 def test_group_types_and_workspace():
@@ -95,7 +105,7 @@ def test_group_types_and_workspace():
     assert _dx(sc=0, x=None) == "MOE_ERR_NULL"
 
 
-LIN = dict(M=4, N=96, K=256, act=0, xq=FAKE, xs=FAKE, w=FAKE, ws=FAKE, b=FAKE, r=None, ldr=0, out=FAKE,
+LIN = dict(M=4, N=96, K=256, act=0, xq=FAKE, xs=FAKE, w=FAKE, ws=FAKE, b=FAKE, r=None, ldr=0, out=FAKE3,
            ldo=96, wk=FAKE, wkb=BIG)
 
 
@@ -118,7 +128,9 @@ def test_linear_refusals():
     assert _lin(N=(1 << 20) + 1) == "MOE_ERR_UNSUPPORTED"
     assert _lin(ldo=95) == "MOE_ERR_SHAPE"
     assert _lin(r=ctypes.c_void_p(0x20000), ldr=95) == "MOE_ERR_SHAPE"
-    assert _lin(r=FAKE, ldr=104) == "MOE_ERR_SHAPE"     # residual is out, other leading dimension
+    assert _lin(r=FAKE3, ldr=104) == "MOE_ERR_SHAPE"     # residual is out, other leading dimension
+    assert _lin(out=FAKE) == "MOE_ERR_SHAPE"            # out is x_q or w
+    assert _lin(M=1 << 30, N=1 << 20, ldo=1 << 20) == "MOE_ERR_UNSUPPORTED"
     for n in ("xq", "xs", "w", "ws", "out"):
         assert _lin(**{n: None}) == "MOE_ERR_NULL"
     for n, p in (("xq", 0x10008), ("w", 0x10008), ("xs", 0x10002), ("ws", 0x10002), ("b", 0x10002),
