@@ -226,20 +226,6 @@ __device__ __forceinline__ int xcd_remap(int x, int n) {
     return xcd * q + (xcd < r ? xcd : r) + k;
 }
 
-// Order of the output tiles of a product: panels of PANEL row tiles, column
-// tiles outer and the panel's row tiles inner, so that the tiles that run at
-// the same time on an XCD (neighbours in this order) share both operands in
-// its L2.  Item i of rows x cols -> its row and column tile.
-template <int PANEL>
-__device__ __forceinline__ void panel_tile(int i, int rows, int cols, int &row, int &col) {
-    const int panel = i / (PANEL * cols);
-    const int first = panel * PANEL;
-    const int height = rows - first < PANEL ? rows - first : PANEL;
-    const int rem = i - first * cols;
-    col = rem / height;
-    row = first + rem - col * height;
-}
-
 // Work queues of the persistent kernels, one per XCD.  The n units (row
 // tiles) are cut into 8 contiguous ranges; XCD x hands out the items of range
 // x (units * per_unit items, unit-major, so all items of one row tile run on

@@ -25,8 +25,7 @@ struct GroupMmArgs {
     void *out;               // y [R, ld_out], dx [M or R, ld_out] or dw [E, N, K]
     // the schedule and the workspace (group_mm_workspace)
     int stream;              // the few-rows kernel (forward): 16-row tiles per pass, 0: the tile kernel
-    int tile_rows;           // rows and columns of a tile (forward, dx)
-    int tile_cols;
+    int tile_rows;           // rows of a tile (forward, dx)
     int max_tiles;           // most row tiles that any routing gives
     int dw_tile;             // output tile of dw: 128 or 256 squared
     int nsplit;              // dw: parts that an expert's rows are cut into

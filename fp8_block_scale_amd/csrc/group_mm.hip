@@ -25,8 +25,8 @@
 #include <algorithm>
 #include <cmath>
 
-#include "common.h"
 #include "group_mm.h"
+#include "tiles.h"
 
 namespace moe {
 
@@ -64,8 +64,6 @@ __device__ __forceinline__ float from16(uint32_t v) {
 // What the copies of contraction values past the end read: zeros on both
 // operands (0 * garbage could be NaN).
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
-
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // ------------------------------------------------------------ set-up launch
 
@@ -700,27 +698,30 @@ group_stream_kernel(GroupMmArgs g) {
 
 // ------------------------------------------------------------ joining sums
 
-// dx[t] = the sum of the token's routes' FP32 rows, in route order.
+// dx[t] = the sum of the token's routes' FP32 rows, in route order.  A
+// workgroup takes 256 / lanes tokens and lanes x 8 columns of them.
 template <bool F16>
 __global__ void __launch_bounds__(256)
-group_sum_kernel(GroupMmArgs g) {
-    const int per = (g.K / 8 + 255) / 256;
-    const int64_t t = blockIdx.x / per;
-    const int c = ((int)(blockIdx.x % per) * 256 + threadIdx.x) * 8;
-    if (c >= g.K) return;
-    v4f x = {0.f, 0.f, 0.f, 0.f}, y = x;
-    for (int j = 0; j < g.top_k; ++j) {
-        const int64_t r = t * g.top_k + j;
-        if (g.rpos[r] < 0) continue;
-        x += *reinterpret_cast<const v4f *>(g.part + r * g.K + c);
-        y += *reinterpret_cast<const v4f *>(g.part + r * g.K + c + 4);
+group_sum_kernel(GroupMmArgs g, int lanes, int64_t blocks) {
+    const int per = (g.K / 8 + lanes - 1) / lanes, row = threadIdx.x / lanes, col = threadIdx.x % lanes;
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+        const int64_t t = b / per * (256 / lanes) + row;
+        const int c = ((int)(b % per) * lanes + col) * 8;
+        if (t >= g.M || c >= g.K) continue;
+        v4f x = {0.f, 0.f, 0.f, 0.f}, y = x;
+        for (int j = 0; j < g.top_k; ++j) {
+            const int64_t r = t * g.top_k + j;
+            if (g.rpos[r] < 0) continue;
+            x += *reinterpret_cast<const v4f *>(g.part + r * g.K + c);
+            y += *reinterpret_cast<const v4f *>(g.part + r * g.K + c + 4);
+        }
+        u32x4 o;
+        o.x = to16x2<F16>(x[0], x[1]);
+        o.y = to16x2<F16>(x[2], x[3]);
+        o.z = to16x2<F16>(y[0], y[1]);
+        o.w = to16x2<F16>(y[2], y[3]);
+        *reinterpret_cast<u32x4 *>((uint16_t *)g.out + t * g.ld_out + c) = o;
     }
-    u32x4 o;
-    o.x = to16x2<F16>(x[0], x[1]);
-    o.y = to16x2<F16>(x[2], x[3]);
-    o.z = to16x2<F16>(y[0], y[1]);
-    o.w = to16x2<F16>(y[2], y[3]);
-    *reinterpret_cast<u32x4 *>((uint16_t *)g.out + t * g.ld_out + c) = o;
 }
 
 // dw = the sum of the splits' FP32 tiles, in split order.
@@ -769,8 +770,7 @@ hipError_t launch_tile(const GroupMmArgs &g, int64_t max_items, hipStream_t st) 
 template <bool F16, int OP>
 hipError_t launch_rows(const GroupMmArgs &g, hipStream_t st) {
     const int np = OP == kGmmFwd ? g.N : g.K;
-    const int64_t items = (int64_t)g.max_tiles * ((np + g.tile_cols - 1) / g.tile_cols);
-    if (g.tile_cols == 128) return launch_tile<F16, OP, 128, 64, 2, 2, 6>(g, items, st);
+    const int64_t items = (int64_t)g.max_tiles * ((np + 255) / 256);
     switch (g.tile_rows) {
         case 256: return launch_tile<F16, OP, 256, 256, 4, 2, 2>(g, items, st);
         case 128: return launch_tile<F16, OP, 256, 128, 4, 2, 3>(g, items, st);
@@ -805,8 +805,11 @@ hipError_t launch(const GroupMmArgs &g, hipStream_t st) {
     }
     e = g.op == kGmmFwd ? launch_rows<F16, kGmmFwd>(g, st) : launch_rows<F16, kGmmDx>(g, st);
     if (e != hipSuccess || !summed) return e;
-    const int64_t per = (g.K / 8 + 255) / 256;
-    group_sum_kernel<F16><<<(unsigned)(g.M * per), 256, 0, st>>>(g);
+    int lanes = 256;                                   // threads of a token: K / 8, up to a power of two
+    while (lanes > 1 && lanes / 2 >= g.K / 8) lanes /= 2;
+    const int64_t tokens = 256 / lanes;
+    const int64_t blocks = (g.M + tokens - 1) / tokens * ((g.K / 8 + lanes - 1) / lanes);
+    group_sum_kernel<F16><<<(unsigned)std::min(blocks, (int64_t)1 << 23), 256, 0, st>>>(g, lanes, blocks);
     return hipGetLastError();
 }
 
@@ -835,21 +838,20 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
     // Forward, dx: the tile by estimated time (us), with routes spread evenly
     // over the experts (rows of one: about normal, variance `rows`).  Per step
     // of 64 of the contraction, measured with every CU busy, 256 columns x
-    // 256 / 128 / 64 / 32 rows take 2.1 / 0.95 / 0.65 / 0.55 and 128 x 64 takes
-    // 0.72; a tile's fill and store about 4.  Each row tile reads its expert's
-    // weights, at most 5.5 TB/s of them.  Measured at E = 288, K = 4096, N =
-    // 2048 with 14, 28, 56, 113, 227 rows an expert: 256 rows 1271, 1267,
-    // 1214, 1273, 1545; 128: 938, 938, 878, 1057, 1686; 64: 864, 875, 958,
-    // 1313, 2024; 32: 850, 913, 1196, 1692, 3015.
+    // 256 / 128 / 64 / 32 rows take 2.1 / 0.95 / 0.65 / 0.55 (128 columns x 64
+    // rows 0.72: no gain from narrower tiles); a tile's fill and store about
+    // 4.  Each row tile reads its expert's weights, at most 5.5 TB/s of them.
+    // Measured at E = 288, K = 4096, N = 2048 with 14, 28, 56, 113, 227 rows
+    // an expert: 256 rows 1271, 1267, 1214, 1273, 1545; 128: 938, 938, 878,
+    // 1057, 1686; 64: 864, 875, 958, 1313, 2024; 32: 850, 913, 1196, 1692, 3015.
     const int np = g.op == kGmmFwd ? g.N : g.K, nred = g.op == kGmmFwd ? g.K : g.N;
     const int steps = (nred + 63) / 64;
     struct Form {
-        int cols, rows;
+        int rows;
         double step;
     };
-    static const Form forms[5] = {{256, 256, 2.1}, {256, 128, 0.95}, {256, 64, 0.65}, {256, 32, 0.55}, {128, 64, 0.72}};
+    static const Form forms[4] = {{256, 2.1}, {128, 0.95}, {64, 0.65}, {32, 0.55}};
     double t_tile = 1e300;
-    g.tile_cols = 256;
     g.tile_rows = 32;
     for (const Form &f : forms) {
         double per = 0;                                   // row tiles of an expert
@@ -858,13 +860,12 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
             for (int i = 0; i * f.rows < rows + 5 * std::sqrt(rows) + 1; ++i)
                 per += 0.5 * std::erfc((i * f.rows + 0.5 - rows) / std::sqrt(2 * rows));
         if (per < 1) per = 1;
-        const double rounds = hit * per * ((np + f.cols - 1) / f.cols) / 256;
+        const double rounds = hit * per * ((np + 255) / 256) / 256;
         const double busy = (rounds < 4 ? std::ceil(rounds) : rounds + 0.5) * (steps * f.step + 4);
         const double mem = per * wbytes / 5.5e6;
         const double t = std::max(busy, mem) + 0.1 * std::min(busy, mem);
         if (t < t_tile) {
             t_tile = t;
-            g.tile_cols = f.cols;
             g.tile_rows = f.rows;
         }
     }

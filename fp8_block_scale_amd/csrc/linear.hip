@@ -13,14 +13,12 @@
 // In both the weights are the A side of the FP8 MFMA and the rows of x the B
 // side, so a lane's results share one row of x (one scale) and run along the
 // output's columns.
-#include "common.h"
 #include "linear.h"
+#include "tiles.h"
 
 namespace moe {
 
 namespace {
-
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ v8i join8(const u32x4 &lo, const u32x4 &hi) {
     v8i r;
@@ -580,10 +578,13 @@ hipError_t launch_tile(const LinearArgs &g, hipStream_t st) {
     grid = (grid + 7) / 8 * 8;
     fn<<<(unsigned)grid, 64 * WP * WQ, T::Smem, st>>>(g);
     e = hipGetLastError();
-    if (e != hipSuccess || !SPLIT || g.nsplit == 1) return e;
-    const int64_t waves = items / g.nsplit * (WP * WQ) * (GLU ? 1 : T::NP / 2) * T::NQ;
-    linear_join_kernel<TP, TQ, WP, WQ, GLU><<<(unsigned)((waves + 3) / 4), 256, 0, st>>>(g);
-    return hipGetLastError();
+    if constexpr (SPLIT)
+        if (e == hipSuccess && g.nsplit > 1) {
+            const int64_t waves = items / g.nsplit * (WP * WQ) * (GLU ? 1 : T::NP / 2) * T::NQ;
+            linear_join_kernel<TP, TQ, WP, WQ, GLU><<<(unsigned)((waves + 3) / 4), 256, 0, st>>>(g);
+            e = hipGetLastError();
+        }
+    return e;
 }
 
 template <int GLU>

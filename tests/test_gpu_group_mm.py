@@ -188,6 +188,16 @@ def test_larger(M, E, K, N, k, bm, dt):
     check_all(Problem(dt, M, E, K, N, k, bm, routing="full"))
 
 
+@pytest.mark.parametrize("M,E,K,N,k,bm", [
+    (4500, 2, 1032, 1032, 2, 64), (9000, 2, 264, 264, 2, 128),      # 256-row tiles
+    (70001, 3, 8, 16, 1, 16),                                       # many tokens, short rows
+    (300, 1024, 136, 264, 8, 16), (2000, 1024, 64, 40, 4, 8),       # the most experts
+    (40, 6, 72, 136, 6, 128), (3, 6, 264, 8, 6, 64)])               # every expert for every token
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_ranges(M, E, K, N, k, bm, dt):
+    check_all(Problem(dt, M, E, K, N, k, bm))
+
+
 def test_no_tokens():
     p = Problem(BF, 4, 3, 64, 32, 2, 16)
     e = torch.empty((0, 64), dtype=BF, device=DEV)
@@ -271,6 +281,25 @@ def test_overflow_rounds_to_infinity():
     p.x.fill_(60.0)
     p.w.fill_(60.0)                               # 64 * 3600 > 65504
     assert torch.isposinf(p.y()).all()
+
+
+@pytest.mark.parametrize("M", [9, 700])
+def test_subnormals(M):
+    """FP16 subnormals (here the multiples of 2^-24 up to 2^-14) are values
+    like any other.  y and dx, with small whole numbers: sums of at most 2^20
+    units of 2^-24, exact.  dw: some 466 products of up to 10^6 units of 2^-48
+    pass the 2^24 units that FP32 sums hold exactly, so to its tolerance."""
+    p = Problem(HF, M, 3, 64, 72, 2, 16)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(8)
+    draw = lambda shape, n: torch.randint(-n, n + 1, shape, generator=g, device=DEV).double()
+    p.x, p.dy = (draw(t.shape, 1000).mul(2.0 ** -24).to(HF) for t in (p.x, p.dy))
+    p.w = draw(p.w.shape, 4).to(HF)
+    valid = p.valid()
+    v = p.ref_y()[0][valid]
+    assert torch.equal(p.y()[valid], v.to(HF)) and v.abs().max() > 0
+    assert torch.equal(p.dx(), p.ref_dx()[0].to(HF))
+    check(p.dw(F32), p.ref_dw(), F32)
 
 
 @pytest.mark.parametrize("M,E,K,N,k,bm", [(40, 6, 64, 48, 2, 16), (333, 3, 40, 24, 2, 32)])

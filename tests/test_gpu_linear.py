@@ -125,6 +125,12 @@ def test_formula(M, N, K, act):
     check(p(), p.ref())
 
 
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+@pytest.mark.parametrize("M,N,K", [(2500, 4096, 256), (2501, 4130, 256), (2500, 1026, 384),     # 256 and 128 row tiles
+                                   (1000, 1024, 2048), (70, 200, 4992)])                         # K splits
+def test_larger(M, N, K, act):
+    p = Problem(M, N, K, act)
+    check(p(), p.ref())
 
 
 def test_no_rows():
