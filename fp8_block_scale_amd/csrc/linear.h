@@ -22,6 +22,7 @@ struct LinearArgs {
     int act;
     // the schedule and the workspace (linear_workspace)
     int form;                // kernel form
+    int stream_nq;           // few rows: tiles of 16 rows per workgroup
     int nsplit;              // parts that K is cut into (tile forms)
     float *part;             // FP32 sums of every (tile, split)
 };

@@ -43,30 +43,58 @@ __device__ __forceinline__ float act1(float z, int act) {
 
 // 16 weight rows (with SwiGLU 8 gate and their 8 up rows) x 16 NQ rows of x
 // per workgroup.  Wave w takes the K-blocks w, w + NW, ...; U of them are
-// loaded before the first is multiplied.  NaN codes or scales of rows past
-// the end only reach results that are not stored (those lanes read the last
-// row instead).
-template <int NQ, int NW, int U, bool SW>
+// loaded before the first is multiplied, and the waves' sums are added in
+// order.  Rows past the end read the last row: their results are not stored.
+//
+// Bound by the reads of x and w from the L2 (each workgroup reads all of its
+// rows of both).  Weights go straight into registers.  Rows of x that differ
+// (XL) are copied to the wave's share of LDS, 8 whole rows of 128 bytes an
+// instruction, and read from there: register loads in the operand's layout
+// touch 16 rows, 64 bytes each, and ran at some 13 bytes a clock and CU.
+// Measured (us, registers -> LDS), K = 4096, N = 2048: 16 rows 6.5 -> 5.4, 32
+// rows 12.6 -> 6.7, 48 rows 12.1 -> 8.3, 64 rows 15.3 -> 9.8; one row, whose
+// 16 copies are one line, 4.3 -> 4.7, so up to 4 rows stay in registers.
+// One row at K = 7168, N = 4096 takes 8.5 us (29 MB, 3.5 TB/s with the launch).
+
+// Bytes of LDS of nw waves: their rows of x, then their sums.
+constexpr int stream_lds(int nq, int nw, int u, bool xl) {
+    const int sums = (nq * 16 * 17 * 4 + 15) / 16 * 16, x = xl ? u * nq * 2048 : 0;
+    return nw * (x > sums ? x : sums);
+}
+
+template <int NQ, int NW, int U, bool SW, bool XL>
 __global__ void __launch_bounds__(64 * NW)
 linear_stream_kernel(LinearArgs g) {
-    __shared__ float red[NW][NQ][16][17];
+    // a wave's share of LDS: its rows of x (XL), then its sums [NQ][16][17]
+    constexpr int kWave = stream_lds(NQ, 1, U, XL);
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6), i16 = l & 15, grp = l >> 4;
     const int nkb = g.K >> 7;
-    const int c0 = blockIdx.x * (SW ? 8 : 16);
+    const int c0 = blockIdx.x * (SW ? 8 : 16), m0 = blockIdx.y * (16 * NQ);
 
     auto wrow = [&](int i) {                     // weight row of MFMA row i
         const int c = c0 + (SW ? i & 7 : i);
         return (c < g.n_out ? c : g.n_out - 1) + (SW && i >= 8 ? g.n_out : 0);
     };
     const uint8_t *ap = g.w + (int64_t)wrow(i16) * g.K + grp * 16;
-    const uint8_t *bp[NQ];
+    uint8_t *const lds = smem + w * kWave;
+    const uint8_t *bp[XL ? 2 * NQ : NQ];
     const float *xp[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-        const int64_t m = 16 * n + i16 < g.M ? 16 * n + i16 : g.M - 1;
-        bp[n] = g.xq + m * g.K + grp * 16;
+        const int64_t m = min(m0 + 16 * n + i16, (int)g.M - 1);
+        if (!XL) bp[n] = g.xq + m * g.K + grp * 16;
         xp[n] = g.xs + m * nkb;
     }
+    if (XL) {
+        // copies of 8 rows x 128 bytes; chunk c of row r lies at c ^ (r & 7)
+#pragma unroll
+        for (int j = 0; j < 2 * NQ; ++j) {
+            const int64_t m = min(m0 + 8 * j + (l >> 3), (int)g.M - 1);
+            bp[j] = g.xq + m * g.K + ((l & 7) ^ (l >> 3)) * 16;
+        }
+    }
+    const int x_off = i16 * 128 + ((grp ^ (i16 & 7)) << 4);
     // a lane's four results are weight rows 4 grp + v; with SwiGLU and an odd
     // number of columns they can straddle a block of 128
     const float *wp[4];
@@ -80,48 +108,67 @@ linear_stream_kernel(LinearArgs g) {
         float sx[U][NQ], sw[U][SW ? 4 : 1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int kb = min(kb0 + u * NW, nkb - 1);
+            const int kb = kb0 + u * NW;
+            if (kb >= nkb) break;
             a[u][0] = __builtin_nontemporal_load((const u32x4 *)(ap + (int64_t)kb * 128));
             a[u][1] = __builtin_nontemporal_load((const u32x4 *)(ap + (int64_t)kb * 128 + 64));
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                b[u][n][0] = *(const u32x4 *)(bp[n] + (int64_t)kb * 128);
-                b[u][n][1] = *(const u32x4 *)(bp[n] + (int64_t)kb * 128 + 64);
+                if (XL) {
+                    lds_dma16(bp[2 * n] + (int64_t)kb * 128, lds + (u * NQ + n) * 2048);
+                    lds_dma16(bp[2 * n + 1] + (int64_t)kb * 128, lds + (u * NQ + n) * 2048 + 1024);
+                } else {
+                    b[u][n][0] = *(const u32x4 *)(bp[n] + (int64_t)kb * 128);
+                    b[u][n][1] = *(const u32x4 *)(bp[n] + (int64_t)kb * 128 + 64);
+                }
                 sx[u][n] = xp[n][kb];
             }
 #pragma unroll
             for (int v = 0; v < (SW ? 4 : 1); ++v) sw[u][v] = wp[v][kb];
         }
         __builtin_amdgcn_sched_barrier(0);       // every load above is issued first
+        if (XL) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the wave's own copies
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    if (kb0 + u * NW >= nkb) break;
+                    b[u][n][0] = lds_read16(lds + (u * NQ + n) * 2048 + x_off);
+                    b[u][n][1] = lds_read16(lds + (u * NQ + n) * 2048 + (x_off ^ 64));
+                }
+            // read before the next round's copies write there
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            // past the end the last K-block was read again: its scale is zero
-            // (a NaN in it is in the sum already)
-            const bool on = kb0 + u * NW < nkb;
+            if (kb0 + u * NW >= nkb) break;
             const v8i av = join8(a[u][0], a[u][1]);
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 const v4f t = mfma16x16x128(av, join8(b[u][n][0], b[u][n][1]));
 #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[n][v] += t[v] * (on ? sx[u][n] * sw[u][SW ? v : 0] : 0.f);
+                for (int v = 0; v < 4; ++v) acc[n][v] += t[v] * (sx[u][n] * sw[u][SW ? v : 0]);
             }
         }
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) red[w][n][i16][4 * grp + v] = acc[n][v];
+        for (int v = 0; v < 4; ++v)
+            reinterpret_cast<float *>(lds)[(n * 16 + i16) * 17 + 4 * grp + v] = acc[n][v];
     __syncthreads();
     constexpr int COLS = SW ? 8 : 16;
     for (int i = tid; i < 16 * NQ * COLS; i += 64 * NW) {
         const int c = i % COLS, r = i / COLS;
-        const int64_t m = r;
+        const int64_t m = m0 + r;
         const int col = c0 + c;
         if (m >= g.M || col >= g.n_out) continue;
         float z = 0.f, u = 0.f;
         for (int q = 0; q < NW; ++q) {
-            z += red[q][r >> 4][r & 15][c];
-            if (SW) u += red[q][r >> 4][r & 15][c + 8];
+            const float *d = reinterpret_cast<const float *>(smem + q * kWave) + r * 17 + c;
+            z += d[0];
+            if (SW) u += d[8];
         }
         if (g.bias) {
             z += g.bias[col];
@@ -587,19 +634,29 @@ hipError_t launch_tile(const LinearArgs &g, hipStream_t st) {
     return e;
 }
 
+template <int NQ, int NW, int U, bool SW, bool XL>
+hipError_t launch_stream(const LinearArgs &g, hipStream_t st) {
+    const dim3 grid((g.n_out + (SW ? 7 : 15)) / (SW ? 8 : 16), (unsigned)((g.M + 16 * NQ - 1) / (16 * NQ)));
+    constexpr int smem = stream_lds(NQ, NW, U, XL);
+    static_assert(smem <= 160 * 1024, "LDS");
+    static std::atomic<uint64_t> done{0};
+    auto fn = linear_stream_kernel<NQ, NW, U, SW, XL>;
+    hipError_t e = raise_lds_limit(done, (const void *)fn, smem);
+    if (e != hipSuccess) return e;
+    fn<<<grid, 64 * NW, smem, st>>>(g);
+    return hipGetLastError();
+}
+
 template <int GLU>
 hipError_t launch(const LinearArgs &g, hipStream_t st) {
     constexpr bool SW = GLU != 0;
     switch (g.form) {
         case kLinStream: {
-            const unsigned grid = (unsigned)((g.n_out + (SW ? 7 : 15)) / (SW ? 8 : 16));
-            if (g.M > 48) linear_stream_kernel<4, 16, 1, SW><<<grid, 1024, 0, st>>>(g);
-            else if (g.M > 32) linear_stream_kernel<3, 16, 2, SW><<<grid, 1024, 0, st>>>(g);
-            else if (g.M > 16) linear_stream_kernel<2, 8, 3, SW><<<grid, 512, 0, st>>>(g);
-            else if (g.K > 32 * 128 && (int)grid <= device_cu_count())
-                linear_stream_kernel<1, 8, 7, SW><<<grid, 512, 0, st>>>(g);
-            else linear_stream_kernel<1, 8, 4, SW><<<grid, 512, 0, st>>>(g);
-            return hipGetLastError();
+            if (g.stream_nq == 4) return launch_stream<4, 8, 1, SW, true>(g, st);
+            if (g.stream_nq == 3) return launch_stream<3, 8, 1, SW, true>(g, st);
+            if (g.stream_nq == 2) return launch_stream<2, 8, 1, SW, true>(g, st);
+            if (g.M > 4) return launch_stream<1, 8, 2, SW, true>(g, st);
+            return launch_stream<1, 8, 2, SW, false>(g, st);
         }
         case kLinTile256:
             if constexpr (GLU < 2) return launch_tile<256, 256, 4, 2, 2, GLU, false>(g, st);
@@ -617,16 +674,28 @@ size_t linear_workspace(LinearArgs &a, void *ws) {
     auto items = [&](int tp, int tq) { return ((a.M + tq - 1) / tq) * ((n + tp - 1) / tp); };
     a.nsplit = 1;
     a.part = nullptr;
-    if (a.M <= 64) {
-        a.form = kLinStream;
-        return 0;
-    }
     // Tile form by estimated time: rounds of tiles over the CUs, each nkb
     // steps and a fill and store of the tile.  Per step and per tile, measured
     // with every CU busy: 256 x 256 2.0 and 10 us, 256 x 128 1.1 and 6 us,
     // 128 x 64 0.67 and 3 us.  (The larger tile does the most per step, the
     // smaller ones lose less to a last, partly filled round.)
     const int64_t cus = 256;
+    // Few rows by estimated time: a workgroup of 16 NQ rows takes (0.075 +
+    // 0.055 NQ) us per K-block; small NQ fills the CUs, large NQ reads the
+    // weights less often.  Against the tiles, which also pay some 3 us more
+    // for their ring's first stages.  Measured (us, few rows / tiles): K = N =
+    // 1024, 64 / 256 / 1000 rows 3.2 / 9.8, 4.6 / 10.0, 10.8 / 10.2; K = 4096,
+    // N = 2048, 64 / 128 / 192 rows 6.8 / 11.6, 10.1 / 13.8, 17.3 / 14.7; K =
+    // 4096, N = 8192, 16 / 33 / 64 rows 10.3 / 14.0, 14.5 / 14.6, 19.8 / 14.8.
+    double t_few = 1e300;
+    for (int nq = 1; nq <= 4 && a.M <= 1024; ++nq) {
+        const int64_t wgs = ((n + 15) / 16) * ((a.M + 16 * nq - 1) / (16 * nq));
+        const double t = 2.5 + (wgs > cus ? wgs / 256.0 : 1.0) * nkb * (0.075 + 0.055 * nq);
+        if (t < t_few) {
+            t_few = t;
+            a.stream_nq = nq;
+        }
+    }
     auto est = [&](int64_t it, int steps, double step, double tile) {
         return (double)((it + cus - 1) / cus) * (steps * step + tile);
     };
@@ -650,6 +719,8 @@ size_t linear_workspace(LinearArgs &a, void *ws) {
     a.form = kLinTile64;
     if (t128 < t64) a.form = kLinTile128;
     if (!no256 && t256 < (t128 < t64 ? t128 : t64)) a.form = kLinTile256;
+    const double t_tile = a.form == kLinTile64 ? t64 : a.form == kLinTile128 ? t128 : t256;
+    if (t_few < t_tile + 3) a.form = kLinStream;
     if (a.form != kLinTile64) a.nsplit = 1;
     if (a.nsplit == 1) return 0;
     a.part = (float *)ws;

@@ -127,7 +127,8 @@ def test_formula(M, N, K, act):
 
 @pytest.mark.parametrize("act", ["gelu", "swiglu"])
 @pytest.mark.parametrize("M,N,K", [(2500, 4096, 256), (2501, 4130, 256), (2500, 1026, 384),     # 256 and 128 row tiles
-                                   (1000, 1024, 2048), (70, 200, 4992)])                         # K splits
+                                   (1100, 264, 384), (1100, 520, 1024),                           # 64 row tiles
+                                   (1000, 1024, 2048), (1030, 264, 2432), (70, 200, 4992)])       # K splits
 def test_larger(M, N, K, act):
     p = Problem(M, N, K, act)
     check(p(), p.ref())
@@ -138,7 +139,8 @@ def test_no_rows():
     p()
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 192, 256), (40, 130, 384), (300, 520, 1024)])
+@pytest.mark.parametrize("M,N,K", [(3, 192, 256), (40, 130, 384), (300, 520, 1024), (1100, 264, 384),
+                                   (1030, 264, 2432), (2500, 1026, 384), (2500, 4096, 256)])
 @pytest.mark.parametrize("act", ["gelu", "swiglu"])
 def test_strides_and_residual_in_place(M, N, K, act):
     p = Problem(M, N, K, act)
@@ -159,7 +161,7 @@ def test_strides_and_residual_in_place(M, N, K, act):
     assert torch.equal(odd[1:].view(M, n), ref) and odd[0] == 3.0
 
 
-@pytest.mark.parametrize("M", [5, 200])
+@pytest.mark.parametrize("M", [4, 5, 200, 1100])
 @pytest.mark.parametrize("N", [96, 264])
 def test_values_at_the_edges(M, N):
     """NaN codes and infinite scales stay in their rows and columns; all-zero
@@ -211,7 +213,7 @@ def test_far_offsets():
 
 
 def test_deterministic_streams_and_graph():
-    for M, N, K, act in ((3, 512, 2048, "none"), (150, 1000, 1024, "swiglu")):
+    for M, N, K, act in ((3, 512, 2048, "none"), (150, 1000, 1024, "swiglu"), (1030, 264, 2432, "gelu")):
         p = Problem(M, N, K, act)
         ref = p()
         assert torch.equal(ref, p())
