@@ -607,20 +607,35 @@ group_tile_kernel(GroupMmArgs g) {
 // The forward product where experts hold a few rows each (decoded tokens):
 // the time is that of reading the touched experts' weights once.  A workgroup
 // takes 16 weight rows of one plan block; its NW waves split K, load weights
-// and x rows straight into registers (no LDS ring and no set-up launch to
-// wait for) U steps of 64 at a time, and add up in LDS.  Plan blocks with more than 16 NQ
-// routes go through the weights again for each further 16 NQ.
-template <bool F16, int NQ, int NW, int U>
+// straight into registers (no LDS ring and no set-up launch to wait for) U
+// steps of 64 at a time, and add up in LDS in order.  x rows are loaded in
+// the operand's layout too where a row or so is left of an expert; where more
+// differ (XL) they are copied to the wave's share of LDS, 8 whole rows of 128
+// bytes an instruction: a register load touches 16 rows, 64 bytes of each,
+// and costs the L1 twice the accesses (E = 8, K = 4096, N = 2048, 8 rows an
+// expert: 28.2 -> 25.7 us).  Plan blocks with more than 16 NQ routes go
+// through the weights again for each further 16 NQ.  Measured: one token, 9
+// of 257 experts, K = 7168, N = 512: 19 us for 66 MB, 3.5 TB/s with the
+// launch; 64 experts of 8 rows, K = 2048, N = 1024: 268 MB at 5.5 TB/s.
+template <bool F16, int NQ, int NW, int U, bool XL>
 __global__ void __launch_bounds__(64 * NW, 3)
 group_stream_kernel(GroupMmArgs g) {
-    __shared__ float red[NW][NQ][16][17];
+    // a wave's share of LDS: its rows of x (XL), then its sums [NQ][16][17]
+    constexpr int kSums = (NQ * 16 * 17 * 4 + 15) / 16 * 16, kRows = XL ? U * NQ * 2048 : 0;
+    constexpr int kWave = kRows > kSums ? kRows : kSums;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[NW * kWave];
     const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6), i16 = l & 15, grp = l >> 4;
+    uint8_t *const lds = smem + w * kWave;
+    // the lane's rows of x: row 16 n + i16, or in copies of 8 rows x 128 bytes
+    // row 8 n + l / 8
+    constexpr int NR = XL ? 2 * NQ : NQ;
+    auto row_of = [&](int n) { return XL ? 8 * n + (l >> 3) : 16 * n + i16; };
     // the plan's length and the block's routes are read together (the block
     // lies within sorted_cap), its expert once the block is known to exist
     const int b = blockIdx.y, bm = g.block_m;
-    int P = *g.ntp, ids[NQ];
+    int P = *g.ntp, ids[NR];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) ids[n] = g.sorted[b * bm + min(16 * n + i16, bm - 1)];
+    for (int n = 0; n < NR; ++n) ids[n] = g.sorted[b * bm + min(row_of(n), bm - 1)];
     P = P < g.sorted_cap ? P : (int)g.sorted_cap;
     if ((b + 1) * bm > P) return;
     const int e = uni(g.eids[b]);
@@ -629,19 +644,21 @@ group_stream_kernel(GroupMmArgs g) {
     const int c = c0 + i16 < g.N ? c0 + i16 : g.N - 1;
     const uint16_t *ap = g.w + ((int64_t)e * g.N + c) * g.K;
     const int nk = (g.K + 63) / 64;
+    const int x_off = i16 * 128 + ((grp ^ (i16 & 7)) << 4);
+    const u32x4 zero = {0u, 0u, 0u, 0u};
 
     for (int row0 = b * bm; row0 < (b + 1) * bm; row0 += 16 * NQ) {
         if (row0 > b * bm) {
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) ids[n] = g.sorted[row0 + min(16 * n + i16, bm - 1)];
+            for (int n = 0; n < NR; ++n) ids[n] = g.sorted[row0 + min(row_of(n), bm - 1)];
         }
         const int r0 = uni(ids[0]);                     // (lane 0: the first row)
         if (r0 < 0 || r0 >= g.R) break;                 // sentinels end the segment
-        const uint16_t *bp[NQ];
+        const uint16_t *bp[NR];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
+        for (int n = 0; n < NR; ++n) {
             int r = ids[n];
-            if (r < 0 || r >= g.R) r = r0;              // results of these lanes are not stored
+            if (r < 0 || r >= g.R) r = r0;              // results of these rows are not stored
             bp[n] = g.x + (int64_t)(g.per_route ? r : g.token_of(r)) * g.ld_x;
         }
         v4f acc[NQ];
@@ -651,33 +668,60 @@ group_stream_kernel(GroupMmArgs g) {
             u32x4 a[U][2], x[U][NQ][2];
             bool ok[U][2];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    int k = (k0 + u * NW) * 64 + 32 * h + 8 * grp;
-                    ok[u][h] = k < g.K;
-                    k = ok[u][h] ? k : 0;
-                    a[u][h] = *(const u32x4 *)(ap + k);
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) x[u][n][h] = *(const u32x4 *)(bp[n] + k);
-                }
-            __builtin_amdgcn_sched_barrier(0);          // every load above is issued first
-            const u32x4 zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u) {
+                const int ks = (k0 + u * NW) * 64;
+                if (ks >= g.K) break;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     // past the end of K: zeros on both sides
+                    const int k = ks + 32 * h + 8 * grp;
+                    ok[u][h] = k < g.K;
+                    a[u][h] = *(const u32x4 *)(ap + (ok[u][h] ? k : 0));
+                    if (!XL) {
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) x[u][n][h] = *(const u32x4 *)(bp[n] + (ok[u][h] ? k : 0));
+                    }
+                }
+                if (XL) {
+                    const int k = ks + 8 * ((l & 7) ^ (l >> 3));       // chunk c of row r lies at c ^ (r & 7)
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        lds_dma16(k < g.K ? (const void *)(bp[n] + k) : (const void *)kZeros,
+                                  lds + (u * NR + n) * 1024);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);          // every load above is issued first
+            if (XL) {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the wave's own copies
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if ((k0 + u * NW) * 64 >= g.K) break;
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        x[u][n][0] = lds_read16(lds + (u * NQ + n) * 2048 + x_off);
+                        x[u][n][1] = lds_read16(lds + (u * NQ + n) * 2048 + (x_off ^ 64));
+                    }
+                }
+                // read before the next steps' copies write there
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if ((k0 + u * NW) * 64 >= g.K) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     const u32x4 av = ok[u][h] ? a[u][h] : zero;
 #pragma unroll
                     for (int n = 0; n < NQ; ++n)
-                        acc[n] = mfma32<F16>(av, ok[u][h] ? x[u][n][h] : zero, acc[n]);
+                        acc[n] = mfma32<F16>(av, XL || ok[u][h] ? x[u][n][h] : zero, acc[n]);
                 }
+            }
         }
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) red[w][n][i16][4 * grp + v] = acc[n][v];
+            for (int v = 0; v < 4; ++v)
+                reinterpret_cast<float *>(lds)[(n * 16 + i16) * 17 + 4 * grp + v] = acc[n][v];
         __syncthreads();
         for (int i = tid; i < 16 * NQ * 8; i += 64 * NW) {
             const int cc = (i & 7) * 2, q = i >> 3;
@@ -686,8 +730,9 @@ group_stream_kernel(GroupMmArgs g) {
             if (r < 0 || r >= g.R) continue;
             float z0 = 0.f, z1 = 0.f;
             for (int k = 0; k < NW; ++k) {
-                z0 += red[k][q >> 4][q & 15][cc];
-                z1 += red[k][q >> 4][q & 15][cc + 1];
+                const float *d = reinterpret_cast<const float *>(smem + k * kWave) + q * 17 + cc;
+                z0 += d[0];
+                z1 += d[1];
             }
             *reinterpret_cast<uint32_t *>((uint16_t *)g.out + (int64_t)r * g.ld_out + c0 + cc) =
                 to16x2<F16>(z0, z1);
@@ -783,9 +828,9 @@ template <bool F16>
 hipError_t launch(const GroupMmArgs &g, hipStream_t st) {
     if (g.stream) {
         const dim3 grid((g.N + 15) / 16, (unsigned)(g.sorted_cap / g.block_m));
-        if (g.stream == 2) group_stream_kernel<F16, 2, 4, 4><<<grid, 256, 0, st>>>(g);
-        else if (g.K >= 4096) group_stream_kernel<F16, 1, 4, 7><<<grid, 256, 0, st>>>(g);
-        else group_stream_kernel<F16, 1, 4, 4><<<grid, 256, 0, st>>>(g);
+        if (g.stream == 2) group_stream_kernel<F16, 2, 4, 2, true><<<grid, 256, 0, st>>>(g);
+        else if (g.R > 4 * g.E) group_stream_kernel<F16, 1, 4, 4, true><<<grid, 256, 0, st>>>(g);
+        else group_stream_kernel<F16, 1, 4, 4, false><<<grid, 256, 0, st>>>(g);
         return hipGetLastError();
     }
     const bool summed = g.op == kGmmDx && !g.per_route;
@@ -851,15 +896,18 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
         double step;
     };
     static const Form forms[4] = {{256, 2.1}, {128, 0.95}, {64, 0.65}, {32, 0.55}};
+    auto parts = [&](int size) {                          // of at most `size` rows, of an expert
+        double per = 0;
+        if (rows > 32.0 * size) per = rows / size + 0.5;
+        else
+            for (int i = 0; i * size < rows + 5 * std::sqrt(rows) + 1; ++i)
+                per += 0.5 * std::erfc((i * size + 0.5 - rows) / std::sqrt(2 * rows));
+        return std::max(per, 1.0);
+    };
     double t_tile = 1e300;
     g.tile_rows = 32;
     for (const Form &f : forms) {
-        double per = 0;                                   // row tiles of an expert
-        if (rows > 32.0 * f.rows) per = rows / f.rows + 0.5;
-        else
-            for (int i = 0; i * f.rows < rows + 5 * std::sqrt(rows) + 1; ++i)
-                per += 0.5 * std::erfc((i * f.rows + 0.5 - rows) / std::sqrt(2 * rows));
-        if (per < 1) per = 1;
+        const double per = parts(f.rows);
         const double rounds = hit * per * ((np + 255) / 256) / 256;
         const double busy = (rounds < 4 ? std::ceil(rounds) : rounds + 0.5) * (steps * f.step + 4);
         const double mem = per * wbytes / 5.5e6;
@@ -869,19 +917,26 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
             g.tile_rows = f.rows;
         }
     }
-    // The few-rows kernel takes one workgroup per plan block and 16 columns,
-    // about 768 at a time, each some 2 us and 1 us per 256 of K, again for
-    // every 16 (or, from 16 rows per expert, 32) rows of a block; the tile
-    // kernels need a set-up launch, some 8 us.  Measured (us, few-rows against
-    // tile): K = 7168, N = 512, 9 / 36 / 112 experts hit 19 / 37 / 149 against
-    // 69 / 73 / 147; K = 1024, N = 512, 4 experts of 8 rows 5 against 17; K =
-    // 2048, N = 1024, 32 experts of 8 rows 34 against 28.
-    const double nq = rows <= 16 ? 1 : 2;
-    const double blocks = std::min(hit + R / g.block_m, (double)(g.sorted_cap / g.block_m));
-    const double passes = std::max(1.0, std::min(rows, (double)g.block_m) / (16 * nq));
-    const double t_few = std::ceil(blocks * ((g.N + 15) / 16) / 768) * passes * (2.0 + g.K / 256.0);
+    // The few-rows kernel, whose workgroups go through 16 columns' weights
+    // once for every 16 or 32 rows of a plan block: about 0.07 or 0.1 us per
+    // 64 of K on each CU, or the weights' way from HBM.  The tile kernels need
+    // a set-up launch before, some 3 us.  Measured (us, 16 rows / 32 rows /
+    // tile): E = 8, K = 4096, N = 2048, block_m 64 with 8, 16, 32, 75 rows an
+    // expert 26, 40, 62, 109 / 27, 28, 45, 72 / 45, 45, 46, 54; E = 8, K =
+    // 256, N = 512 with 2, 16, 75 rows 3.4, 4.6, 7.6 / 3.7, 3.8, 5.5 / 10, 10,
+    // 10.5; E = 32, K = 2048, N = 1024 with 2, 16, 62 rows 28, 41, 89 / 28,
+    // 29, 59 / 27, 27, 33.
+    double t_few = 0;
     g.stream = 0;
-    if (g.op == kGmmFwd && t_few < t_tile + 8 && g.sorted_cap / g.block_m <= 65535) g.stream = (int)nq;
+    if (g.op == kGmmFwd && g.sorted_cap / g.block_m <= 65535)
+        for (int nq = 1; nq <= 2; ++nq) {
+            const double wgs = hit * parts(std::min(g.block_m, 16 * nq)) * ((g.N + 15) / 16);
+            const double t = 2.5 + std::max(std::max(wgs / 256, 1.0) * steps * (0.04 + 0.03 * nq), wbytes / 5.5e6);
+            if (t < t_tile + 3 && (g.stream == 0 || t < t_few)) {
+                g.stream = nq;
+                t_few = t;
+            }
+        }
     if (g.stream) return 0;
     g.max_tiles = (int)(g.R / g.tile_rows + (g.E < g.R ? g.E : g.R));
     g.nsplit = 1;
