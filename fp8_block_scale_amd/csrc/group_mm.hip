@@ -942,15 +942,30 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
     g.nsplit = 1;
     g.dw_tile = 256;
     if (g.op == kGmmDw) {
-        int64_t tiles = (int64_t)g.E * ((g.N + 255) / 256) * ((g.K + 255) / 256);
-        if (tiles <= 128) {
-            g.dw_tile = 128;
-            tiles = (int64_t)g.E * ((g.N + 127) / 128) * ((g.K + 127) / 128);
+        // The tile and the splits by estimated time (us): 256-squared tiles
+        // take about 2.3 for each 64 rows, one to a CU; 128-squared ones 1.3,
+        // or 1.5 with two on a CU; a tile's fill and store 4; the join 4 and
+        // the way of the parts out and in.  Measured (us, 128-squared without
+        // splits beyond 256 items / so chosen): E = 4, K = 712, N = 1288 with
+        // 2048, 8192 rows an expert 59, 187 / 50, 106; E = 1, K = 4096, N =
+        // 2048 with 16384 rows 389 / 289; E = 3, K = 1000, N = 2048 with 5461
+        // rows 136 / 103.
+        double best = 1e300;
+        for (int t = 128; t <= 256; t += 128) {
+            const int64_t tiles = (int64_t)g.E * ((g.N + t - 1) / t) * ((g.K + t - 1) / t);
+            for (int sp = 1; sp == 1 || (sp <= 64 && sp <= rpe / 128 && tiles * sp <= 1024); ++sp) {
+                const int64_t items = tiles * sp, fit = t == 128 && items > 256 ? 512 : 256;
+                const double step = t == 256 ? 2.3 : fit == 512 ? 1.5 : 1.3;
+                const int64_t stages = (rpe + 64 * sp - 1) / (64 * sp);
+                const double cost = (double)((items + fit - 1) / fit) * ((double)stages * step + 4) +
+                                    (sp > 1 ? 4 + sp * ((double)g.E * g.N * g.K * 8 / 5e6) : 0);
+                if (cost < best) {
+                    best = cost;
+                    g.dw_tile = t;
+                    g.nsplit = sp;
+                }
+            }
         }
-        int64_t sp = 256 / tiles;                      // fewer tiles than CUs: cut the rows
-        if (sp > rpe / 128) sp = rpe / 128;
-        if (sp > 64) sp = 64;
-        if (sp > 1) g.nsplit = (int)sp;
     }
     uint8_t *base = (uint8_t *)ws;
     size_t off = 0;
