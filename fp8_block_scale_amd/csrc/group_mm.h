@@ -25,17 +25,17 @@ struct GroupMmArgs {
     void *out;               // y [R, ld_out], dx [M or R, ld_out] or dw [E, N, K]
     // the schedule and the workspace (group_mm_workspace)
     int stream;              // the few-rows kernel (forward): 16-row tiles per pass, 0: the tile kernel
-    int tile_rows;           // rows of a tile (forward, dx)
+    int tile_rows;           // rows of a tile (forward, dx) or a part (dw)
     int max_tiles;           // most row tiles that any routing gives
     int dw_tile;             // output tile of dw: 128 or 256 squared
-    int nsplit;              // dw: parts that an expert's rows are cut into
+    int max_slots;           // dw: most FP32 sums of parts of cut experts (0: none is cut)
     uint32_t div_m;          // r / top_k
     int div_s;
-    int32_t *meta;           // [1] row tiles
-    int2 *segs;              // [E] {first plan row, valid rows} of each expert
-    int4 *tiles;             // [max_tiles] {first plan row, rows, expert, 0}
+    int32_t *meta;           // [2] row tiles or parts; cut experts (dw)
+    int4 *tiles;             // [max_tiles] {first plan row, rows, expert, slot}
+    int4 *joins;             // [max_slots] {expert, first slot, slots} of the cut experts (dw)
     int32_t *rpos;           // [R] -1 if the route is masked (dx summed over routes)
-    float *part;             // FP32 rows [R, K] (dx summed over routes) or [nsplit, E, N, K] (dw)
+    float *part;             // FP32 rows [R, K] (dx summed over routes) or [max_slots, N, K] (dw)
 
     __host__ __device__ int token_of(int r) const {
         return (int)(((uint64_t)(uint32_t)r * div_m) >> (31 + div_s));

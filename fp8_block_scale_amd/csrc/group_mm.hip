@@ -22,6 +22,18 @@
 // stages are multiplied and its tile is stored (weight gradients have only a
 // few stages per tile).  Neighbouring items, which share rows or weights, run
 // on one XCD at the same time (panel_tile).
+//
+// What bounds it, measured.  Experts of a hundred rows and more: the matrix
+// cores' power.  E = 288, K = 4096, N = 2048, 8192 tokens of 8 routes in BF16
+// take 1.44 ms, 760 TFLOP/s of routes (1.1 PFLOP/s of the padded tiles), at
+// 1.4 GHz on random values; on zeros the clock stays at 2.4 GHz.  Experts of
+// some tens of rows: the weights (E = 512, K = 2048, N = 1024, 40 routes an
+// expert: 0.45 ms, 4.9 TB/s).  dx summed over a token's routes adds the FP32
+// rows' way through memory (4096 tokens at the first sizes: 1.25 ms, 440
+// TFLOP/s).  dw with a few stages per tile: the tile's store, some 3.5 us,
+// that the next tile's products do not cover (36 experts of 227 rows: 0.27 ms
+// for 0.6 GB out).  Small calls: the set-up launch (4.5 us) and the latency
+// of a tile's first copies.
 #include <algorithm>
 #include <cmath>
 
@@ -67,11 +79,13 @@ __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 
 
 // ------------------------------------------------------------ set-up launch
 
-// Workgroup 0 finds every expert's rows in the plan, segs[e] = {first plan
-// row, valid rows} (its sentinels, all at the end, cut off by a binary search
-// of its last block), and cuts them into row tiles of tile_rows, listed as
-// {first row, rows, expert, 0} with their count in meta[0].  The other
-// workgroups set rpos[0, R) = -1 for the sum over a token's routes.
+// Workgroup 0 finds every expert's rows in the plan (its sentinels are all at
+// the end of its last block) and cuts them into row tiles of tile_rows, listed
+// as {first row, rows, expert, slot} with their count in meta[0].  For dw an expert without rows has one empty tile, the
+// tiles of an expert with several have slots one after the other (else -1),
+// and those experts, meta[1] of them, are listed as joins = {expert, first
+// slot, slots}.  The other workgroups set rpos[0, R) = -1 for the sum over a
+// token's routes.
 constexpr int kPrepThreads = 1024;
 
 __global__ void __launch_bounds__(kPrepThreads)
@@ -82,49 +96,70 @@ group_prep_kernel(GroupMmArgs g, int tile_rows) {
         for (int64_t i = (int64_t)(blockIdx.x - 1) * kPrepThreads + tid; i < g.R; i += stride) g.rpos[i] = -1;
         return;
     }
-    __shared__ int first[1024], last[1024], pre[1025], wsum[16];
+    __shared__ int first[1024], last[1024], pre[1025], slot[1024], wsum[16];
     int P = *g.ntp;
     P = P < g.sorted_cap ? P : (int)g.sorted_cap;
     const int bm = g.block_m, nb = P > 0 ? P / bm : 0;
     first[tid] = last[tid] = 0;
     __syncthreads();
     for (int b = tid; b < nb; b += kPrepThreads) {
-        const int e = g.eids[b];
+        const int e = g.eids[b], before = g.eids[b > 0 ? b - 1 : 0], after = g.eids[b < nb - 1 ? b + 1 : b];
         if (e < 0 || e >= g.E) continue;
-        if (b == 0 || g.eids[b - 1] != e) first[e] = b;
-        if (b == nb - 1 || g.eids[b + 1] != e) last[e] = b + 1;
+        if (b == 0 || before != e) first[e] = b;
+        if (b == nb - 1 || after != e) last[e] = b + 1;
     }
     __syncthreads();
     int rows = 0;
     if (last[tid] > first[tid]) {
-        int lo = (last[tid] - 1) * bm, hi = last[tid] * bm;
-        while (lo < hi) {                       // first sentinel of the last block
-            const int mid = (lo + hi) >> 1;
-            const int r = g.sorted[mid];
-            if (r >= 0 && r < g.R) lo = mid + 1;
-            else hi = mid;
+        // the valid rows of the last block: in eighths, then in the eighth
+        // that they end in (two rounds of loads, where halving takes up to 7)
+        const int *blk = g.sorted + (last[tid] - 1) * bm;
+        auto valid = [&](int i) { return (uint32_t)blk[i] < (uint32_t)g.R; };
+        const int step = bm >> 3;                    // 1 to 16
+        int pos = 0;
+#pragma unroll
+        for (int k = 1; k <= 8; ++k) pos += valid(k * step - 1) ? step : 0;
+        int more = 0;
+        if (pos < bm) {
+#pragma unroll
+            for (int k = 0; k < 15; ++k) more += (int)valid(min(pos + k, bm - 1)) & (int)(k < step - 1);
         }
-        rows = lo - first[tid] * bm;
+        rows = (last[tid] - 1 - first[tid]) * bm + pos + more;
     }
-    if (tid < g.E) g.segs[tid] = make_int2(first[tid] * bm, rows);
-    const int cnt = (rows + tile_rows - 1) / tile_rows;
-    int incl = cnt;
-    for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(incl, d, 64);
-        if ((tid & 63) >= d) incl += v;
-    }
-    if ((tid & 63) == 63) wsum[tid >> 6] = incl;
-    __syncthreads();
-    for (int q = 0; q < (tid >> 6); ++q) incl += wsum[q];
-    pre[tid + 1] = incl;
+    int cnt = (rows + tile_rows - 1) / tile_rows;
+    if (g.op == kGmmDw && tid < g.E && cnt == 0) cnt = 1;
+    const int waves = (g.E + 63) >> 6;          // with experts (the others add nothing)
+    auto scan = [&](int v) {                    // inclusive sum over the threads
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(v, d, 64);
+            if ((tid & 63) >= d) v += o;
+        }
+        __syncthreads();
+        if ((tid & 63) == 63) wsum[tid >> 6] = v;
+        __syncthreads();
+        for (int q = 0; q < (tid >> 6) && q < waves; ++q) v += wsum[q];
+        return v;
+    };
+    pre[tid + 1] = scan(cnt);
     if (tid == 0) pre[0] = 0;
+    slot[tid] = -1;
+    if (g.max_slots > 0) {
+        const int end = scan(cnt > 1 ? cnt : 0);
+        const bool cut = cnt > 1 && end <= g.max_slots;        // (no more in a plan that lists a route once)
+        const int j = scan(cut ? 1 : 0);
+        if (cut) {
+            slot[tid] = end - cnt;
+            g.joins[j - 1] = make_int4(tid, end - cnt, cnt, 0);
+        }
+        if (tid == kPrepThreads - 1) g.meta[1] = j;
+    }
     __syncthreads();
     const int n = pre[1024];
     if (tid == 0) g.meta[0] = n;
     last[tid] = rows;
     __syncthreads();
     for (int i = tid; i < n && i < g.max_tiles; i += kPrepThreads) {
-        int lo = 0, hi = 1023;                  // the expert e with pre[e] <= i < pre[e + 1]
+        int lo = 0, hi = g.E - 1;               // the expert e with pre[e] <= i < pre[e + 1]
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (pre[mid + 1] <= i) lo = mid + 1;
@@ -132,7 +167,8 @@ group_prep_kernel(GroupMmArgs g, int tile_rows) {
         }
         const int off = (i - pre[lo]) * tile_rows;
         const int rem = last[lo] - off;
-        g.tiles[i] = make_int4(first[lo] * bm + off, rem < tile_rows ? rem : tile_rows, lo, 0);
+        g.tiles[i] = make_int4(first[lo] * bm + off, rem < tile_rows ? rem : tile_rows, lo,
+                               slot[lo] >= 0 ? slot[lo] + i - pre[lo] : -1);
     }
 }
 
@@ -152,7 +188,7 @@ struct Tile {
     static constexpr int Ahead = (S - 2) * (JP + QB / 1024 / NW);   // copies that may be in flight
     static constexpr int NP = TP / WP / 16, NQ = TQ / WQ / 16;
     // behind the stages: the routes of an item's rows (forward, dx; a ring of
-    // S items), or the routes of a stage's rows (two) and all experts' rows (dw)
+    // S items), or the routes of a stage's rows (two) and the list of parts (dw)
     static constexpr int Tail = QKS ? 2 * 256 : S * TQ * 4;
     static constexpr size_t Smem = (size_t)S * Stage + Tail;
     static_assert(NP % 2 == 0 && JP >= 1 && NW % 2 == 0 && Smem <= 160 * 1024, "tile");
@@ -176,7 +212,7 @@ group_tile_kernel(GroupMmArgs g) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     int *rids = reinterpret_cast<int *>(smem + (size_t)S * T::Stage);          // [S][TQ] (forward, dx)
     int *sids = rids;                                                          // [2][64] (dw)
-    int2 *segs = reinterpret_cast<int2 *>(smem + (size_t)S * T::Stage + 512);  // [E] (dw)
+    int4 *parts = reinterpret_cast<int4 *>(smem + (size_t)S * T::Stage + 512); // [max_tiles] (dw)
 
     const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6);
     const int wp = w % WP, wq = w / WP;
@@ -184,46 +220,33 @@ group_tile_kernel(GroupMmArgs g) {
     const int nct = (np + TP - 1) / TP;
 
     // ---- the items of this workgroup: a contiguous range per XCD
-    int n_items, qtiles = 1, ntiles = 0;
-    if (DW) {
-        qtiles = (g.N + TQ - 1) / TQ;
-        n_items = g.E * qtiles * nct * g.nsplit;
-    } else {
-        ntiles = uni(g.meta[0]);
-        ntiles = ntiles < g.max_tiles ? ntiles : g.max_tiles;
-        n_items = ntiles * nct;
-    }
+    const int ntiles = min(uni(g.meta[0]), g.max_tiles);
+    const int qtiles = DW ? (g.N + TQ - 1) / TQ : 1;
+    const int n_items = ntiles * nct * qtiles;
     const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
     const int end = (int)((int64_t)(xcd + 1) * n_items / 8);
     int lit = (int)((int64_t)xcd * n_items / 8) + (blockIdx.x >> 3);     // load cursor
     int cit = lit;                                                        // compute cursor
     if (cit >= end) return;
     if (DW) {
-        for (int i = tid; i < g.E; i += 64 * NW) segs[i] = g.segs[i];
+        for (int i = tid; i < ntiles; i += 64 * NW) parts[i] = g.tiles[i];
         __syncthreads();
     }
 
     struct Item {
-        int e, ct, qt, sp;           // expert, column tile, row tile and split (dw)
+        int e, ct, qt, slot;         // expert, column tile; row tile and slot of the FP32 sums (dw)
         int row0, rows;              // its plan rows
     };
     auto item_of = [&](int i) {
         Item it = {};
         if (DW) {
-            it.sp = i % g.nsplit;
-            i /= g.nsplit;
-            int rt;
-            const int per_e = qtiles * nct;
-            it.e = i / per_e;
-            panel_tile<4>(i - it.e * per_e, qtiles, nct, rt, it.ct);
-            it.qt = rt;
-            const int2 sg = segs[it.e];
-            const int seg_rows = uni(sg.y);
-            const int per = (seg_rows + 64 * g.nsplit - 1) / (64 * g.nsplit) * 64;   // rows per split
-            const int r0 = it.sp * per;
-            const int left = seg_rows - r0;
-            it.row0 = uni(sg.x) + (left > 0 ? r0 : 0);
-            it.rows = left < 0 ? 0 : left < per ? left : per;
+            const int per = qtiles * nct, j = i / per;
+            panel_tile<4>(i - j * per, qtiles, nct, it.qt, it.ct);
+            const int4 t = parts[j];
+            it.row0 = uni(t.x);
+            it.rows = uni(t.y);
+            it.e = uni(t.z);
+            it.slot = uni(t.w);
         } else {
             int rt;
             panel_tile<4>(i, ntiles, nct, rt, it.ct);
@@ -428,8 +451,8 @@ group_tile_kernel(GroupMmArgs g) {
                     const int c = c0 + 32 * m;
                     if (c >= g.K) continue;
                     v4f x = acc[2 * m][n], y = acc[2 * m + 1][n];
-                    if (g.nsplit > 1) {
-                        float *d = g.part + (int64_t)it.sp * g.E * g.N * g.K + o + c;
+                    if (it.slot >= 0) {
+                        float *d = g.part + ((int64_t)it.slot * g.N + row) * g.K + c;
                         *reinterpret_cast<v4f *>(d) = x;
                         *reinterpret_cast<v4f *>(d + 4) = y;
                     } else if (g.out_f32) {
@@ -769,40 +792,49 @@ group_sum_kernel(GroupMmArgs g, int lanes, int64_t blocks) {
     }
 }
 
-// dw = the sum of the splits' FP32 tiles, in split order.
+// dw of the experts whose rows were cut = the sum of their parts' FP32 tiles,
+// in order.
 template <bool F16>
 __global__ void __launch_bounds__(256)
 group_join_kernel(GroupMmArgs g) {
-    const int64_t n = (int64_t)g.E * g.N * g.K;
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= n) return;
-    v4f s = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < g.nsplit; ++k) s += *reinterpret_cast<const v4f *>(g.part + k * n + i);
-    if (g.out_f32) {
-        v4f *d = reinterpret_cast<v4f *>((float *)g.out + i);
-        *d = g.accumulate ? *d + s : s;
-    } else {
-        uint2 *d = reinterpret_cast<uint2 *>((uint16_t *)g.out + i);
-        if (g.accumulate) {
-            const uint2 o = *d;
-            s[0] += from16<F16>(o.x);
-            s[1] += from16<F16>(o.x >> 16);
-            s[2] += from16<F16>(o.y);
-            s[3] += from16<F16>(o.y >> 16);
+    const int64_t n = (int64_t)g.N * g.K, per = (n / 4 + 255) / 256;
+    const int64_t items = g.meta[1] * per;
+    for (int64_t b = blockIdx.x; b < items; b += gridDim.x) {
+        const int4 t = g.joins[b / per];
+        const int64_t i = ((b % per) * 256 + threadIdx.x) * 4;
+        if (i >= n) continue;
+        v4f s = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < t.z; ++k) s += *reinterpret_cast<const v4f *>(g.part + (t.y + k) * n + i);
+        if (g.out_f32) {
+            v4f *d = reinterpret_cast<v4f *>((float *)g.out + t.x * n + i);
+            *d = g.accumulate ? *d + s : s;
+        } else {
+            uint2 *d = reinterpret_cast<uint2 *>((uint16_t *)g.out + t.x * n + i);
+            if (g.accumulate) {
+                const uint2 o = *d;
+                s[0] += from16<F16>(o.x);
+                s[1] += from16<F16>(o.x >> 16);
+                s[2] += from16<F16>(o.y);
+                s[3] += from16<F16>(o.y >> 16);
+            }
+            *d = uint2{to16x2<F16>(s[0], s[1]), to16x2<F16>(s[2], s[3])};
         }
-        *d = uint2{to16x2<F16>(s[0], s[1]), to16x2<F16>(s[2], s[3])};
     }
 }
 
 // ----------------------------------------------------------------- launch
+
+// Most parts that dw cuts the experts' rows into: their list stays in LDS.
+constexpr int kMaxParts = 1984;
+static_assert(Tile<true, kGmmDw, 256, 256, 4, 2, 2>::Smem + kMaxParts * 16 <= 160 * 1024, "list of parts");
 
 template <bool F16, int OP, int TP, int TQ, int WP, int WQ, int S>
 hipError_t launch_tile(const GroupMmArgs &g, int64_t max_items, hipStream_t st) {
     using T = Tile<F16, OP, TP, TQ, WP, WQ, S>;
     static std::atomic<uint64_t> done{0};
     auto fn = group_tile_kernel<F16, OP, TP, TQ, WP, WQ, S>;
-    const size_t smem = T::Smem + (OP == kGmmDw ? (size_t)g.E * 8 : 0);
-    hipError_t e = raise_lds_limit(done, (const void *)fn, (int)(T::Smem + (OP == kGmmDw ? 1024 * 8 : 0)));
+    const size_t smem = T::Smem + (OP == kGmmDw ? (size_t)g.max_tiles * 16 : 0);
+    hipError_t e = raise_lds_limit(done, (const void *)fn, (int)(T::Smem + (OP == kGmmDw ? kMaxParts * 16 : 0)));
     if (e != hipSuccess) return e;
     const int64_t per_cu = (160 * 1024) / (int64_t)smem;
     int64_t grid = (int64_t)device_cu_count() * (per_cu < 2 ? 1 : 2);
@@ -840,12 +872,12 @@ hipError_t launch(const GroupMmArgs &g, hipStream_t st) {
     if (e != hipSuccess) return e;
     if (g.op == kGmmDw) {
         const int64_t t = g.dw_tile;
-        const int64_t items = (int64_t)g.E * ((g.N + t - 1) / t) * ((g.K + t - 1) / t) * g.nsplit;
+        const int64_t items = (int64_t)g.max_tiles * ((g.N + t - 1) / t) * ((g.K + t - 1) / t);
         e = t == 256 ? launch_tile<F16, kGmmDw, 256, 256, 4, 2, 2>(g, items, st)
                      : launch_tile<F16, kGmmDw, 128, 128, 2, 2, 2>(g, items, st);
-        if (e != hipSuccess || g.nsplit == 1) return e;
-        const int64_t n = (int64_t)g.E * g.N * g.K / 4;
-        group_join_kernel<F16><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g);
+        if (e != hipSuccess || g.max_slots == 0) return e;
+        const int64_t n = (int64_t)g.max_slots * (((int64_t)g.N * g.K / 4 + 255) / 256);
+        group_join_kernel<F16><<<(unsigned)std::min(n, (int64_t)2048), 256, 0, st>>>(g);
         return hipGetLastError();
     }
     e = g.op == kGmmFwd ? launch_rows<F16, kGmmFwd>(g, st) : launch_rows<F16, kGmmDx>(g, st);
@@ -938,8 +970,7 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
             }
         }
     if (g.stream) return 0;
-    g.max_tiles = (int)(g.R / g.tile_rows + (g.E < g.R ? g.E : g.R));
-    g.nsplit = 1;
+    g.max_slots = 0;
     g.dw_tile = 256;
     if (g.op == kGmmDw) {
         // The tile and the splits by estimated time (us): 256-squared tiles
@@ -951,9 +982,10 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
         // 2048 with 16384 rows 389 / 289; E = 3, K = 1000, N = 2048 with 5461
         // rows 136 / 103.
         double best = 1e300;
+        int nsplit = 1;
         for (int t = 128; t <= 256; t += 128) {
             const int64_t tiles = (int64_t)g.E * ((g.N + t - 1) / t) * ((g.K + t - 1) / t);
-            for (int sp = 1; sp == 1 || (sp <= 64 && sp <= rpe / 128 && tiles * sp <= 1024); ++sp) {
+            for (int sp = 1; sp == 1 || (sp <= 64 && sp <= rpe / 128 && tiles * sp <= 512); ++sp) {
                 const int64_t items = tiles * sp, fit = t == 128 && items > 256 ? 512 : 256;
                 const double step = t == 256 ? 2.3 : fit == 512 ? 1.5 : 1.3;
                 const int64_t stages = (rpe + 64 * sp - 1) / (64 * sp);
@@ -962,11 +994,28 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
                 if (cost < best) {
                     best = cost;
                     g.dw_tile = t;
-                    g.nsplit = sp;
+                    nsplit = sp;
                 }
             }
         }
+        // Rows of an expert are cut into parts of tile_rows.  Also where an
+        // even spread needs no cut: an expert with more than twice the average
+        // would take its time alone (190 experts of K = 152, N = 240 with 230
+        // rows on average, one of them with a fifth of all: 141 us uncut, 37
+        // cut).  The join's launch costs 4 us and a cut expert's parts FP32
+        // slots (an expert with several parts has fewer than 2 rows /
+        // tile_rows of them): not for few rows, and not for more than 256 MB.
+        // (Room for the spread of a random routing, so that it gives no
+        // further part.)
+        const int64_t most = rpe + (int64_t)(3 * std::sqrt((double)rpe)) + 1;
+        const int64_t even = (most + 64 * nsplit - 1) / (64 * nsplit) * 64;
+        int64_t cut = nsplit > 1 ? even : 2 * even;
+        if (nsplit == 1 && (g.R < 4096 || g.R * 2 / cut * g.N * g.K > (int64_t)1 << 26)) cut = g.R;
+        if (g.R / cut + g.E > kMaxParts) cut = g.R;
+        g.tile_rows = (int)cut;
+        if (cut < g.R) g.max_slots = (int)(2 * g.R / cut);
     }
+    g.max_tiles = (int)(g.R / g.tile_rows + (g.E < g.R || g.op == kGmmDw ? g.E : g.R));
     uint8_t *base = (uint8_t *)ws;
     size_t off = 0;
     auto take = [&](size_t n) {
@@ -974,14 +1023,16 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
         off += (n + 255) & ~size_t(255);
         return p;
     };
-    g.meta = (int32_t *)take(4);
-    g.segs = (int2 *)take((size_t)g.E * 8);
+    g.meta = (int32_t *)take(8);
     g.tiles = (int4 *)take((size_t)g.max_tiles * 16);
     if (g.op == kGmmDx && !g.per_route) {
         g.rpos = (int32_t *)take((size_t)g.R * 4);
         g.part = (float *)take((size_t)g.R * g.K * 4);
     }
-    if (g.nsplit > 1) g.part = (float *)take((size_t)g.nsplit * g.E * g.N * g.K * 4);
+    if (g.max_slots > 0) {
+        g.joins = (int4 *)take((size_t)g.max_slots * 16);
+        g.part = (float *)take((size_t)g.max_slots * g.N * g.K * 4);
+    }
     return off;
 }
 

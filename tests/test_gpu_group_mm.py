@@ -283,6 +283,28 @@ def test_overflow_rounds_to_infinity():
     assert torch.isposinf(p.y()).all()
 
 
+@pytest.mark.parametrize("M,E,K,N,k,bm", [(2100, 190, 152, 240, 2, 16), (3000, 9, 136, 200, 2, 64),
+                                          (5000, 40, 264, 520, 1, 32)])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_dw_of_a_crowded_expert(M, E, K, N, k, bm, dt, accumulate):
+    """One expert holds most routes (its rows are cut and joined), some a few,
+    the first and the last none."""
+    p = Problem(dt, M, E, K, N, k, bm)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    p.ids = torch.randint(1, E - 1, (M, k), generator=g, device=DEV)
+    p.ids[torch.rand((M, k), generator=g, device=DEV) < 0.6] = 3
+    p.plan = make_plan(p.ids, E, bm)
+    for out in (dt, F32):
+        before = torch.randn((E, N, K), generator=g, device=DEV).to(out)
+        v, s, n = p.ref_dw()
+        ref = (v + before.double(), s + before.double().abs(), n + 1) if accumulate else (v, s, n)
+        got = p.dw(out, before.clone(), accumulate)
+        check(got, ref, out)
+        assert torch.equal(got, p.dw(out, before.clone(), accumulate))
+
+
 @pytest.mark.parametrize("M", [9, 700])
 def test_subnormals(M):
     """FP16 subnormals (here the multiples of 2^-24 up to 2^-14) are values
