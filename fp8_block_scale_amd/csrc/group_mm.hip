@@ -25,15 +25,15 @@
 //
 // What bounds it, measured.  Experts of a hundred rows and more: the matrix
 // cores' power.  E = 288, K = 4096, N = 2048, 8192 tokens of 8 routes in BF16
-// take 1.44 ms, 760 TFLOP/s of routes (1.1 PFLOP/s of the padded tiles), at
-// 1.4 GHz on random values; on zeros the clock stays at 2.4 GHz.  Experts of
-// some tens of rows: the weights (E = 512, K = 2048, N = 1024, 40 routes an
-// expert: 0.45 ms, 4.9 TB/s).  dx summed over a token's routes adds the FP32
-// rows' way through memory (4096 tokens at the first sizes: 1.25 ms, 440
-// TFLOP/s).  dw with a few stages per tile: the tile's store, some 3.5 us,
-// that the next tile's products do not cover (36 experts of 227 rows: 0.27 ms
-// for 0.6 GB out).  Small calls: the set-up launch (4.5 us) and the latency
-// of a tile's first copies.
+// take 1.45 ms, 760 TFLOP/s of routes (the padding of each expert's last tile
+// comes on top), at 1.4 GHz on random values; on zeros the clock stays at 2.4
+// GHz.  Experts of some tens of rows: the weights (E = 512, K = 2048, N =
+// 1024, 40 routes an expert: 0.45 ms, 4.7 TB/s).  dx summed over a token's
+// routes adds the FP32 rows' way through memory (4096 tokens at the first
+// sizes: 1.25 ms, 440 TFLOP/s).  dw with a few stages per tile: the tile's
+// store, some 3.5 us, that the next tile's products do not cover (36 experts
+// of 227 rows: 0.26 ms for 0.6 GB out).  Small calls: the set-up launch (4 us)
+// and the latency of a tile's first copies.
 #include <algorithm>
 #include <cmath>
 
