@@ -994,8 +994,10 @@ moe_status check_group_shape(int64_t M, int64_t K, int64_t N, int32_t E, int32_t
         return fail(MOE_ERR_UNSUPPORTED, "block_m %d not in {8, 16, 32, 64, 128}", block_m);
     if (sorted_cap < 0 || sorted_cap % block_m != 0)
         return fail(MOE_ERR_SHAPE, "sorted_cap must be a non-negative multiple of block_m");
-    if (M >= ((int64_t)1 << 31) / top_k || sorted_cap >= (int64_t)1 << 31)
-        return fail(MOE_ERR_SHAPE, "M * top_k and sorted_cap must fit in int32");
+    // (rows of the plan are int32, rounded up to whole stages)
+    constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1024;
+    if (M > kMaxRows / top_k || sorted_cap > kMaxRows)
+        return fail(MOE_ERR_SHAPE, "M * top_k and sorted_cap must not exceed 2^31 - 1024");
     // the kernels number their output tiles (at least 32 routes x 128 columns,
     // 128 x 128 of a weight) in int32
     const int64_t n = (N + 127) / 128, k = (K + 127) / 128, rows = M * top_k / 32 + E;

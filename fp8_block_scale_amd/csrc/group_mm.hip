@@ -126,7 +126,7 @@ group_prep_kernel(GroupMmArgs g, int tile_rows) {
         }
         rows = (last[tid] - 1 - first[tid]) * bm + pos + more;
     }
-    int cnt = (rows + tile_rows - 1) / tile_rows;
+    int cnt = rows / tile_rows + (rows % tile_rows != 0);
     if (g.op == kGmmDw && tid < g.E && cnt == 0) cnt = 1;
     const int waves = (g.E + 63) >> 6;          // with experts (the others add nothing)
     auto scan = [&](int v) {                    // inclusive sum over the threads
@@ -1012,6 +1012,7 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
         int64_t cut = nsplit > 1 ? even : 2 * even;
         if (nsplit == 1 && (g.R < 4096 || g.R * 2 / cut * g.N * g.K > (int64_t)1 << 26)) cut = g.R;
         if (g.R / cut + g.E > kMaxParts) cut = g.R;
+        if (cut > g.R) cut = g.R;
         g.tile_rows = (int)cut;
         if (cut < g.R) g.max_slots = (int)(2 * g.R / cut);
     }

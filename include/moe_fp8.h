@@ -455,7 +455,8 @@ moe_status moe_w4a8_experts(const uint8_t *x_q, const float *x_s,
  * ascending expert id, sentinels at the end of a segment only, each route
  * listed once; entries that are not ids of a route or an expert are skipped.
  * Constraints: K and N multiples of 8, at most 2^20; E <= 1024; block_m in
- * {8, 16, 32, 64, 128}; sorted_cap % block_m == 0; x, w, dy, y, dx and dw
+ * {8, 16, 32, 64, 128}; sorted_cap % block_m == 0; M * top_k and sorted_cap
+ * at most 2^31 - 1024; x, w, dy, y, dx and dw
  * 16-byte aligned, leading dimensions multiples of 8 and at most 2^30;
  * outputs overlap no input.  The workspace (256-byte aligned) holds
  * moe_group_mm_workspace_size(op, ...) bytes (0: none needed, NULL accepted;

@@ -59,6 +59,8 @@ def test_group_refusals(f):
     assert f(sc=120) == "MOE_ERR_SHAPE"
     assert f(M=1 << 30, k=2) == "MOE_ERR_SHAPE"
     assert f(sc=1 << 31) == "MOE_ERR_SHAPE"
+    assert f(sc=(1 << 31) - 16) == "MOE_ERR_SHAPE"
+    assert f(M=(1 << 31) - 1023, k=1) == "MOE_ERR_SHAPE"
     assert f(dt=2) == "MOE_ERR_SHAPE"
     assert f(ldx=56) == "MOE_ERR_SHAPE"
     assert f(ldy=24) == "MOE_ERR_SHAPE"
