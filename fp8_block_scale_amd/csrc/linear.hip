@@ -21,6 +21,8 @@
 // 8192 cubed): bound by the scaling's vector instructions next to the matrix
 // cores' power.  1000 x 1001 x 2048: 16 us, bound by latency: 13 us for 8
 // steps of a ring on every CU, 4 us for the join's launch.
+#include <algorithm>
+
 #include "linear.h"
 #include "tiles.h"
 
@@ -670,7 +672,7 @@ hipError_t launch(const LinearArgs &g, hipStream_t st) {
             if constexpr (GLU < 2) return launch_tile<256, 256, 4, 2, 2, GLU, false>(g, st);
             [[fallthrough]];
         case kLinTile128: return launch_tile<256, 128, 4, 2, 3, GLU, false>(g, st);
-        default: return launch_tile<128, 64, 2, 2, 6, GLU, true>(g, st);
+        default: return launch_tile<128, 64, 2, 2, 3, GLU, true>(g, st);
     }
 }
 
@@ -685,7 +687,7 @@ size_t linear_workspace(LinearArgs &a, void *ws) {
     // Tile form by estimated time: rounds of tiles over the CUs, each nkb
     // steps and a fill and store of the tile.  Per step and per tile, measured
     // with every CU busy: 256 x 256 2.0 and 10 us, 256 x 128 1.1 and 6 us,
-    // 128 x 64 0.67 and 3 us.  (The larger tile does the most per step, the
+    // 128 x 64, alone on its CU, 0.8 and 3 us.  (The larger tile does the most per step, the
     // smaller ones lose less to a last, partly filled round.)
     const int64_t cus = 256;
     // Few rows by estimated time: a workgroup of 16 NQ rows takes (0.075 +
@@ -708,15 +710,24 @@ size_t linear_workspace(LinearArgs &a, void *ws) {
         return (double)((it + cus - 1) / cus) * (steps * step + tile);
     };
     const double t256 = est(items(256, 256), nkb, 2.0, 10.0), t128 = est(items(256, 128), nkb, 1.1, 6.0);
-    // the small tile may split K over the idle CUs (at least 4 steps each);
-    // joining the parts costs about 4 us
+    // The small tile has a ring of three stages, so that two fit a CU and hide
+    // each other's waits: 0.97 us a step and 3.5 a tile for both (K = 4096, N =
+    // 1024, 4000 rows 46 us with six stages and one tile a CU, 36 so).  It may
+    // split K over idle CUs (at least 4 steps each); joining the parts costs
+    // about 4 us and their way through memory.  Measured, K = 4096, N = 1024
+    // (us, parts): 512 rows 15.6 (4), 18.1 (8); 700 rows 18.8 (2), 16.5 (5);
+    // 1500 rows 26.9 (1), 23.8 (2).
     const int64_t it64 = items(128, 64);
-    int64_t sp = cus / it64 < nkb / 4 ? cus / it64 : nkb / 4;
-    double t64 = est(it64, nkb, 0.67, 3.0);
-    if (sp > 1) {
+    auto est64 = [&](int64_t it, int steps) {
+        return it <= cus ? steps * 0.8 + 3.0 : (double)((it + 2 * cus - 1) / (2 * cus)) * (steps * 0.97 + 3.5);
+    };
+    double t64 = est64(it64, nkb);
+    for (int64_t fit = cus; fit <= 2 * cus; fit += cus) {
+        int64_t sp = std::min(fit / it64, (int64_t)nkb / 4);
+        if (sp < 2) continue;
         const int per = (int)((nkb + sp - 1) / sp);
         sp = (nkb + per - 1) / per;                                // none empty
-        const double t = est(it64 * sp, per, 0.67, 3.0) + 4.0;
+        const double t = est64(it64 * sp, per) + 4.0 + (double)sp * a.M * n * 1.1e-6;
         if (t < t64) {
             t64 = t;
             a.nsplit = (int)sp;
