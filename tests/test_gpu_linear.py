@@ -128,7 +128,9 @@ def test_formula(M, N, K, act):
 @pytest.mark.parametrize("act", ["gelu", "swiglu"])
 @pytest.mark.parametrize("M,N,K", [(2500, 4096, 256), (2501, 4130, 256), (2500, 1026, 384),     # 256 and 128 row tiles
                                    (1100, 264, 384), (1100, 520, 1024),                           # 64 row tiles
-                                   (1000, 1024, 2048), (1030, 264, 2432), (70, 200, 4992)])       # K splits
+                                   (1000, 1024, 2048), (1030, 264, 2432), (70, 200, 4992),        # K splits
+                                   (700, 1024, 4096), (4100, 1040, 384), (6000, 1026, 256), (2500, 2048, 2048),
+                                   (3000, 1026, 512)])
 def test_larger(M, N, K, act):
     p = Problem(M, N, K, act)
     check(p(), p.ref())
