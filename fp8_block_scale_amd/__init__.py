@@ -513,8 +513,12 @@ def _x_rows(where, name, t, R, top_k, per_route):
     return int(bool(per_route))
 
 
-def _ws(workspace):
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+def _ws(where, workspace):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise MoeError(MOE_ERR_SHAPE, where, "workspace must be contiguous")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def moe_group_mm_workspace_size(op, M, K, N, E, top_k, block_m, sorted_cap, x_per_route=False):
@@ -539,7 +543,7 @@ def moe_group_mm(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, top
     per_route = _x_rows(where, "x", x, R, top_k, x_per_route)
     _launch(where, stream, (x, w, out, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace),
             xp, ld_x, per_route, w.data_ptr(), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
-            sorted_token_ids.numel(), yp, ld_y, *_ws(workspace))
+            sorted_token_ids.numel(), yp, ld_y, *_ws(where, workspace))
 
 
 def moe_group_mm_dx(dy, w, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, dx,
@@ -558,7 +562,7 @@ def moe_group_mm_dx(dy, w, sorted_token_ids, expert_ids, num_tokens_post_padded,
     per_route = _x_rows(where, "dx", dx, R, top_k, x_per_route)
     _launch(where, stream, (dy, w, dx, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace),
             yp, ld_y, w.data_ptr(), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
-            sorted_token_ids.numel(), xp, ld_x, per_route, *_ws(workspace))
+            sorted_token_ids.numel(), xp, ld_x, per_route, *_ws(where, workspace))
 
 
 def moe_group_mm_dw(dy, x, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, dw,
@@ -579,7 +583,7 @@ def moe_group_mm_dw(dy, x, sorted_token_ids, expert_ids, num_tokens_post_padded,
     _launch(where, stream, (dy, x, dw, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace),
             yp, ld_y, xp, ld_x, per_route, _DT[dy.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
             sorted_token_ids.numel(), dw.data_ptr(), _DT[dw.dtype], int(bool(accumulate)),
-            *_ws(workspace))
+            *_ws(where, workspace))
 
 
 # --------------------------------------------------------- dense product --
@@ -616,7 +620,7 @@ def moe_fp8_linear(x_q, x_s, w, w_s, out, bias=None, residual=None, act=MOE_ACT_
         _need(residual.shape[0] == M, where, "residual and x_q disagree on M")
     _launch(where, stream, (x_q, x_s, w, w_s, out, bias, residual, workspace), x_q.data_ptr(),
             x_s.data_ptr(), w.data_ptr(), w_s.data_ptr(), None if bias is None else bias.data_ptr(), rp,
-            ld_res, M, N, K, act, op, ld_out, *_ws(workspace))
+            ld_res, M, N, K, act, op, ld_out, *_ws(where, workspace))
 
 
 def moe_status_str(status):

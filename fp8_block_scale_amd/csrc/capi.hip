@@ -1049,7 +1049,7 @@ moe_status run_group(moe::GroupMmArgs &g, int32_t dtype, void *workspace, size_t
         return fail(MOE_ERR_ALIGN, "the plan must be 4-byte aligned");
     if (g.out == g.x || g.out == g.dy || g.out == g.w)
         return fail(MOE_ERR_SHAPE, "the output is one of the inputs");
-    const size_t need = moe::group_mm_workspace(g, nullptr);
+    const size_t need = moe::group_mm_workspace(g, workspace);
     if (need > 0) {
         if (!workspace) return fail(MOE_ERR_NULL, "workspace is required");
         if (((uintptr_t)workspace & 255u) != 0)
@@ -1057,7 +1057,6 @@ moe_status run_group(moe::GroupMmArgs &g, int32_t dtype, void *workspace, size_t
         if (workspace_bytes < need)
             return fail(MOE_ERR_CAPACITY, "workspace %zu bytes < required %zu", workspace_bytes, need);
     }
-    moe::group_mm_workspace(g, workspace);
     return hip_check(moe::launch_group_mm(g, (hipStream_t)stream), what);
 }
 
@@ -1227,7 +1226,7 @@ MOE_API moe_status moe_fp8_linear(const uint8_t *x_q, const float *x_s, const ui
         return fail(MOE_ERR_ALIGN, "residual and out must be 2-byte aligned");
     if (out_bf16 == x_q || out_bf16 == w)
         return fail(MOE_ERR_SHAPE, "out is one of the operands");
-    const size_t need = moe::linear_workspace(a, nullptr);
+    const size_t need = moe::linear_workspace(a, workspace);
     if (need > 0) {
         if (!workspace) return fail(MOE_ERR_NULL, "workspace is required");
         if (((uintptr_t)workspace & 255u) != 0)
@@ -1235,7 +1234,6 @@ MOE_API moe_status moe_fp8_linear(const uint8_t *x_q, const float *x_s, const ui
         if (workspace_bytes < need)
             return fail(MOE_ERR_CAPACITY, "workspace %zu bytes < required %zu", workspace_bytes, need);
     }
-    moe::linear_workspace(a, workspace);
     a.xq = x_q;
     a.xs = x_s;
     a.w = w;

@@ -170,6 +170,7 @@ def test_binding_refusals():
     assert "int32" in _refused(f, x, w, _plan()[0].long(), *_plan()[1:], 2, 16, y)
     assert "shorter" in _refused(f, x, w, *_plan(128, 7), 2, 16, y)
     assert "overlap" in _refused(f, x[:1].expand(4, 64), w, *_plan(), 2, 16, y)
+    assert "contiguous" in _refused(f, x, w, *_plan(), 2, 16, y, torch.zeros(4096, dtype=torch.uint8)[::2])
     g = moe.moe_group_mm_dw
     assert "dw must be" in _refused(g, y, x, *_plan(), 2, 16, w.to(hf))
     assert "x must be" in _refused(g, y, x.float(), *_plan(), 2, 16, w)
