@@ -174,6 +174,23 @@ group_prep_kernel(GroupMmArgs g, int tile_rows) {
 
 // ------------------------------------------------------------- tile kernel
 
+// The routes of an item's rows (forward, dx) stay in LDS from the step that
+// sets its copies up to the one that stores its tile, in a ring of slots.
+// Steps count the stages multiplied, k per item, with the copies S - 1 ahead:
+// item i's routes are written in step i k - S, before that step's barrier
+// (right after the copies of item i - 1's last stage), and read by its
+// epilogue in step (i + 1) k - 1, after that step's barrier.  The item that
+// takes the slot over may be written two steps after that and no sooner: only
+// then is the next step's barrier between a slow wave's read and a fast wave's
+// write.  A contraction of one stage needs S + 2 slots, longer ones fewer.
+constexpr bool route_ring_holds(int slots, int S) {
+    for (int k = 1; k <= S + 2; ++k) {
+        const int read = k - 1, overwritten = slots * k - S;         // of item 0's slot
+        if (overwritten < read + 2) return false;
+    }
+    return true;
+}
+
 // Columns of MFMA tile pair t: row i of tile 2 t + h is column
 // 32 t + 8 (i / 4) + 4 h + i % 4, so that a lane's results of the pair
 // (rows 4 (l / 16) + v of either) are 8 consecutive columns.
@@ -187,9 +204,11 @@ struct Tile {
     static constexpr int JQ = (QB / 1024 + NW - 1) / NW;
     static constexpr int Ahead = (S - 2) * (JP + QB / 1024 / NW);   // copies that may be in flight
     static constexpr int NP = TP / WP / 16, NQ = TQ / WQ / 16;
-    // behind the stages: the routes of an item's rows (forward, dx; a ring of
-    // S items), or the routes of a stage's rows (two) and the list of parts (dw)
-    static constexpr int Tail = QKS ? 2 * 256 : S * TQ * 4;
+    // behind the stages: the ring of the routes of items' rows (forward, dx),
+    // or the routes of a stage's rows (two) and the list of parts (dw)
+    static constexpr int Ring = S + 2;
+    static_assert(route_ring_holds(Ring, S), "a slot is overwritten before its item is stored");
+    static constexpr int Tail = QKS ? 2 * 256 : Ring * TQ * 4;
     static constexpr size_t Smem = (size_t)S * Stage + Tail;
     static_assert(NP % 2 == 0 && JP >= 1 && NW % 2 == 0 && Smem <= 160 * 1024, "tile");
     static_assert(!QKS || (TP == TQ && NQ % 2 == 0 && S == 2), "dw tile");
@@ -210,7 +229,7 @@ group_tile_kernel(GroupMmArgs g) {
     constexpr int NW = T::NW, JP = T::JP, JQ = T::JQ, NP = T::NP, NQ = T::NQ;
     constexpr bool DW = OP == kGmmDw;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    int *rids = reinterpret_cast<int *>(smem + (size_t)S * T::Stage);          // [S][TQ] (forward, dx)
+    int *rids = reinterpret_cast<int *>(smem + (size_t)S * T::Stage);          // [Ring][TQ] (forward, dx)
     int *sids = rids;                                                          // [2][64] (dw)
     int4 *parts = reinterpret_cast<int4 *>(smem + (size_t)S * T::Stage + 512); // [max_tiles] (dw)
 
@@ -309,7 +328,7 @@ group_tile_kernel(GroupMmArgs g) {
             const int row = 8 * (j * NW + w) + lrow;
             int r = row < ld.rows ? g.sorted[ld.row0 + row] : -1;
             if (r >= g.R) r = -1;
-            if (row < TQ && (l & 7) == 0) rids[(lord % S) * TQ + row] = r;
+            if (row < TQ && (l & 7) == 0) rids[(lord % T::Ring) * TQ + row] = r;
             const int64_t xr = OP == kGmmFwd && !g.per_route ? g.token_of(r) : r;
             qptr[j] = r < 0 ? nullptr : reinterpret_cast<const uint8_t *>(src + xr * ldq) + kc_q * 16;
         }
@@ -479,7 +498,7 @@ group_tile_kernel(GroupMmArgs g) {
                     }
                 }
             } else {
-                const int r = rids[(ord % S) * TQ + q];
+                const int r = rids[(ord % T::Ring) * TQ + q];
                 if (r < 0) continue;
                 if (OP == kGmmDx && !g.per_route) {
                     if (it.ct == 0 && wp == 0 && grp == 0) g.rpos[r] = 0;

@@ -198,6 +198,62 @@ def test_ranges(M, E, K, N, k, bm, dt):
     check_all(Problem(dt, M, E, K, N, k, bm))
 
 
+# Contractions of one, two and more stages of 64 with many items a workgroup,
+# in each row-tile form (by the rule on sizes: 256, 128, 64 or 32 rows, 6 to
+# 12 items on each of 256 workgroups): (op, rows of the form, M, E, the
+# contraction's sizes, output columns).  The forward takes 32 rows only above
+# one stage.
+MANY = [("fwd", 256, 35496, 256, (8, 64, 72, 128), 520), ("fwd", 256, 35496, 64, (200,), 1032),
+        ("fwd", 128, 28397, 1024, (8, 64), 520), ("fwd", 128, 14540, 512, (72, 128), 1032),
+        ("fwd", 128, 35496, 256, (200,), 520),
+        ("fwd", 64, 4765, 256, (8, 64), 2056), ("fwd", 64, 1562, 128, (72, 128), 4104),
+        ("fwd", 64, 3812, 256, (200,), 2056),
+        ("fwd", 32, 2440, 256, (72,), 2056), ("fwd", 32, 1250, 128, (128,), 4104),
+        ("fwd", 32, 1562, 256, (200,), 2056),
+        ("dx", 256, 35496, 256, (8, 64, 72, 128), 520), ("dx", 256, 35496, 64, (200,), 1032),
+        ("dx", 128, 28397, 1024, (8, 64), 520), ("dx", 128, 14540, 512, (72, 128), 1032),
+        ("dx", 128, 35496, 256, (200,), 520),
+        ("dx", 64, 5956, 512, (8, 64), 1032), ("dx", 64, 1562, 128, (72, 128), 4104),
+        ("dx", 64, 3812, 256, (200,), 2056),
+        ("dx", 32, 1000, 1024, (8, 64, 72, 128, 200), 520)]
+
+
+@pytest.mark.parametrize("op,rows,M,E,red,cols",
+                         [(op, rows, M, E, c, n) for op, rows, M, E, cs, n in MANY for c in cs])
+@pytest.mark.parametrize("per_route", [False, True])
+def test_many_items_and_few_stages(op, rows, M, E, red, cols, per_route):
+    """Each tile is stored to its own rows while the routes of the items after
+    it are fetched; twice, with the same bits."""
+    K, N = (red, cols) if op == "fwd" else (cols, red)
+    p = Problem(HF if E == 256 else BF, M, E, K, N, 2, 8, per_route)
+    valid = p.valid()
+    call, (v, s, n) = (p.y, p.ref_y()) if op == "fwd" else (p.dx, p.ref_dx())
+    got = call()
+    if op == "fwd" or per_route:
+        check(got[valid], (v[valid], s[valid], n), p.dt)
+        assert (got[~valid] == 3.0).all(), "rows of masked routes changed"
+    else:
+        check(got, (v, s, n), p.dt)
+    assert torch.equal(got, call())
+
+
+@pytest.mark.parametrize("K", [8, 64])
+def test_one_stage_forward_with_a_long_plan_buffer(K):
+    """A plan buffer of more blocks than a grid takes goes to the row tiles
+    (32 rows) at any size; blocks past the plan's length are never read."""
+    p = Problem(BF, 1000, 1024, K, 520, 2, 8)
+    srt, eid, ntp = p.plan
+    blocks = 65536 + 8
+    p.plan = (torch.cat([srt, torch.full((blocks * 8 - srt.numel(),), -9, dtype=torch.int32, device=DEV)]),
+              torch.cat([eid, torch.full((blocks - eid.numel(),), 1 << 30, dtype=torch.int32, device=DEV)]), ntp)
+    valid = p.valid()
+    v, s, n = p.ref_y()
+    got = p.y()
+    check(got[valid], (v[valid], s[valid], n), BF)
+    assert (got[~valid] == 3.0).all()
+    assert torch.equal(got, p.y())
+
+
 def test_no_tokens():
     p = Problem(BF, 4, 3, 64, 32, 2, 16)
     e = torch.empty((0, 64), dtype=BF, device=DEV)
