@@ -1075,7 +1075,8 @@ MOE_API size_t moe_group_mm_workspace_size(int32_t op, int64_t M, int64_t K, int
         fail(MOE_ERR_SHAPE, "unknown op %d", op);
         return 0;
     }
-    if (check_group_shape(M, K, N, E, top_k, block_m, sorted_cap) != MOE_OK || M == 0) return 0;
+    if (check_group_shape(M, K, N, E, top_k, block_m, sorted_cap) != MOE_OK || M == 0 || sorted_cap == 0)
+        return 0;
     moe::GroupMmArgs g = group_args(op, MOE_DT_BF16, nullptr, nullptr, nullptr, M, K, N, E, top_k, block_m,
                                     sorted_cap, x_per_route);
     return moe::group_mm_workspace(g, nullptr);
@@ -1115,17 +1116,21 @@ MOE_API moe_status moe_group_mm_dx(const void *dy, int64_t ld_dy, const void *w,
     if (st == MOE_OK) st = check_dtype(dtype);
     if (st != MOE_OK) return st;
     if (M == 0 || (sorted_cap == 0 && x_per_route)) return MOE_OK;
-    if ((st = check_rows("dy", dy, ld_dy, N)) != MOE_OK) return st;
-    if ((st = check_rows("w", w, K, K)) != MOE_OK) return st;
-    if ((st = check_rows("dx", dx, ld_dx, K)) != MOE_OK) return st;
     moe::GroupMmArgs g = group_args(moe::kGmmDx, dtype, sorted_token_ids, expert_ids,
                                     num_tokens_post_padded, M, K, N, E, top_k, block_m, sorted_cap,
                                     x_per_route);
+    g.out = dx;
+    g.ld_out = ld_dx;
+    if (sorted_cap == 0) {                           // no routes: dx = 0
+        if ((st = check_rows("dx", dx, ld_dx, K)) != MOE_OK) return st;
+        return hip_check(moe::launch_group_no_routes(g, (hipStream_t)stream), "moe_group_mm_dx: clear dx");
+    }
+    if ((st = check_rows("dy", dy, ld_dy, N)) != MOE_OK) return st;
+    if ((st = check_rows("w", w, K, K)) != MOE_OK) return st;
+    if ((st = check_rows("dx", dx, ld_dx, K)) != MOE_OK) return st;
     g.dy = (const uint16_t *)dy;
     g.w = (const uint16_t *)w;
-    g.out = dx;
     g.ld_dy = ld_dy;
-    g.ld_out = ld_dx;
     return run_group(g, dtype, workspace, workspace_bytes, stream, "moe_group_mm_dx: launch");
 }
 

@@ -45,5 +45,7 @@ struct GroupMmArgs {
 // Lays the workspace out at ws (NULL: sizes only) and returns its bytes.
 size_t group_mm_workspace(GroupMmArgs &g, void *ws);
 hipError_t launch_group_mm(const GroupMmArgs &g, hipStream_t st);
+// dx of tokens without a route (M, K, out and ld_out are read): zeros.
+hipError_t launch_group_no_routes(GroupMmArgs g, hipStream_t st);
 
 }  // namespace moe

@@ -876,6 +876,16 @@ hipError_t launch_rows(const GroupMmArgs &g, hipStream_t st) {
 }
 
 template <bool F16>
+hipError_t launch_sum(const GroupMmArgs &g, hipStream_t st) {
+    int lanes = 256;                                   // threads of a token: K / 8, up to a power of two
+    while (lanes > 1 && lanes / 2 >= g.K / 8) lanes /= 2;
+    const int64_t tokens = 256 / lanes;
+    const int64_t blocks = (g.M + tokens - 1) / tokens * ((g.K / 8 + lanes - 1) / lanes);
+    group_sum_kernel<F16><<<(unsigned)std::min(blocks, (int64_t)1 << 23), 256, 0, st>>>(g, lanes, blocks);
+    return hipGetLastError();
+}
+
+template <bool F16>
 hipError_t launch(const GroupMmArgs &g, hipStream_t st) {
     if (g.stream) {
         const dim3 grid((g.N + 15) / 16, (unsigned)(g.sorted_cap / g.block_m));
@@ -901,18 +911,18 @@ hipError_t launch(const GroupMmArgs &g, hipStream_t st) {
     }
     e = g.op == kGmmFwd ? launch_rows<F16, kGmmFwd>(g, st) : launch_rows<F16, kGmmDx>(g, st);
     if (e != hipSuccess || !summed) return e;
-    int lanes = 256;                                   // threads of a token: K / 8, up to a power of two
-    while (lanes > 1 && lanes / 2 >= g.K / 8) lanes /= 2;
-    const int64_t tokens = 256 / lanes;
-    const int64_t blocks = (g.M + tokens - 1) / tokens * ((g.K / 8 + lanes - 1) / lanes);
-    group_sum_kernel<F16><<<(unsigned)std::min(blocks, (int64_t)1 << 23), 256, 0, st>>>(g, lanes, blocks);
-    return hipGetLastError();
+    return launch_sum<F16>(g, st);
 }
 
 }  // namespace
 
 hipError_t launch_group_mm(const GroupMmArgs &g, hipStream_t st) {
     return g.f16 ? launch<true>(g, st) : launch<false>(g, st);
+}
+
+hipError_t launch_group_no_routes(GroupMmArgs g, hipStream_t st) {
+    g.top_k = 0;                                       // sums of nothing
+    return launch_sum<false>(g, st);
 }
 
 size_t group_mm_workspace(GroupMmArgs &g, void *ws) {

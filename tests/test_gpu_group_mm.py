@@ -270,6 +270,31 @@ def test_no_tokens():
         assert (dw == 0).all()
 
 
+@pytest.mark.parametrize("M,K", [(5, 64), (1, 8), (700, 2056)])
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_tokens_and_an_empty_plan(M, K, dt):
+    """Plan buffers of length 0 (whose pointers are NULL): every route is
+    masked, so y and dx rows of routes stay, dx of the tokens and dw are 0."""
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    plan = none, none, torch.zeros(1, dtype=torch.int32, device=DEV)
+    w = torch.randn((3, 32, K), device=DEV).to(dt)
+    x, dy = torch.randn((M, K), device=DEV).to(dt), torch.randn((2 * M, 32), device=DEV).to(dt)
+    y = torch.full((2 * M, 32), 3.0, dtype=dt, device=DEV)
+    moe.moe_group_mm(x, w, *plan, 2, 16, y)
+    assert (y == 3.0).all()
+    dx = torch.full((2 * M, K), 3.0, dtype=dt, device=DEV)
+    moe.moe_group_mm_dx(dy, w, *plan, 2, 16, dx)
+    assert (dx == 3.0).all()
+    wide = torch.full((M, K + 8), 3.0, dtype=dt, device=DEV)
+    moe.moe_group_mm_dx(dy, w, *plan, 2, 16, wide[:, :K])
+    assert not wide[:, :K].view(torch.int16).any() and (wide[:, K:] == 3.0).all()
+    dw = torch.full((3, 32, K), 3.0, dtype=dt, device=DEV)
+    moe.moe_group_mm_dw(dy, x, *plan, 2, 16, dw, accumulate=True)
+    assert (dw == 3.0).all()
+    moe.moe_group_mm_dw(dy, x, *plan, 2, 16, dw)
+    assert not dw.view(torch.int16).any()
+
+
 @pytest.mark.parametrize("dt", [BF, HF, F32])
 def test_accumulate(dt):
     p = Problem(HF if dt == HF else BF, 210, 5, 136, 72, 2, 16)

@@ -107,6 +107,20 @@ def test_group_types_and_workspace():
     assert _dx(sc=0, x=None) == "MOE_ERR_NULL"
 
 
+def test_group_empty_plan():
+    """A plan without routes needs neither its pointers nor a workspace; dx of
+    the tokens is written, so its rows are checked."""
+    none = dict(sc=0, s=None, e=None, n=None, ws=None, wsb=0)
+    for op in range(3):
+        assert moe.moe_group_mm_workspace_size(op, 4, 64, 32, 8, 2, 16, 0) == 0
+    assert _fwd(**none) == "MOE_OK"
+    assert _dx(pr=1, ldx=64, **none) == "MOE_OK"
+    assert _dw(acc=1, **none) == "MOE_OK"
+    assert _dx(x=None, **none) == "MOE_ERR_NULL"
+    assert _dx(x=ctypes.c_void_p(0x10008), **none) == "MOE_ERR_ALIGN"
+    assert _dx(ldx=56, **none) == "MOE_ERR_SHAPE"
+
+
 LIN = dict(M=4, N=96, K=256, act=0, xq=FAKE, xs=FAKE, w=FAKE, ws=FAKE, b=FAKE, r=None, ldr=0, out=FAKE3,
            ldo=96, wk=FAKE, wkb=BIG)
 
