@@ -81,11 +81,12 @@ __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 
 
 // Workgroup 0 finds every expert's rows in the plan (its sentinels are all at
 // the end of its last block) and cuts them into row tiles of tile_rows, listed
-// as {first row, rows, expert, slot} with their count in meta[0].  For dw an expert without rows has one empty tile, the
-// tiles of an expert with several have slots one after the other (else -1),
-// and those experts, meta[1] of them, are listed as joins = {expert, first
-// slot, slots}.  The other workgroups set rpos[0, R) = -1 for the sum over a
-// token's routes.
+// as {first row, rows, expert, slot} with their count in meta[0].  For dw an
+// expert without rows has one empty tile (none if dw is added to: it stays as
+// it is), the tiles of an expert with several have slots one after the other
+// (else -1), and those experts, meta[1] of them, are listed as joins =
+// {expert, first slot, slots}.  The other workgroups set rpos[0, R) = -1 for
+// the sum over a token's routes.
 constexpr int kPrepThreads = 1024;
 
 __global__ void __launch_bounds__(kPrepThreads)
@@ -127,7 +128,7 @@ group_prep_kernel(GroupMmArgs g, int tile_rows) {
         rows = (last[tid] - 1 - first[tid]) * bm + pos + more;
     }
     int cnt = rows / tile_rows + (rows % tile_rows != 0);
-    if (g.op == kGmmDw && tid < g.E && cnt == 0) cnt = 1;
+    if (g.op == kGmmDw && !g.accumulate && tid < g.E && cnt == 0) cnt = 1;
     const int waves = (g.E + 63) >> 6;          // with experts (the others add nothing)
     auto scan = [&](int v) {                    // inclusive sum over the threads
         for (int d = 1; d < 64; d <<= 1) {

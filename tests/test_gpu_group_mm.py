@@ -304,6 +304,23 @@ def test_accumulate(dt):
     check(got, (v + before.double(), s + before.double().abs(), n + 1), dt)
 
 
+@pytest.mark.parametrize("M,E,K,N,bm", [(210, 5, 136, 72, 16), (9000, 3, 264, 264, 64), (2100, 190, 152, 240, 16)])
+@pytest.mark.parametrize("dt", [BF, HF, F32])
+def test_accumulate_leaves_experts_without_routes(M, E, K, N, bm, dt):
+    """Their dw is not rewritten: negative zeros and the bits of a NaN stay."""
+    p = Problem(HF if dt == HF else BF, M, E, K, N, 2, bm)
+    p.ids[(p.ids == 0) | (p.ids == E - 1)] = 1
+    p.plan = make_plan(p.ids, E, bm)
+    dw = torch.zeros((E, N, K), dtype=dt, device=DEV)
+    bits = dw.view(torch.int32 if dt == F32 else torch.int16)
+    bits[0] = torch.iinfo(bits.dtype).min                             # -0
+    bits[E - 1] = {BF: 0x7F81, HF: 0x7C01, F32: 0x7F800001}[dt]       # a signalling NaN
+    before = bits.clone()
+    p.dw(dt, dw, accumulate=True)
+    assert torch.equal(bits[0], before[0]) and torch.equal(bits[E - 1], before[E - 1])
+    check(dw[1:E - 1], tuple(t[1:E - 1] for t in p.ref_dw()[:2]) + (2 * M,), dt)
+
+
 @pytest.mark.parametrize("M,K,N", [(40, 72, 40), (1, 520, 136), (700, 328, 264)])
 def test_strides_and_neighbours(M, K, N):
     """Operands inside larger buffers whose other values are NaN: none enters
