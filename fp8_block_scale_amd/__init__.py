@@ -490,17 +490,20 @@ def _rows_arg(where, name, t, dtype, cols):
 
 
 def _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m):
+    """The plan's pointers and the length that the kernels may trust."""
     for t in (sorted_token_ids, expert_ids, num_tokens_post_padded):
         _need(t.dtype == torch.int32 and t.is_contiguous(), where, "the plan must be contiguous int32")
     _need(num_tokens_post_padded.numel() >= 1, where, "num_tokens_post_padded is empty")
     _need(top_k >= 1 and R % top_k == 0, where, "the routes are no multiple of top_k")
-    # blocks past the plan's length are never read: P / block_m is at most
-    # sorted_cap / block_m, and at most the capacity that any routing needs
-    if block_m > 0:
-        need = min(sorted_token_ids.numel() // block_m,
-                   -(-(R + min(E, R) * (block_m - 1)) // block_m))
+    # A block's expert is read wherever the device's plan length says there is
+    # one, within sorted_cap: so that is cut to the blocks that expert_ids has.
+    # No plan is longer than any routing of these routes needs.
+    cap = sorted_token_ids.numel()
+    if block_m > 0 and cap % block_m == 0:
+        need = min(cap // block_m, -(-(R + min(E, R) * (block_m - 1)) // block_m))
         _need(expert_ids.numel() >= need, where, "expert_ids shorter than the plan can need")
-    return sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr()
+        cap = min(cap, expert_ids.numel() * block_m)
+    return (sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr()), cap
 
 
 def _x_rows(where, name, t, R, top_k, per_route):
@@ -539,11 +542,11 @@ def moe_group_mm(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, top
     xp, ld_x = _rows_arg(where, "x", x, w.dtype, K)
     yp, ld_y = _rows_arg(where, "out", out, w.dtype, N)
     R = out.shape[0]
-    plan = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
+    plan, cap = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
     per_route = _x_rows(where, "x", x, R, top_k, x_per_route)
     _launch(where, stream, (x, w, out, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace),
             xp, ld_x, per_route, w.data_ptr(), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
-            sorted_token_ids.numel(), yp, ld_y, *_ws(where, workspace))
+            cap, yp, ld_y, *_ws(where, workspace))
 
 
 def moe_group_mm_dx(dy, w, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, dx,
@@ -558,11 +561,11 @@ def moe_group_mm_dx(dy, w, sorted_token_ids, expert_ids, num_tokens_post_padded,
     yp, ld_y = _rows_arg(where, "dy", dy, w.dtype, N)
     xp, ld_x = _rows_arg(where, "dx", dx, w.dtype, K)
     R = dy.shape[0]
-    plan = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
+    plan, cap = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
     per_route = _x_rows(where, "dx", dx, R, top_k, x_per_route)
     _launch(where, stream, (dy, w, dx, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace),
             yp, ld_y, w.data_ptr(), _DT[w.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
-            sorted_token_ids.numel(), xp, ld_x, per_route, *_ws(where, workspace))
+            cap, xp, ld_x, per_route, *_ws(where, workspace))
 
 
 def moe_group_mm_dw(dy, x, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m, dw,
@@ -578,11 +581,11 @@ def moe_group_mm_dw(dy, x, sorted_token_ids, expert_ids, num_tokens_post_padded,
     yp, ld_y = _rows_arg(where, "dy", dy, dy.dtype, N)
     xp, ld_x = _rows_arg(where, "x", x, dy.dtype, K)
     R = dy.shape[0]
-    plan = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
+    plan, cap = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
     per_route = _x_rows(where, "x", x, R, top_k, x_per_route)
     _launch(where, stream, (dy, x, dw, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace),
             yp, ld_y, xp, ld_x, per_route, _DT[dy.dtype], *plan, R // top_k, K, N, E, top_k, block_m,
-            sorted_token_ids.numel(), dw.data_ptr(), _DT[dw.dtype], int(bool(accumulate)),
+            cap, dw.data_ptr(), _DT[dw.dtype], int(bool(accumulate)),
             *_ws(where, workspace))
 
 

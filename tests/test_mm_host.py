@@ -169,6 +169,23 @@ def _refused(f, *a, **kw):
     return str(ei.value)
 
 
+@pytest.mark.parametrize("rows,blocks,want", [(128, 8, 128), (128, 9, 128), (256, 8, 128), (512, 11, 176)])
+def test_binding_plan_length(monkeypatch, rows, blocks, want):
+    """The kernels read a block's expert wherever the plan's length on the
+    device says there is a block: the binding lets them go no further than
+    expert_ids reaches, however long sorted_token_ids is."""
+    seen = {}
+    monkeypatch.setattr(moe, "_launch", lambda where, stream, tensors, *args: seen.update({where: args}))
+    bf = torch.bfloat16
+    x, w, y = torch.zeros(4, 64, dtype=bf), torch.zeros(8, 32, 64, dtype=bf), torch.zeros(8, 32, dtype=bf)
+    plan = _plan(rows, blocks)
+    moe.moe_group_mm(x, w, *plan, 2, 16, y)
+    moe.moe_group_mm_dx(y, w, *plan, 2, 16, x)
+    moe.moe_group_mm_dw(y, x, *plan, 2, 16, w)
+    for where, at in (("moe_group_mm", 14), ("moe_group_mm_dx", 13), ("moe_group_mm_dw", 15)):
+        assert seen[where][at - 1] == 16 and seen[where][at] == want, where
+
+
 def test_binding_refusals():
     bf, hf = torch.bfloat16, torch.float16
     x, w, y = torch.zeros(4, 64, dtype=bf), torch.zeros(8, 32, 64, dtype=bf), torch.zeros(8, 32, dtype=bf)
