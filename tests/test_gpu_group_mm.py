@@ -403,6 +403,33 @@ def test_dw_of_a_crowded_expert(M, E, K, N, k, bm, dt, accumulate):
         assert torch.equal(got, p.dw(out, before.clone(), accumulate))
 
 
+@pytest.mark.parametrize("M,E,K,N,k,bm,crowd", [
+    (70001, 3, 8, 16, 1, 16, 0), (9000, 2, 264, 264, 2, 128, 0), (33000, 1, 264, 136, 1, 32, 0),   # cut, 128 squared
+    (2100, 190, 152, 240, 2, 16, 0.6), (5000, 40, 264, 520, 1, 32, 0.3), (60000, 9, 136, 200, 2, 64, 0.5),
+    (16384, 1, 1032, 2056, 1, 64, 0), (9000, 33, 1032, 1032, 1, 16, 0.4),                          # cut, 256 squared
+    (700, 190, 264, 520, 2, 8, 0), (1500, 33, 1032, 1032, 1, 8, 0), (3000, 33, 1032, 1032, 1, 16, 0),
+    (20000, 190, 264, 520, 2, 8, 0), (9000, 40, 1032, 2056, 2, 16, 0.2)])                          # many items
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_dw_of_whole_numbers(M, E, K, N, k, bm, crowd, dt):
+    """Every route counts, at any number of rows: with |x| <= 1 and |dy| <= 2
+    each sum of at most 2^17 routes is a whole number below 2^24, exact in
+    FP32 in any order, so dw equals the sum in 64 bits, rounded once.  A share
+    `crowd` of the routes goes to one expert."""
+    p = Problem(dt, M, E, K, N, k, bm)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M + E)
+    p.ids[torch.rand((M, k), generator=g, device=DEV) < crowd] = E - 1
+    p.plan = make_plan(p.ids, E, bm)
+    draw = lambda shape, n: torch.randint(-n, n + 1, shape, generator=g, device=DEV)
+    p.x, p.dy = draw(p.x.shape, 1).to(dt), draw(p.dy.shape, 2).to(dt)
+    assert p.R <= 1 << 17
+    v = p.ref_dw()[0]
+    before = draw(v.shape, 100)
+    for out in (F32, dt):
+        assert torch.equal(p.dw(out), v.to(out))
+        assert torch.equal(p.dw(out, before.to(out), accumulate=True), (v + before).to(out))
+
+
 @pytest.mark.parametrize("M", [9, 700])
 def test_subnormals(M):
     """FP16 subnormals (here the multiples of 2^-24 up to 2^-14) are values
