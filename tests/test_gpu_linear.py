@@ -136,6 +136,44 @@ def test_larger(M, N, K, act):
     check(p(), p.ref())
 
 
+WHOLE = [(1, 257, 1024), (3, 1000, 128), (16, 520, 640), (40, 1001, 2048), (100, 520, 4096),     # few rows
+         (700, 1024, 4096), (1000, 1001, 2048),                                                    # 64 rows, K split
+         (9000, 4097, 128), (5000, 4096, 2048),                                                    # 128 rows
+         (9000, 1030, 256), (30000, 4096, 128), (30000, 4100, 256), (20000, 1030, 512)]            # 256 rows
+
+
+@pytest.mark.parametrize("M,N,K", WHOLE)
+@pytest.mark.parametrize("extras", [False, True])
+def test_whole_numbers(M, N, K, extras):
+    """Codes of whole numbers up to 2, scales 1/2, 1 and 2: every product is a
+    multiple of 1/4 of at most 16, the sums of up to 4096 of them are below
+    2^24 quarters, and a block's products lie within 4 bits: all exact, with a
+    bias and a residual too, so the output equals the value in 64 bits, rounded
+    once."""
+    p = Problem(M, N, K, "none", bias=extras, residual=extras)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M + N)
+    draw = lambda shape, n: torch.randint(-n, n + 1, shape, generator=g, device=DEV).float()
+    code = lambda shape: draw(shape, 2).to(torch.float8_e4m3fn).view(torch.uint8)
+    p.xq, p.w = code((M, K)), code((N, K))
+    p.xs, p.ws = torch.exp2(draw(p.xs.shape, 1)), torch.exp2(draw(p.ws.shape, 1))
+    if extras:
+        p.bias, p.res = draw((N,), 50) / 4, (draw((M, N), 50) / 2).to(BF)
+    z = p.ref()[0]
+    assert torch.equal(p(), z.to(BF))
+
+
+@pytest.mark.parametrize("M,N,K", [(30000, 264, 128), (50000, 300, 384), (20000, 1030, 512), (30000, 4096, 128),
+                                   (30000, 4100, 256)])
+def test_many_items(M, N, K):
+    """SwiGLU with several tiles of few stages on each workgroup, in every row
+    tile form; the same bits twice."""
+    p = Problem(M, N, K, "swiglu")
+    got = p()
+    check(got, p.ref())
+    assert torch.equal(got, p())
+
+
 def test_no_rows():
     p = Problem(0, 64, 256)
     p()
