@@ -174,6 +174,18 @@ def test_many_items(M, N, K):
     assert torch.equal(got, p())
 
 
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("M,N,K", [(3, 520, 1024), (40, 1002, 2048), (700, 1024, 4096), (5000, 1030, 512),
+                                   (9000, 1030, 256)])
+def test_before_rounding(M, N, K, act):
+    """The value before its rounding to BF16: a residual of minus the rounded
+    result leaves the low bits, to the tolerance without the result's own
+    2^-8."""
+    p = Problem(M, N, K, act, residual=False)
+    p.res = -p.ref()[0].to(BF)
+    check(p(), p.ref(), norm=False)
+
+
 def test_no_rows():
     p = Problem(0, 64, 256)
     p()
