@@ -1,5 +1,6 @@
 // C ABI of libmoe_fp8.so: argument validation, workspace layout and the
 // launch sequence of each entry point (declared in include/moe_fp8.h).
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <hip/hip_runtime.h>
@@ -998,11 +999,16 @@ moe_status check_group_shape(int64_t M, int64_t K, int64_t N, int32_t E, int32_t
     constexpr int64_t kMaxRows = ((int64_t)1 << 31) - 1024;
     if (M > kMaxRows / top_k || sorted_cap > kMaxRows)
         return fail(MOE_ERR_SHAPE, "M * top_k and sorted_cap must not exceed 2^31 - 1024");
-    // the kernels number their output tiles (at least 32 routes x 128 columns,
-    // 128 x 128 of a weight) in int32
-    const int64_t n = (N + 127) / 128, k = (K + 127) / 128, rows = M * top_k / 32 + E;
-    if (rows * (n > k ? n : k) >= (int64_t)1 << 31 || E * n * k >= (int64_t)1 << 31)
-        return fail(MOE_ERR_UNSUPPORTED, "more than 2^31 output tiles");
+    // The kernels number their output tiles in int32: of 32 or more routes x
+    // 256 columns (forward, dx), of 128 x 128 or more of a weight (dw; the
+    // parts of cut experts add at most 1024 tiles or 2^26 values, which are
+    // at most 2^20 tiles as N and K are at least 8).  The walk over them may
+    // step past the last by the grid.
+    const int64_t c = (std::max(N, K) + 255) / 256, rows = M * top_k / 32 + E;
+    const int64_t weight = (int64_t)E * ((N + 127) / 128) * ((K + 127) / 128);
+    constexpr int64_t kMaxTiles = ((int64_t)1 << 31) - ((int64_t)1 << 21);
+    if (rows * c >= kMaxTiles || weight >= kMaxTiles)
+        return fail(MOE_ERR_UNSUPPORTED, "more output tiles than int32 counts");
     return MOE_OK;
 }
 

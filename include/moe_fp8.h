@@ -466,7 +466,8 @@ moe_status moe_w4a8_experts(const uint8_t *x_q, const float *x_s,
  * calls on one stream may share it, calls that overlap may not.
  * Errors: MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_CAPACITY
  * (workspace), MOE_ERR_UNSUPPORTED (E, block_m, K or N out of range, or more
- * than 2^31 output tiles), MOE_ERR_HIP. */
+ * output tiles than int32 counts: of 32 routes x 256 columns, of 128 x 128
+ * values of the weights), MOE_ERR_HIP. */
 enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 };
 enum { MOE_GMM_FWD = 0, MOE_GMM_DX = 1, MOE_GMM_DW = 2 };
 

@@ -79,6 +79,21 @@ def test_group_refusals(f):
         assert f(**{n: ctypes.c_void_p(0x10002)}) == "MOE_ERR_ALIGN"
 
 
+def test_group_tile_limit():
+    """Tiles of 32 routes x 256 columns and of 128 x 128 of a weight, below
+    2^31 - 2^21 of either: the size query tells by the status it leaves."""
+    def size(M, E, K, N):
+        moe.moe_group_mm_workspace_size(9, 1, 8, 8, 1, 1, 8, 8)          # leaves another message
+        moe.moe_group_mm_workspace_size(moe.MOE_GMM_DX, M, K, N, E, 1, 8, 8)
+        return "output tiles" in moe.moe_last_error()
+
+    cols = 1 << 20
+    rows = ((1 << 31) - (1 << 21)) // (cols // 256)                       # M / 32 + E of the first refusal
+    assert size(32 * (rows - 1), 1, cols, 8) and not size(32 * (rows - 2), 1, cols, 8)
+    assert size(32 * (rows - 1), 1, 8, cols) and not size(32 * (rows - 2), 1, 8, cols)
+    assert size(8, 32, cols, cols) and not size(8, 31, cols, cols)
+
+
 def test_group_output_is_no_input():
     assert _fwd(y=FAKE) == _fwd(y=FAKE2) == "MOE_ERR_SHAPE"
     assert _dx(x=FAKE3) == _dx(x=FAKE2) == "MOE_ERR_SHAPE"
