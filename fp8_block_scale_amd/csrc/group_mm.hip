@@ -23,17 +23,21 @@
 // few stages per tile).  Neighbouring items, which share rows or weights, run
 // on one XCD at the same time (panel_tile).
 //
-// What bounds it, measured.  Experts of a hundred rows and more: the matrix
-// cores' power.  E = 288, K = 4096, N = 2048, 8192 tokens of 8 routes in BF16
-// take 1.45 ms, 760 TFLOP/s of routes (the padding of each expert's last tile
-// comes on top), at 1.4 GHz on random values; on zeros the clock stays at 2.4
-// GHz.  Experts of some tens of rows: the weights (E = 512, K = 2048, N =
-// 1024, 40 routes an expert: 0.45 ms, 4.7 TB/s).  dx summed over a token's
-// routes adds the FP32 rows' way through memory (4096 tokens at the first
-// sizes: 1.25 ms, 440 TFLOP/s).  dw with a few stages per tile: the tile's
-// store, some 3.5 us, that the next tile's products do not cover (36 experts
-// of 227 rows: 0.26 ms for 0.6 GB out).  Small calls: the set-up launch (4 us)
-// and the latency of a tile's first copies.
+// What bounds it, measured (counters on random values, and on zeros, where the
+// clock is higher).  Experts of two hundred rows: neither side alone.  E =
+// 288, K = 4096, N = 2048, 8192 tokens of 8 routes in BF16 take 1.44 ms, 766
+// TFLOP/s of routes (the padding of each expert's last tile comes on top): the
+// matrix cores are busy 46% of the time at 1.7 GHz, HBM moves 6.1 GB at 4.1
+// TB/s and the waves wait 35% of their time for the two-stage ring; zeros, at
+// 2.3 GHz, are 11% faster.  Experts of some tens of rows: the weights (E =
+// 512, K = 2048, N = 1024, 40 routes an expert: 0.45 ms, 2.4 GB at 5.3 TB/s).
+// dx summed over a token's routes: HBM too, with the FP32 rows' way through
+// memory (4096 tokens at the first sizes: 1.25 ms, 440 TFLOP/s; the tile
+// kernel moves 6.5 GB at 5.7 TB/s, zeros are 1% faster).  dw with a few stages
+// per tile: the tile's store, some 3.5 us, that the next tile's products do
+// not cover as they wait for it (36 experts of 227 rows: 0.25 ms for 0.6 GB
+// out, matrix cores busy 25%).  Small calls: the set-up launch (4 us) and the
+// latency of a tile's first copies.
 #include <algorithm>
 #include <cmath>
 
