@@ -254,6 +254,21 @@ def test_one_stage_forward_with_a_long_plan_buffer(K):
     assert torch.equal(got, p.y())
 
 
+@pytest.mark.parametrize("K,N", [(1 << 20, 8), (8, 1 << 20), ((1 << 20) - 8, 24)])
+@pytest.mark.parametrize("M,k,bm", [(1, 1, 8), (5, 2, 16), (150, 2, 32)])
+def test_longest_contractions_and_rows(K, N, M, k, bm):
+    """K and N up to 2^20, on whole numbers of at most 1: sums of fewer than
+    2^24, so every result equals the value in 64 bits, rounded once."""
+    p = Problem(BF, M, 2, K, N, k, bm, routing="full")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    p.x, p.dy, p.w = (torch.randint(-1, 2, t.shape, generator=g, device=DEV, dtype=torch.int8).to(BF)
+                      for t in (p.x, p.dy, p.w))
+    assert torch.equal(p.y(), p.ref_y()[0].to(BF))
+    assert torch.equal(p.dx(), p.ref_dx()[0].to(BF))
+    assert torch.equal(p.dw(F32), p.ref_dw()[0].float())
+
+
 def test_no_tokens():
     p = Problem(BF, 4, 3, 64, 32, 2, 16)
     e = torch.empty((0, 64), dtype=BF, device=DEV)

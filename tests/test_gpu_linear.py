@@ -163,6 +163,26 @@ def test_whole_numbers(M, N, K, extras):
     assert torch.equal(p(), z.to(BF))
 
 
+@pytest.mark.parametrize("N,K", [(1 << 20, 128), (24, 1 << 20), (300, 1 << 19)])
+@pytest.mark.parametrize("M", [1, 20, 300, 1100])
+def test_longest_rows(M, N, K):
+    """K and N up to 2^20, on codes of whole numbers of at most 1: sums below
+    2^24, exact."""
+    p = Problem(1, 1, 128, "none", bias=False, residual=False)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(M)
+    one = torch.tensor([0x38, 0x00, 0xB8], dtype=torch.uint8, device=DEV)             # 1, 0, -1
+    draw = lambda shape: one[torch.randint(0, 3, shape, generator=g, device=DEV, dtype=torch.int32).long()]
+    p.M, p.N, p.K, p.n_out = M, N, K, N
+    p.xq, p.w = draw((M, K)), draw((N, K))
+    p.xs = torch.ones((M, K // 128), device=DEV)
+    p.ws = torch.ones(((N + 127) // 128, K // 128), device=DEV)
+    z = torch.zeros((M, N), dtype=torch.float64, device=DEV)
+    for k in range(0, K, 1 << 15):
+        z += decode(p.xq[:, k:k + (1 << 15)]) @ decode(p.w[:, k:k + (1 << 15)]).t()
+    assert torch.equal(p(), z.to(BF))
+
+
 @pytest.mark.parametrize("M,N,K", [(30000, 264, 128), (50000, 300, 384), (20000, 1030, 512), (30000, 4096, 128),
                                    (30000, 4100, 256)])
 def test_many_items(M, N, K):
