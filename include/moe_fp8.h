@@ -455,7 +455,8 @@ moe_status moe_w4a8_experts(const uint8_t *x_q, const float *x_s,
  * ascending expert id, sentinels at the end of a segment only, each route
  * listed once; entries that are not ids of a route or an expert are skipped.
  * expert_ids holds sorted_cap / block_m entries; a device-side plan length
- * above sorted_cap is taken as sorted_cap.
+ * above sorted_cap is taken as sorted_cap.  sorted_cap = 0 is a plan without
+ * routes: its pointers and the workspace may be NULL.
  * Constraints: K and N multiples of 8, at most 2^20; E <= 1024; block_m in
  * {8, 16, 32, 64, 128}; sorted_cap % block_m == 0; M * top_k and sorted_cap
  * at most 2^31 - 1024; x, w, dy, y, dx and dw
