@@ -35,6 +35,7 @@ MOE_FUSE_AUTO, MOE_FUSE_OFF, MOE_FUSE_ON = 0, 1, 2
 MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32 = 0, 1, 2
 MOE_GMM_FWD, MOE_GMM_DX, MOE_GMM_DW = 0, 1, 2
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_SWIGLU = 0, 1, 2, 3
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_ALIGN",
                 4: "MOE_ERR_CAPACITY", 5: "MOE_ERR_UNSUPPORTED", 6: "MOE_ERR_HIP"}
@@ -49,7 +50,9 @@ EXPORTED = ("moe_plan_capacity", "moe_plan_workspace_size", "moe_plan", "moe_qua
             "moe_w4a8_experts_workspace_size", "moe_w4a8_experts", "moe_prepack_w13_size",
             "moe_prepack_w13", "moe_fp8_layer", "moe_group_mm_workspace_size", "moe_group_mm",
             "moe_group_mm_dx", "moe_group_mm_dw", "moe_fp8_linear_workspace_size",
-            "moe_fp8_linear")
+            "moe_fp8_linear", "moe_route_scored", "moe_route_scored_bwd", "moe_combine", "moe_combine_bwd",
+            "moe_quant_i8", "moe_i8_linear_workspace_size", "moe_i8_linear",
+            "moe_i8_group_mm_workspace_size", "moe_i8_group_mm")
 
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -127,6 +130,22 @@ _c = {
                                             _i32),
     "moe_fp8_linear": _proto("moe_fp8_linear", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
                              _i64, _i32, _vp, _i64, _vp, _sz, _vp),
+    "moe_route_scored": _proto("moe_route_scored", _i32, _vp, _i32, _i64, _i64, _i32, _i32, _i32, _vp, _i32,
+                               _i32, _i32, _i32, ctypes.c_float, _i32, _vp, _vp, _vp),
+    "moe_route_scored_bwd": _proto("moe_route_scored_bwd", _i32, _vp, _i32, _i64, _i64, _i32, _i32, _i32, _i32,
+                                   ctypes.c_float, _vp, _vp, _vp, _i64, _vp),
+    "moe_combine": _proto("moe_combine", _i32, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp, _i64, _i64, _i64,
+                          _i32, _vp, _i64, _vp),
+    "moe_combine_bwd": _proto("moe_combine_bwd", _i32, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _i32, _i64,
+                              _i64, _i32, _vp, _i64, _vp, _vp),
+    "moe_quant_i8": _proto("moe_quant_i8", _i32, _vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp),
+    "moe_i8_linear_workspace_size": _proto("moe_i8_linear_workspace_size", _sz, _i64, _i64, _i64, _i32),
+    "moe_i8_linear": _proto("moe_i8_linear", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32,
+                            _vp, _i32, _i64, _vp, _sz, _vp),
+    "moe_i8_group_mm_workspace_size": _proto("moe_i8_group_mm_workspace_size", _sz, _i64, _i64, _i64, _i32,
+                                             _i32, _i32, _i64, _i32, _i32),
+    "moe_i8_group_mm": _proto("moe_i8_group_mm", _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                              _i64, _i64, _i32, _i32, _i32, _i64, _i32, _vp, _i32, _i64, _vp, _sz, _vp),
     "moe_status_str": _proto("moe_status_str", ctypes.c_char_p, _i32),
     "moe_last_hip_error": _proto("moe_last_hip_error", ctypes.c_char_p),
     "moe_last_error": _proto("moe_last_error", ctypes.c_char_p),
@@ -624,6 +643,190 @@ def moe_fp8_linear(x_q, x_s, w, w_s, out, bias=None, residual=None, act=MOE_ACT_
     _launch(where, stream, (x_q, x_s, w, w_s, out, bias, residual, workspace), x_q.data_ptr(),
             x_s.data_ptr(), w.data_ptr(), w_s.data_ptr(), None if bias is None else bias.data_ptr(), rp,
             ld_res, M, N, K, act, op, ld_out, *_ws(where, workspace))
+
+
+# ------------------------------------------------------ routing by scores --
+
+def _slots(where, name, t, dtype, shape):
+    _need(t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == shape, where,
+          f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def moe_route_scored(router_logits, top_k, topk_ids, topk_weights, score=MOE_SCORE_SIGMOID, bias=None,
+                     n_group=1, topk_group=1, group_top=2, renorm=True, routed_scaling=1.0, n_shared=0,
+                     stream=None):
+    """Experts by scores: router_logits [M, E_routed] fp32, bf16 or fp16 ->
+    topk_ids int32 and topk_weights fp32 [M, top_k + n_shared].  Scores are the
+    logits' sigmoids or softmax; score + bias [E_routed] fp32 decides who is
+    chosen, within the topk_group of n_group groups with the largest sums of
+    group_top scores; weights are the chosen scores, divided by their sum
+    (renorm), times routed_scaling; a shared expert follows with weight 1.
+    Slots that no expert is left for (logits of -infinity) hold id -1."""
+    where = "moe_route_scored"
+    _need(router_logits.dim() == 2 and router_logits.dtype in _DT, where,
+          "router_logits must be a 2-d fp32, bf16 or fp16 tensor")
+    M, E = router_logits.shape
+    lp, ld = _rows_arg(where, "router_logits", router_logits, router_logits.dtype, E)
+    shape = (M, top_k + n_shared)
+    bp = None if bias is None else _slots(where, "bias", bias, torch.float32, (E,))
+    ip = _slots(where, "topk_ids", topk_ids, torch.int32, shape)
+    wp = _slots(where, "topk_weights", topk_weights, torch.float32, shape)
+    _launch(where, stream, (router_logits, bias, topk_ids, topk_weights), lp, _DT[router_logits.dtype], M, ld,
+            E, top_k, score, bp, n_group, topk_group, group_top, int(bool(renorm)), routed_scaling, n_shared,
+            ip, wp)
+
+
+def moe_route_scored_bwd(router_logits, topk_ids, d_weights, d_logits, score=MOE_SCORE_SIGMOID, renorm=True,
+                         routed_scaling=1.0, stream=None):
+    """The gradient of moe_route_scored's weights by the logits, the choice
+    taken as fixed: d_logits [M, E_routed] of the logits' type from topk_ids
+    int32 and d_weights fp32 [M, top_k + n_shared]."""
+    where = "moe_route_scored_bwd"
+    _need(router_logits.dim() == 2 and router_logits.dtype in _DT, where,
+          "router_logits must be a 2-d fp32, bf16 or fp16 tensor")
+    M, E = router_logits.shape
+    lp, ld = _rows_arg(where, "router_logits", router_logits, router_logits.dtype, E)
+    dp, ld_d = _rows_arg(where, "d_logits", d_logits, router_logits.dtype, E)
+    _need(d_logits.shape[0] == M and topk_ids.dim() == 2 and topk_ids.shape[0] == M, where,
+          "router_logits, topk_ids and d_logits disagree on M")
+    shape = tuple(topk_ids.shape)
+    ip = _slots(where, "topk_ids", topk_ids, torch.int32, shape)
+    wp = _slots(where, "d_weights", d_weights, torch.float32, shape)
+    _launch(where, stream, (router_logits, topk_ids, d_weights, d_logits), lp, _DT[router_logits.dtype], M, ld,
+            E, shape[1], score, int(bool(renorm)), routed_scaling, ip, wp, dp, ld_d)
+
+
+# ------------------------------------------------- weighted sum of routes --
+
+_IDS = {torch.int32: MOE_IDS_I32, torch.int64: MOE_IDS_I64}
+
+
+def _combine_args(where, y, topk_weights, topk_ids, E):
+    """(M, top_k, K, y's pointer and leading dimension, ids' pointer and type)"""
+    _need(y.dim() == 2 and y.dtype in (torch.bfloat16, torch.float16), where, "y must be a 2-d bf16 or fp16 tensor")
+    _need(topk_weights.dim() == 2, where, "topk_weights must be [M, top_k]")
+    M, k = topk_weights.shape
+    _need(y.shape[0] == M * k, where, "y must have one row per route")
+    yp, ld_y = _rows_arg(where, "y", y, y.dtype, y.shape[1])
+    ip, dt = None, MOE_IDS_I32
+    if topk_ids is not None:
+        _need(topk_ids.dtype in _IDS, where, "topk_ids must be int32 or int64")
+        _need(E is not None, where, "topk_ids need E")
+        ip, dt = _slots(where, "topk_ids", topk_ids, topk_ids.dtype, (M, k)), _IDS[topk_ids.dtype]
+    return M, k, y.shape[1], yp, ld_y, ip, dt
+
+
+def moe_combine(y, topk_weights, out, topk_ids=None, E=None, residual=None, stream=None):
+    """out[t] = residual[t] + sum_j topk_weights[t, j] y[t * top_k + j]: y
+    [M * top_k, K] bf16 or fp16 (moe_group_mm's or moe_i8_group_mm's rows),
+    topk_weights [M, top_k] fp32, out and residual [M, K] of y's type (residual
+    may be out).  Routes whose topk_ids lie outside [0, E) are masked; without
+    topk_ids every route counts."""
+    where = "moe_combine"
+    M, k, K, yp, ld_y, ip, dt = _combine_args(where, y, topk_weights, topk_ids, E)
+    wp = _slots(where, "topk_weights", topk_weights, torch.float32, (M, k))
+    op, ld_out = _rows_arg(where, "out", out, y.dtype, K)
+    _need(out.shape[0] == M, where, "out and topk_weights disagree on M")
+    rp, ld_res = None, 0
+    if residual is not None:
+        rp, ld_res = _rows_arg(where, "residual", residual, y.dtype, K)
+        _need(residual.shape[0] == M, where, "residual and topk_weights disagree on M")
+    _launch(where, stream, (y, topk_weights, out, topk_ids, residual), yp, ld_y, _DT[y.dtype], wp, ip, dt,
+            0 if E is None else E, rp, ld_res, M, K, k, op, ld_out)
+
+
+def moe_combine_bwd(dout, y, topk_weights, dy, d_weights, topk_ids=None, E=None, stream=None):
+    """The gradient of moe_combine: dy [M * top_k, K] = topk_weights * dout
+    (rows of masked routes left as they were) and d_weights [M, top_k] fp32 =
+    the products of dout's and y's rows (0 for masked routes)."""
+    where = "moe_combine_bwd"
+    M, k, K, yp, ld_y, ip, dt = _combine_args(where, y, topk_weights, topk_ids, E)
+    wp = _slots(where, "topk_weights", topk_weights, torch.float32, (M, k))
+    gp = _slots(where, "d_weights", d_weights, torch.float32, (M, k))
+    op, ld_out = _rows_arg(where, "dout", dout, y.dtype, K)
+    dp, ld_dy = _rows_arg(where, "dy", dy, y.dtype, K)
+    _need(dout.shape[0] == M and dy.shape[0] == M * k, where, "dout, dy and topk_weights disagree on rows")
+    _launch(where, stream, (dout, y, topk_weights, dy, d_weights, topk_ids), op, ld_out, yp, ld_y, _DT[y.dtype],
+            wp, ip, dt, 0 if E is None else E, M, K, k, dp, ld_dy, gp)
+
+
+# ------------------------------------------------- 8-bit integer products --
+
+def moe_quant_i8(x, x_q, x_s, stream=None):
+    """x [M, K] bf16 or fp16 (row stride may exceed K) -> x_q int8 [M, K] and
+    one scale a row, x_s fp32 [M]: s = max(amax / 127, 2^-126), codes rounded
+    to nearest even.  Activations by token, or weights [N, K] by channel."""
+    where = "moe_quant_i8"
+    _need(x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float16), where, "x must be a 2-d bf16 or fp16 tensor")
+    M, K = x.shape
+    xp, ld = _rows_arg(where, "x", x, x.dtype, K)
+    qp = _slots(where, "x_q", x_q, torch.int8, (M, K))
+    sp = _slots(where, "x_s", x_s, torch.float32, (M,))
+    _launch(where, stream, (x, x_q, x_s), xp, _DT[x.dtype], M, K, ld, qp, sp)
+
+
+def moe_i8_linear_workspace_size(M, N, K, act=MOE_ACT_NONE):
+    return _c["moe_i8_linear_workspace_size"](M, N, K, act)
+
+
+def moe_i8_linear(x_q, x_s, w, w_s, out, bias=None, residual=None, act=MOE_ACT_NONE, workspace=None,
+                  stream=None):
+    """out = act(x_s w_s (x_q w^T) + bias) + residual: x_q [M, K] and w [N, K]
+    int8 with scales x_s [M] and w_s [N] fp32, bias [N] fp32, residual and out
+    bf16 or fp16 [M, N] -- [M, N/2] with MOE_ACT_SWIGLU, whose w holds the gate
+    rows, then the up rows.  residual may be out itself."""
+    where = "moe_i8_linear"
+    _need(x_q.dim() == 2 and w.dim() == 2, where, "x_q and w must be 2-d")
+    M, K = x_q.shape
+    N = w.shape[0]
+    qp = _slots(where, "x_q", x_q, torch.int8, (M, K))
+    wp = _slots(where, "w", w, torch.int8, (N, K))
+    xsp = _slots(where, "x_s", x_s, torch.float32, (M,))
+    wsp = _slots(where, "w_s", w_s, torch.float32, (N,))
+    bp = None if bias is None else _slots(where, "bias", bias, torch.float32, (N,))
+    _need(out.dtype in (torch.bfloat16, torch.float16), where, "out must be bf16 or fp16")
+    n_out = N // 2 if act == MOE_ACT_SWIGLU else N
+    op, ld_out = _rows_arg(where, "out", out, out.dtype, n_out)
+    _need(out.shape[0] == M, where, "out and x_q disagree on M")
+    rp, ld_res = None, 0
+    if residual is not None:
+        rp, ld_res = _rows_arg(where, "residual", residual, out.dtype, n_out)
+        _need(residual.shape[0] == M, where, "residual and x_q disagree on M")
+    _launch(where, stream, (x_q, x_s, w, w_s, out, bias, residual, workspace), qp, xsp, wp, wsp, bp, rp, ld_res,
+            M, N, K, act, op, _DT[out.dtype], ld_out, *_ws(where, workspace))
+
+
+def moe_i8_group_mm_workspace_size(M, K, N, E, top_k, block_m, sorted_cap, act=MOE_ACT_NONE,
+                                   x_per_route=False):
+    return _c["moe_i8_group_mm_workspace_size"](M, K, N, E, top_k, block_m, sorted_cap, act,
+                                                int(bool(x_per_route)))
+
+
+def moe_i8_group_mm(x_q, x_s, w, w_s, sorted_token_ids, expert_ids, num_tokens_post_padded, top_k, block_m,
+                    out, bias=None, act=MOE_ACT_NONE, workspace=None, stream=None, x_per_route=None):
+    """out[r] = act(x_s[t(r)] w_s[e(r)] (x_q[t(r)] w[e(r)]^T) + bias[e(r)]) for
+    every route r of the plan: w [E, N, K] int8 with w_s [E, N] fp32, bias
+    [E, N] fp32, x_q [M, K] (t(r) = r // top_k) or [M * top_k, K] (t(r) = r)
+    int8 with x_s fp32, out [M * top_k, N] bf16 or fp16 (N/2 columns with
+    MOE_ACT_SWIGLU); x_per_route tells which rows x_q has (None: by their
+    number).  Rows of masked routes are left as they were."""
+    where = "moe_i8_group_mm"
+    _need(w.dim() == 3 and x_q.dim() == 2, where, "w must be 3-d, x_q 2-d")
+    E, N, K = w.shape
+    wp = _slots(where, "w", w, torch.int8, (E, N, K))
+    wsp = _slots(where, "w_s", w_s, torch.float32, (E, N))
+    bp = None if bias is None else _slots(where, "bias", bias, torch.float32, (E, N))
+    qp = _slots(where, "x_q", x_q, torch.int8, (x_q.shape[0], K))
+    xsp = _slots(where, "x_s", x_s, torch.float32, (x_q.shape[0],))
+    _need(out.dtype in (torch.bfloat16, torch.float16), where, "out must be bf16 or fp16")
+    op, ld_out = _rows_arg(where, "out", out, out.dtype, N // 2 if act == MOE_ACT_SWIGLU else N)
+    R = out.shape[0]
+    plan, cap = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
+    per_route = _x_rows(where, "x_q", x_q, R, top_k, x_per_route)
+    _launch(where, stream, (x_q, x_s, w, w_s, out, bias, sorted_token_ids, expert_ids, num_tokens_post_padded,
+                            workspace), qp, xsp, per_route, wp, wsp, bp, *plan, R // top_k, K, N, E, top_k,
+            block_m, cap, act, op, _DT[out.dtype], ld_out, *_ws(where, workspace))
 
 
 def moe_status_str(status):

@@ -11,9 +11,12 @@
 
 #include "../../include/moe_fp8.h"
 #include "group_mm.h"
+#include "i8_mm.h"
 #include "internal.h"
 #include "layer.h"
 #include "linear.h"
+#include "router.h"
+#include "rows.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
 
@@ -1046,13 +1049,19 @@ moe_status check_rows(const char *name, const void *p, int64_t ld, int64_t cols)
     return MOE_OK;
 }
 
-// The checks that the three operators share, then their launches.
-moe_status run_group(moe::GroupMmArgs &g, int32_t dtype, void *workspace, size_t workspace_bytes,
-                     void *stream, const char *what) {
+moe_status check_group_plan(const moe::GroupMmArgs &g) {
     if (!g.sorted || !g.eids || !g.ntp)
         return fail(MOE_ERR_NULL, "sorted_token_ids, expert_ids and num_tokens_post_padded are required");
     if (((uintptr_t)g.sorted & 3u) || ((uintptr_t)g.eids & 3u) || ((uintptr_t)g.ntp & 3u))
         return fail(MOE_ERR_ALIGN, "the plan must be 4-byte aligned");
+    return MOE_OK;
+}
+
+// The checks that the three operators share, then their launches.
+moe_status run_group(moe::GroupMmArgs &g, int32_t dtype, void *workspace, size_t workspace_bytes,
+                     void *stream, const char *what) {
+    const moe_status st = check_group_plan(g);
+    if (st != MOE_OK) return st;
     if (g.out == g.x || g.out == g.dy || g.out == g.w)
         return fail(MOE_ERR_SHAPE, "the output is one of the inputs");
     const size_t need = moe::group_mm_workspace(g, workspace);
@@ -1255,6 +1264,388 @@ MOE_API moe_status moe_fp8_linear(const uint8_t *x_q, const float *x_s, const ui
     a.out = (uint16_t *)out_bf16;
     a.ld_out = ld_out;
     return hip_check(moe::launch_linear(a, (hipStream_t)stream), "moe_fp8_linear: launch");
+}
+
+// ---------------------------------------------------- routing by scores
+
+static_assert(MOE_DT_BF16 == moe::kDtBf16 && MOE_DT_F16 == moe::kDtF16 && MOE_DT_F32 == moe::kDtF32, "types");
+static_assert(MOE_SCORE_SOFTMAX == moe::kScoreSoftmax && MOE_SCORE_SIGMOID == moe::kScoreSigmoid, "scores");
+
+namespace {
+
+// What the forward and the gradient check alike.
+moe_status check_scored(int32_t dtype, int64_t M, int64_t ld, int32_t E, int32_t score, float scale) {
+    if (M < 0 || M > ((int64_t)1 << 31) - 1024) return fail(MOE_ERR_SHAPE, "need 0 <= M <= 2^31 - 1024");
+    if (E < 1 || E > kMaxE) return fail(MOE_ERR_SHAPE, "need 1 <= E_routed <= %d (%d)", kMaxE, E);
+    if (dtype < MOE_DT_BF16 || dtype > MOE_DT_F32) return fail(MOE_ERR_SHAPE, "unknown dtype %d", dtype);
+    if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID)
+        return fail(MOE_ERR_SHAPE, "unknown score %d", score);
+    if (ld < E) return fail(MOE_ERR_SHAPE, "leading dimension (%lld) < E_routed (%d)", (long long)ld, E);
+    if (ld > (int64_t)1 << 30) return fail(MOE_ERR_UNSUPPORTED, "leading dimension exceeds 2^30");
+    if (!std::isfinite(scale)) return fail(MOE_ERR_SHAPE, "routed_scaling must be finite");
+    return MOE_OK;
+}
+
+bool aligned_to(const void *p, int32_t dtype) {
+    return ((uintptr_t)p & (dtype == MOE_DT_F32 ? 3u : 1u)) == 0;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_route_scored(const void *router_logits, int32_t dtype, int64_t M, int64_t ld_logits,
+                                    int32_t E_routed, int32_t top_k, int32_t score, const float *bias,
+                                    int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renorm,
+                                    float routed_scaling, int32_t n_shared, int32_t *topk_ids,
+                                    float *topk_weights, void *stream) {
+    moe_status st = check_scored(dtype, M, ld_logits, E_routed, score, routed_scaling);
+    if (st != MOE_OK) return st;
+    if (n_group < 1 || n_group > moe::kRouteMaxGroups || E_routed % n_group != 0)
+        return fail(MOE_ERR_SHAPE, "n_group (%d) must divide E_routed (%d) and be at most %d", n_group, E_routed,
+                    moe::kRouteMaxGroups);
+    if (topk_group < 1 || topk_group > n_group)
+        return fail(MOE_ERR_SHAPE, "need 1 <= topk_group <= n_group (%d, %d)", topk_group, n_group);
+    if (group_top != 1 && group_top != 2) return fail(MOE_ERR_SHAPE, "group_top must be 1 or 2");
+    if (top_k < 1 || top_k > 32 || top_k > E_routed / n_group * topk_group)
+        return fail(MOE_ERR_SHAPE, "need 1 <= top_k <= 32 and no more than the kept groups' experts (%d)", top_k);
+    if (n_shared != 0 && n_shared != 1) return fail(MOE_ERR_SHAPE, "n_shared must be 0 or 1");
+    if (E_routed + n_shared > kMaxE)
+        return fail(MOE_ERR_SHAPE, "E_routed + n_shared = %d exceeds %d", E_routed + n_shared, kMaxE);
+    if (M == 0) return MOE_OK;
+    if (!router_logits || !topk_ids || !topk_weights)
+        return fail(MOE_ERR_NULL, "router_logits, topk_ids and topk_weights are required");
+    if (!aligned_to(router_logits, dtype) || ((uintptr_t)bias & 3u) || ((uintptr_t)topk_ids & 3u) ||
+        ((uintptr_t)topk_weights & 3u))
+        return fail(MOE_ERR_ALIGN, "every tensor must be aligned to its elements");
+    moe::ScoreArgs a = {};
+    a.logits = router_logits;
+    a.dtype = dtype;
+    a.M = M;
+    a.ld = ld_logits;
+    a.E = E_routed;
+    a.top_k = top_k;
+    a.n_shared = n_shared;
+    a.score = score;
+    a.renorm = renorm != 0;
+    a.scale = routed_scaling;
+    a.bias = bias;
+    a.n_group = n_group;
+    a.topk_group = topk_group;
+    a.group_top = group_top;
+    a.ids = topk_ids;
+    a.w = topk_weights;
+    return hip_check(moe::launch_route_scored(a, (hipStream_t)stream), "moe_route_scored: launch");
+}
+
+MOE_API moe_status moe_route_scored_bwd(const void *router_logits, int32_t dtype, int64_t M, int64_t ld_logits,
+                                        int32_t E_routed, int32_t slots, int32_t score, int32_t renorm,
+                                        float routed_scaling, const int32_t *topk_ids,
+                                        const float *d_weights, void *d_logits, int64_t ld_d_logits,
+                                        void *stream) {
+    moe_status st = check_scored(dtype, M, ld_logits, E_routed, score, routed_scaling);
+    if (st == MOE_OK) st = check_scored(dtype, M, ld_d_logits, E_routed, score, routed_scaling);
+    if (st != MOE_OK) return st;
+    if (slots < 1 || slots > 33) return fail(MOE_ERR_SHAPE, "need 1 <= slots <= 33 (%d)", slots);
+    if (M == 0) return MOE_OK;
+    if (!router_logits || !topk_ids || !d_weights || !d_logits)
+        return fail(MOE_ERR_NULL, "router_logits, topk_ids, d_weights and d_logits are required");
+    if (!aligned_to(router_logits, dtype) || !aligned_to(d_logits, dtype) || ((uintptr_t)topk_ids & 3u) ||
+        ((uintptr_t)d_weights & 3u))
+        return fail(MOE_ERR_ALIGN, "every tensor must be aligned to its elements");
+    if (d_logits == router_logits || d_logits == d_weights || d_logits == topk_ids)
+        return fail(MOE_ERR_SHAPE, "d_logits is one of the inputs");
+    moe::ScoreArgs a = {};
+    a.logits = router_logits;
+    a.dtype = dtype;
+    a.M = M;
+    a.ld = ld_logits;
+    a.E = E_routed;
+    a.slots = slots;
+    a.score = score;
+    a.renorm = renorm != 0;
+    a.scale = routed_scaling;
+    a.ids = const_cast<int32_t *>(topk_ids);
+    a.dw = d_weights;
+    a.dl = d_logits;
+    a.ld_dl = ld_d_logits;
+    return hip_check(moe::launch_route_scored_bwd(a, (hipStream_t)stream), "moe_route_scored_bwd: launch");
+}
+
+// ------------------------------------------------- weighted sum of routes
+
+namespace {
+
+moe_status check_combine(int32_t dtype, int64_t M, int64_t K, int32_t top_k, const void *ids, int32_t ids_dtype,
+                         int32_t E) {
+    moe_status st = check_dtype(dtype);
+    if (st != MOE_OK) return st;
+    if (M < 0 || K <= 0 || K % 8 != 0 || top_k < 1)
+        return fail(MOE_ERR_SHAPE, "need M >= 0, K a positive multiple of 8 and top_k >= 1");
+    if (K > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "K (%lld) exceeds 2^20", (long long)K);
+    if (M > (((int64_t)1 << 31) - 1024) / top_k)
+        return fail(MOE_ERR_SHAPE, "M * top_k must not exceed 2^31 - 1024");
+    if (ids && ids_dtype != MOE_IDS_I32 && ids_dtype != MOE_IDS_I64)
+        return fail(MOE_ERR_SHAPE, "ids_dtype %d is neither MOE_IDS_I32 nor MOE_IDS_I64", ids_dtype);
+    if (ids && E < 1) return fail(MOE_ERR_SHAPE, "need E >= 1 with topk_ids");
+    return MOE_OK;
+}
+
+moe::CombineArgs combine_args(int32_t dtype, int64_t M, int64_t K, int32_t top_k, const float *w,
+                              const void *ids, int32_t ids_dtype, int32_t E, const void *y, int64_t ld_y) {
+    moe::CombineArgs a = {};
+    a.f16 = dtype == MOE_DT_F16;
+    a.M = M;
+    a.K = (int)K;
+    a.top_k = top_k;
+    a.E = E;
+    a.w = w;
+    a.ids = ids;
+    a.ids_i64 = ids_dtype == MOE_IDS_I64;
+    a.y = (const uint16_t *)y;
+    a.ld_y = ld_y;
+    return a;
+}
+
+moe_status check_weights(const void *w, const void *ids, int32_t ids_dtype) {
+    if (!w) return fail(MOE_ERR_NULL, "topk_weights is NULL");
+    if (((uintptr_t)w & 3u) || ((uintptr_t)ids & (ids_dtype == MOE_IDS_I64 ? 7u : 3u)))
+        return fail(MOE_ERR_ALIGN, "topk_weights and topk_ids must be aligned to their elements");
+    return MOE_OK;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_combine(const void *y, int64_t ld_y, int32_t dtype, const float *topk_weights,
+                               const void *topk_ids, int32_t ids_dtype, int32_t E, const void *residual,
+                               int64_t ld_res, int64_t M, int64_t K, int32_t top_k, void *out, int64_t ld_out,
+                               void *stream) {
+    moe_status st = check_combine(dtype, M, K, top_k, topk_ids, ids_dtype, E);
+    if (st != MOE_OK || M == 0) return st;
+    if ((st = check_rows("y", y, ld_y, K)) != MOE_OK) return st;
+    if ((st = check_rows("out", out, ld_out, K)) != MOE_OK) return st;
+    if (residual && (st = check_rows("residual", residual, ld_res, K)) != MOE_OK) return st;
+    if ((st = check_weights(topk_weights, topk_ids, ids_dtype)) != MOE_OK) return st;
+    if (out == y || out == topk_weights || out == topk_ids)
+        return fail(MOE_ERR_SHAPE, "out is one of the inputs");
+    if (residual == out && ld_res != ld_out)
+        return fail(MOE_ERR_SHAPE, "residual is out: ld_res (%lld) must equal ld_out (%lld)", (long long)ld_res,
+                    (long long)ld_out);
+    moe::CombineArgs a = combine_args(dtype, M, K, top_k, topk_weights, topk_ids, ids_dtype, E, y, ld_y);
+    a.res = (const uint16_t *)residual;
+    a.ld_res = ld_res;
+    a.out = (uint16_t *)out;
+    a.ld_out = ld_out;
+    return hip_check(moe::launch_combine(a, (hipStream_t)stream), "moe_combine: launch");
+}
+
+MOE_API moe_status moe_combine_bwd(const void *dout, int64_t ld_dout, const void *y, int64_t ld_y, int32_t dtype,
+                                   const float *topk_weights, const void *topk_ids, int32_t ids_dtype, int32_t E,
+                                   int64_t M, int64_t K, int32_t top_k, void *dy, int64_t ld_dy,
+                                   float *d_weights, void *stream) {
+    moe_status st = check_combine(dtype, M, K, top_k, topk_ids, ids_dtype, E);
+    if (st != MOE_OK || M == 0) return st;
+    if ((st = check_rows("dout", dout, ld_dout, K)) != MOE_OK) return st;
+    if ((st = check_rows("y", y, ld_y, K)) != MOE_OK) return st;
+    if ((st = check_rows("dy", dy, ld_dy, K)) != MOE_OK) return st;
+    if ((st = check_weights(topk_weights, topk_ids, ids_dtype)) != MOE_OK) return st;
+    if (!d_weights) return fail(MOE_ERR_NULL, "d_weights is NULL");
+    if ((uintptr_t)d_weights & 3u) return fail(MOE_ERR_ALIGN, "d_weights must be 4-byte aligned");
+    if (dy == dout || dy == y || d_weights == topk_weights || dy == (void *)d_weights || dy == topk_weights ||
+        dy == topk_ids || (void *)d_weights == dout || (void *)d_weights == y || (void *)d_weights == topk_ids)
+        return fail(MOE_ERR_SHAPE, "an output is one of the inputs or the other output");
+    moe::CombineArgs a = combine_args(dtype, M, K, top_k, topk_weights, topk_ids, ids_dtype, E, y, ld_y);
+    a.dout = (const uint16_t *)dout;
+    a.ld_out = ld_dout;
+    a.dy = (uint16_t *)dy;
+    a.ld_dy = ld_dy;
+    a.dw = d_weights;
+    return hip_check(moe::launch_combine_bwd(a, (hipStream_t)stream), "moe_combine_bwd: launch");
+}
+
+// ------------------------------------------------- 8-bit integer products
+
+namespace {
+
+// 2^17 - 16 products of at most 2^14 stay below 2^31.
+constexpr int64_t kMaxI8K = ((int64_t)1 << 17) - 16;
+
+moe_status check_i8_k(int64_t M, int64_t K) {
+    if (M < 0 || K <= 0 || K % 16 != 0)
+        return fail(MOE_ERR_SHAPE, "need M >= 0 and K a positive multiple of 16");
+    if (K > kMaxI8K)
+        return fail(MOE_ERR_UNSUPPORTED, "K (%lld) exceeds %lld, where 32-bit sums may overflow", (long long)K,
+                    (long long)kMaxI8K);
+    return MOE_OK;
+}
+
+moe_status check_i8_n(int64_t N, int32_t act) {
+    if (N <= 0) return fail(MOE_ERR_SHAPE, "need N > 0");
+    if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return fail(MOE_ERR_SHAPE, "unknown act %d", act);
+    if (act == MOE_ACT_SWIGLU && N % 2 != 0)
+        return fail(MOE_ERR_SHAPE, "MOE_ACT_SWIGLU needs an even N (%lld)", (long long)N);
+    if (N > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "N (%lld) exceeds 2^20", (long long)N);
+    return MOE_OK;
+}
+
+moe_status check_i8_linear(int64_t M, int64_t N, int64_t K, int32_t act) {
+    moe_status st = check_i8_k(M, K);
+    if (st == MOE_OK) st = check_i8_n(N, act);
+    if (st != MOE_OK) return st;
+    if (M > ((int64_t)1 << 31) - 1024) return fail(MOE_ERR_SHAPE, "M must not exceed 2^31 - 1024");
+    // output tiles of at least 32 rows x 64 columns, numbered in int32
+    if (((M + 31) / 32) * ((N + 63) / 64) >= ((int64_t)1 << 31) - ((int64_t)1 << 21))
+        return fail(MOE_ERR_UNSUPPORTED, "more output tiles than int32 counts");
+    return MOE_OK;
+}
+
+moe::I8Args i8_args(int64_t M, int64_t N, int64_t K, int32_t act) {
+    moe::I8Args a = {};
+    a.M = M;
+    a.K = (int)K;
+    a.N = (int)N;
+    a.act = act;
+    a.n_out = act == MOE_ACT_SWIGLU ? a.N / 2 : a.N;
+    return a;
+}
+
+moe_status check_i8_group(int64_t M, int64_t K, int64_t N, int32_t E, int32_t top_k, int32_t block_m,
+                          int64_t sorted_cap, int32_t act) {
+    moe_status st = check_i8_k(M, K);
+    if (st == MOE_OK) st = check_i8_n(N, act);
+    // (multiples of 8, with the same number of tiles)
+    if (st == MOE_OK) st = check_group_shape(M, K, (N + 7) / 8 * 8, E, top_k, block_m, sorted_cap);
+    return st;
+}
+
+// The operands and the output that both products have.
+moe_status check_i8_operands(const moe::I8Args &a, int32_t dtype) {
+    moe_status st = check_dtype(dtype);
+    if (st != MOE_OK) return st;
+    if (a.ld_out < a.n_out)
+        return fail(MOE_ERR_SHAPE, "leading dimension of the output (%lld) < %d columns", (long long)a.ld_out,
+                    a.n_out);
+    if (a.ld_out > (int64_t)1 << 30)
+        return fail(MOE_ERR_UNSUPPORTED, "leading dimension of the output exceeds 2^30");
+    if (!a.xq || !a.xs || !a.w || !a.ws || !a.out)
+        return fail(MOE_ERR_NULL, "x_q, x_s, w, w_s and the output are required");
+    if (!aligned16(a.xq) || !aligned16(a.w)) return fail(MOE_ERR_ALIGN, "x_q and w must be 16-byte aligned");
+    if (((uintptr_t)a.xs & 3u) || ((uintptr_t)a.ws & 3u) || ((uintptr_t)a.bias & 3u))
+        return fail(MOE_ERR_ALIGN, "x_s, w_s and bias must be 4-byte aligned");
+    if ((uintptr_t)a.out & 1u) return fail(MOE_ERR_ALIGN, "the output must be 2-byte aligned");
+    const void *o = a.out;
+    if (o == a.xq || o == a.w || o == a.xs || o == a.ws || o == a.bias)
+        return fail(MOE_ERR_SHAPE, "the output is one of the inputs");
+    return MOE_OK;
+}
+
+moe_status run_i8(moe::I8Args &a, void *workspace, size_t workspace_bytes, void *stream, const char *what) {
+    const size_t need = moe::i8_workspace(a, workspace);
+    if (need > 0) {
+        if (!workspace) return fail(MOE_ERR_NULL, "workspace is required");
+        if (((uintptr_t)workspace & 255u) != 0)
+            return fail(MOE_ERR_ALIGN, "workspace must be 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(MOE_ERR_CAPACITY, "workspace %zu bytes < required %zu", workspace_bytes, need);
+    }
+    return hip_check(moe::launch_i8(a, (hipStream_t)stream), what);
+}
+
+}  // namespace
+
+MOE_API moe_status moe_quant_i8(const void *x, int32_t dtype, int64_t M, int64_t K, int64_t ld_x, int8_t *x_q,
+                                float *x_s, void *stream) {
+    moe_status st = check_i8_k(M, K);
+    if (st == MOE_OK) st = check_dtype(dtype);
+    if (st != MOE_OK) return st;
+    if (M > ((int64_t)1 << 31) - 1024) return fail(MOE_ERR_SHAPE, "M must not exceed 2^31 - 1024");
+    if (M == 0) return MOE_OK;
+    if ((st = check_rows("x", x, ld_x, K)) != MOE_OK) return st;
+    if (!x_q || !x_s) return fail(MOE_ERR_NULL, "x_q and x_s are required");
+    if (!aligned16(x_q)) return fail(MOE_ERR_ALIGN, "x_q must be 16-byte aligned");
+    if ((uintptr_t)x_s & 3u) return fail(MOE_ERR_ALIGN, "x_s must be 4-byte aligned");
+    if ((const void *)x_q == x || (const void *)x_s == x || (void *)x_s == (void *)x_q)
+        return fail(MOE_ERR_SHAPE, "an output is the input or the other output");
+    moe::QuantI8Args a = {};
+    a.x = (const uint16_t *)x;
+    a.f16 = dtype == MOE_DT_F16;
+    a.M = M;
+    a.ld = ld_x;
+    a.K = (int)K;
+    a.xq = x_q;
+    a.xs = x_s;
+    return hip_check(moe::launch_quant_i8(a, (hipStream_t)stream), "moe_quant_i8: launch");
+}
+
+MOE_API size_t moe_i8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act) {
+    if (check_i8_linear(M, N, K, act) != MOE_OK || M == 0) return 0;
+    moe::I8Args a = i8_args(M, N, K, act);
+    return moe::i8_workspace(a, nullptr);
+}
+
+MOE_API moe_status moe_i8_linear(const int8_t *x_q, const float *x_s, const int8_t *w, const float *w_s,
+                                 const float *bias, const void *residual, int64_t ld_res, int64_t M, int64_t N,
+                                 int64_t K, int32_t act, void *out, int32_t out_dtype, int64_t ld_out,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+    moe_status st = check_i8_linear(M, N, K, act);
+    if (st != MOE_OK || M == 0) return st;
+    moe::I8Args a = i8_args(M, N, K, act);
+    a.xq = x_q;
+    a.xs = x_s;
+    a.w = w;
+    a.ws = w_s;
+    a.bias = bias;
+    a.res = (const uint16_t *)residual;
+    a.ld_res = ld_res;
+    a.out = (uint16_t *)out;
+    a.ld_out = ld_out;
+    a.f16 = out_dtype == MOE_DT_F16;
+    if ((st = check_i8_operands(a, out_dtype)) != MOE_OK) return st;
+    if (residual && ld_res < a.n_out)
+        return fail(MOE_ERR_SHAPE, "ld_res (%lld) < %d columns", (long long)ld_res, a.n_out);
+    if (residual && ld_res > (int64_t)1 << 30) return fail(MOE_ERR_UNSUPPORTED, "ld_res exceeds 2^30");
+    if ((uintptr_t)residual & 1u) return fail(MOE_ERR_ALIGN, "residual must be 2-byte aligned");
+    if (residual == out && residual && ld_res != ld_out)
+        return fail(MOE_ERR_SHAPE, "residual is out: ld_res (%lld) must equal ld_out (%lld)", (long long)ld_res,
+                    (long long)ld_out);
+    return run_i8(a, workspace, workspace_bytes, stream, "moe_i8_linear: launch");
+}
+
+MOE_API size_t moe_i8_group_mm_workspace_size(int64_t M, int64_t K, int64_t N, int32_t E, int32_t top_k,
+                                              int32_t block_m, int64_t sorted_cap, int32_t act,
+                                              int32_t x_per_route) {
+    if (check_i8_group(M, K, N, E, top_k, block_m, sorted_cap, act) != MOE_OK || M == 0 || sorted_cap == 0)
+        return 0;
+    moe::I8Args a = i8_args(M, N, K, act);
+    a.grouped = true;
+    a.g = group_args(moe::kGmmFwd, MOE_DT_BF16, nullptr, nullptr, nullptr, M, K, N, E, top_k, block_m,
+                     sorted_cap, x_per_route);
+    return moe::i8_workspace(a, nullptr);
+}
+
+MOE_API moe_status moe_i8_group_mm(const int8_t *x_q, const float *x_s, int32_t x_per_route, const int8_t *w,
+                                   const float *w_s, const float *bias, const int32_t *sorted_token_ids,
+                                   const int32_t *expert_ids, const int32_t *num_tokens_post_padded, int64_t M,
+                                   int64_t K, int64_t N, int32_t E, int32_t top_k, int32_t block_m,
+                                   int64_t sorted_cap, int32_t act, void *y, int32_t y_dtype, int64_t ld_y,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+    moe_status st = check_i8_group(M, K, N, E, top_k, block_m, sorted_cap, act);
+    if (st == MOE_OK) st = check_dtype(y_dtype);
+    if (st != MOE_OK) return st;
+    if (M == 0 || sorted_cap == 0) return MOE_OK;
+    moe::I8Args a = i8_args(M, N, K, act);
+    a.xq = x_q;
+    a.xs = x_s;
+    a.w = w;
+    a.ws = w_s;
+    a.bias = bias;
+    a.out = (uint16_t *)y;
+    a.ld_out = ld_y;
+    a.f16 = y_dtype == MOE_DT_F16;
+    a.grouped = true;
+    a.g = group_args(moe::kGmmFwd, MOE_DT_BF16, sorted_token_ids, expert_ids, num_tokens_post_padded, M, K, N,
+                     E, top_k, block_m, sorted_cap, x_per_route);
+    if ((st = check_i8_operands(a, y_dtype)) != MOE_OK) return st;
+    if ((st = check_group_plan(a.g)) != MOE_OK) return st;
+    return run_i8(a, workspace, workspace_bytes, stream, "moe_i8_group_mm: launch");
 }
 
 // ------------------------------------------------- no-allocation variant

@@ -42,6 +42,8 @@ struct GroupMmArgs {
     }
 };
 
+// Sets div_m and div_s (token_of) from top_k.
+void group_divider(GroupMmArgs &g);
 // Lays the workspace out at ws (NULL: sizes only) and returns its bytes.
 size_t group_mm_workspace(GroupMmArgs &g, void *ws);
 hipError_t launch_group_mm(const GroupMmArgs &g, hipStream_t st);

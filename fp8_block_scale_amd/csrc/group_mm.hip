@@ -61,16 +61,6 @@ __device__ __forceinline__ v4f mfma32(const u32x4 &a, const u32x4 &b, const v4f 
                                                        __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// Two values at once (one packed conversion, round to nearest even).
-template <bool F16>
-__device__ __forceinline__ uint32_t to16x2(float lo, float hi) {
-    typedef float v2f __attribute__((ext_vector_type(2)));
-    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-    const v2f v = {lo, hi};
-    if constexpr (F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2h));
-    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2bf));
-}
-
 template <bool F16>
 __device__ __forceinline__ float from16(uint32_t v) {
     if constexpr (F16) return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
@@ -930,7 +920,7 @@ hipError_t launch_group_no_routes(GroupMmArgs g, hipStream_t st) {
     return launch_sum<false>(g, st);
 }
 
-size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
+void group_divider(GroupMmArgs &g) {
     // r / top_k for 0 <= r < 2^31 by one high product: with s the least
     // number with 2^s >= top_k and m = floor(2^(31 + s) / top_k) + 1 (below
     // 2^32), m top_k exceeds 2^(31 + s) by at most top_k <= 2^s, so
@@ -939,6 +929,10 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
     while (((int64_t)1 << s) < g.top_k) ++s;
     g.div_m = (uint32_t)((((uint64_t)1 << (31 + s)) / (uint64_t)g.top_k) + 1);
     g.div_s = s;
+}
+
+size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
+    group_divider(g);
 
     const int64_t rpe = g.R / g.E;
     const double R = (double)g.R, E = (double)g.E;

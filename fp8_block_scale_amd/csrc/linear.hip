@@ -48,18 +48,6 @@ __device__ __forceinline__ v8i join8(const u32x4 &lo, const u32x4 &hi) {
     return r;
 }
 
-__device__ __forceinline__ float silu(float z) {
-    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
-}
-// tanh form: 0.5 z (1 + tanh(u)) = z / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3)
-__device__ __forceinline__ float gelu(float z) {
-    const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
-    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u2 * -1.44269504088896340736f));
-}
-__device__ __forceinline__ float act1(float z, int act) {
-    return act == kActSilu ? silu(z) : act == kActGelu ? gelu(z) : z;
-}
-
 // ----------------------------------------------------------------- few rows
 
 // 16 weight rows (with SwiGLU 8 gate and their 8 up rows) x 16 NQ rows of x

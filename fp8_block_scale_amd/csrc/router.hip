@@ -1,0 +1,302 @@
+// Routing by scores and the gradient of its weights.
+//   s_e = sigmoid(l_e), or softmax over all of a token's experts
+//   c_e = s_e + bias_e                                     decides who is chosen
+//   groups of E / n_group consecutive experts: the sum of their group_top
+//   (1 or 2) largest c; only the topk_group best groups are kept
+//   chosen: the top_k largest c; w_j = scale s_j, or scale s_j / sum of the chosen s
+//
+// One wave routes one token.
+#include "common.h"
+#include "router.h"
+
+namespace moe {
+
+namespace {
+
+template <int DT>
+__device__ __forceinline__ float load_logit(const void *p, int64_t i) {
+    if constexpr (DT == kDtF32) return static_cast<const float *>(p)[i];
+    else if constexpr (DT == kDtF16) return (float)static_cast<const _Float16 *>(p)[i];
+    else return bf16_bits_to_f32(static_cast<const uint16_t *>(p)[i]);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_grad(void *p, int64_t i, float v) {
+    if constexpr (DT == kDtF32) static_cast<float *>(p)[i] = v;
+    else if constexpr (DT == kDtF16) static_cast<_Float16 *>(p)[i] = (_Float16)v;
+    else static_cast<uint16_t *>(p)[i] = (uint16_t)f32_to_bf16_bits(v);
+}
+
+// FP64 -> uint64 with the same order; -0 and +0 are one value.
+__device__ __forceinline__ uint64_t ordered64(double d) {
+    const uint64_t u = (uint64_t)__double_as_longlong(d + 0.0);
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+    return v;
+}
+
+// A logit that can be chosen: neither NaN nor -infinity.  (+infinity counts as
+// the largest finite value, so that a softmax stays defined.)
+__device__ __forceinline__ bool usable(float l) { return l > -INFINITY; }
+__device__ __forceinline__ float finite(float l) { return fminf(l, 3.402823466e38f); }
+
+__device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
+
+// ------------------------------------------------------------------ forward
+
+// Lane layout: a group's experts lie with 2^sh lanes; lane p of group g holds
+// experts g n + p, g n + p + 2^sh, ... (n experts a group).
+template <int DT, int NPL>
+__global__ void __launch_bounds__(256)
+route_scored_kernel(ScoreArgs a, int sh) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= a.M) return;
+    const int n = a.E / a.n_group, g = lane >> sh, p = lane & ((1 << sh) - 1);
+    const int64_t row = t * a.ld;
+    auto expert = [&](int i) { return g * n + p + (i << sh); };
+    float l[NPL];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        l[i] = -INFINITY;
+        if (g < a.n_group && p + (i << sh) < n) {
+            l[i] = load_logit<DT>(a.logits, row + expert(i));
+            l[i] = usable(l[i]) ? finite(l[i]) : -INFINITY;
+        }
+        mx = fmaxf(mx, l[i]);
+    }
+    double total = 0.0;
+    if (a.score == kScoreSoftmax) {
+        mx = wave_max(mx);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (usable(l[i])) total += exp((double)l[i] - (double)mx);
+        total = wave_sum(total);
+    }
+    // choice keys; 0: not to be chosen
+    uint64_t key[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        key[i] = 0;
+        if (!usable(l[i])) continue;
+        double c = a.score == kScoreSoftmax ? exp((double)l[i] - (double)mx) / total : sigmoid64(l[i]);
+        if (a.bias) c += (double)a.bias[expert(i)];
+        if (c > -INFINITY) key[i] = ordered64(c);
+    }
+    auto value = [](uint64_t k) {
+        return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
+    };
+    if (a.topk_group < a.n_group) {
+        uint64_t b1 = 0, b2 = 0;                 // the two largest of the group
+        auto merge = [&](uint64_t x) {
+            if (x > b1) {
+                b2 = b1;
+                b1 = x;
+            } else if (x > b2) {
+                b2 = x;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) merge(key[i]);
+        for (int d = 1; d < 1 << sh; d <<= 1) {
+            const uint64_t o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
+            merge(o1);
+            merge(o2);
+        }
+        uint64_t sc = 0;
+        if (b1) sc = a.group_top == 2 && b2 ? ordered64(value(b1) + value(b2)) : b1;
+        int rank = 0;
+        for (int h = 0; h < a.n_group; ++h) {
+            const uint64_t o = __shfl(sc, h << sh, 64);
+            rank += o > sc || (o == sc && h < g);
+        }
+        if (rank >= a.topk_group) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) key[i] = 0;
+        }
+    }
+    int sel = -1;
+    for (int r = 0; r < a.top_k; ++r) {
+        uint64_t bk = 0;
+        int be = 1 << 30;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (key[i] > bk) {
+                bk = key[i];
+                be = expert(i);
+            }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) {
+            const uint64_t ok = __shfl_xor(bk, d, 64);
+            const int oe = __shfl_xor(be, d, 64);
+            if (ok > bk || (ok == bk && oe < be)) {
+                bk = ok;
+                be = oe;
+            }
+        }
+        if (bk == 0) break;                      // the wave agrees: nobody is left
+        if (lane == r) sel = be;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (expert(i) == be && p + (i << sh) < n) key[i] = 0;
+    }
+    // weights: lane j holds slot j
+    double s = 0.0;
+    const float ls = sel >= 0 ? finite(load_logit<DT>(a.logits, row + sel)) : -INFINITY;
+    if (a.renorm) {
+        // up to a factor that renormalising takes out, so that not all underflow
+        const float m = a.score == kScoreSoftmax ? wave_max(ls) : fminf(wave_max(ls), 0.f);
+        if (sel >= 0)
+            s = a.score == kScoreSoftmax ? exp((double)ls - (double)m)
+                                         : 1.0 / (exp((double)m) + exp((double)m - (double)ls));
+    } else if (sel >= 0) {
+        s = a.score == kScoreSoftmax ? exp((double)ls - (double)mx) / total : sigmoid64(ls);
+    }
+    if (a.renorm) {
+        const double sum = wave_sum(s);
+        s = sum > 0.0 ? s / sum : 0.0;
+    }
+    const int kk = a.top_k + a.n_shared;
+    if (lane < a.top_k) {
+        a.ids[t * kk + lane] = sel;
+        a.w[t * kk + lane] = (float)(s * (double)a.scale);
+    } else if (lane < kk) {                      // the shared expert
+        a.ids[t * kk + lane] = a.E;
+        a.w[t * kk + lane] = 1.0f;
+    }
+}
+
+// ----------------------------------------------------------------- backward
+
+// With a_j = scale dL/dw_j for the token's slots j that hold an expert:
+//   softmax                dl_e = p_e (sum_{j: e_j = e} a_j - sum_j a_j p_j)
+//   softmax, renormalised  dl_e = sum_{j: e_j = e} p_j (a_j - sum a p), p over the slots
+//   sigmoid                dl_e = sum_{j: e_j = e} s_j (1 - s_j) a_j
+//   sigmoid, renormalised  ... with (a_j - sum a s / S) / S in the place of a_j, S = sum s
+// (1 - s is the sigmoid of -l: no cancellation where s is near 1.)
+template <int DT, int NPL>
+__global__ void __launch_bounds__(256)
+route_scored_bwd_kernel(ScoreArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= a.M) return;
+    const int64_t row = t * a.ld;
+    const bool dense = a.score == kScoreSoftmax && !a.renorm;
+    // lane j holds slot j
+    int id = -1;
+    float av = 0.f;
+    if (lane < a.slots) {
+        id = a.ids[t * a.slots + lane];
+        if (id < 0 || id >= a.E) id = -1;
+        if (id >= 0) av = a.dw[t * a.slots + lane] * a.scale;
+    }
+    float ls = id >= 0 ? load_logit<DT>(a.logits, row + id) : -INFINITY;
+    if (!usable(ls)) id = -1;                    // never chosen: weight 0, whatever its logit
+    ls = id >= 0 ? finite(ls) : -INFINITY;
+    if (id < 0) av = 0.f;
+    float p[NPL], mx = -INFINITY, inv = 0.f, v = 0.f, dot = 0.f;
+    if (dense) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 64 * i;
+            p[i] = e < a.E ? load_logit<DT>(a.logits, row + e) : -INFINITY;
+            p[i] = usable(p[i]) ? finite(p[i]) : -INFINITY;
+            mx = fmaxf(mx, p[i]);
+        }
+        mx = wave_max(mx);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            p[i] = usable(p[i]) ? expf(p[i] - mx) : 0.f;
+            sum += p[i];
+        }
+        sum = wave_sum(sum);
+        inv = sum > 0.f ? 1.0f / sum : 0.f;
+        dot = wave_sum(id >= 0 ? av * expf(ls - mx) * inv : 0.f);
+        v = av;
+    } else if (a.score == kScoreSoftmax) {
+        const float m = wave_max(ls);
+        const float ex = id >= 0 ? expf(ls - m) : 0.f;
+        const float sum = wave_sum(ex);
+        const float q = sum > 0.f ? ex / sum : 0.f;
+        v = q * (av - wave_sum(av * q));
+    } else {
+        // renormalised: s up to a factor, which cancels, so that not all underflow
+        const float m = a.renorm ? fminf(wave_max(ls), 0.f) : 0.f;
+        const float s = id >= 0 ? 1.0f / (expf(m) + expf(m - ls)) : 0.f;
+        const float rest = id >= 0 ? 1.0f / (1.0f + expf(ls)) : 0.f;
+        if (a.renorm) {
+            const float S = wave_sum(s), as = wave_sum(av * s);
+            av = S > 0.f ? (av - as / S) / S : 0.f;
+        }
+        v = s * rest * av;
+    }
+    float d[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) d[i] = 0.f;
+    for (int j = 0; j < a.slots; ++j) {
+        const int ej = __builtin_amdgcn_readlane(id, j);
+        const float vj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), j));
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (lane + 64 * i == ej) d[i] += vj;
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane + 64 * i;
+        if (e < a.E) store_grad<DT>(a.dl, t * a.ld_dl + e, dense ? p[i] * inv * (d[i] - dot) : d[i]);
+    }
+}
+
+template <int DT, int NPL>
+hipError_t launch_fwd(const ScoreArgs &a, int sh, hipStream_t st) {
+    route_scored_kernel<DT, NPL><<<(unsigned)((a.M + 3) / 4), 256, 0, st>>>(a, sh);
+    return hipGetLastError();
+}
+template <int DT, int NPL>
+hipError_t launch_bwd(const ScoreArgs &a, hipStream_t st) {
+    route_scored_bwd_kernel<DT, NPL><<<(unsigned)((a.M + 3) / 4), 256, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t fwd(const ScoreArgs &a, hipStream_t st) {
+    int sh = 6;                                  // log2 of a group's lanes
+    while (sh > 0 && (a.n_group << sh) > 64) --sh;
+    const int n = a.E / a.n_group, npl = (n + (1 << sh) - 1) >> sh;
+    if (npl <= 2) return launch_fwd<DT, 2>(a, sh, st);
+    if (npl <= 4) return launch_fwd<DT, 4>(a, sh, st);
+    if (npl <= 5) return launch_fwd<DT, 5>(a, sh, st);
+    if (npl <= 8) return launch_fwd<DT, 8>(a, sh, st);
+    if (npl <= 16) return launch_fwd<DT, 16>(a, sh, st);
+    return launch_fwd<DT, 32>(a, sh, st);
+}
+template <int DT>
+hipError_t bwd(const ScoreArgs &a, hipStream_t st) {
+    if (a.E <= 128) return launch_bwd<DT, 2>(a, st);
+    if (a.E <= 256) return launch_bwd<DT, 4>(a, st);
+    if (a.E <= 512) return launch_bwd<DT, 8>(a, st);
+    return launch_bwd<DT, 16>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_route_scored(const ScoreArgs &a, hipStream_t st) {
+    return a.dtype == kDtF32 ? fwd<kDtF32>(a, st) : a.dtype == kDtF16 ? fwd<kDtF16>(a, st) : fwd<kDtBf16>(a, st);
+}
+hipError_t launch_route_scored_bwd(const ScoreArgs &a, hipStream_t st) {
+    return a.dtype == kDtF32 ? bwd<kDtF32>(a, st) : a.dtype == kDtF16 ? bwd<kDtF16>(a, st) : bwd<kDtBf16>(a, st);
+}
+
+}  // namespace moe

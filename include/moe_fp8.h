@@ -540,6 +540,166 @@ moe_status moe_fp8_linear(const uint8_t *x_q, const float *x_s, const uint8_t *w
                           void *out_bf16, int64_t ld_out, void *workspace,
                           size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------- routing by scores -- */
+
+/* Experts by scores, for routers beyond moe_route_plan's renormalised softmax;
+ * its ids and weights are those that moe_plan, moe_plan_quant, moe_fp8_layer,
+ * moe_fp8_experts and moe_combine take.  For every token, with l its logits:
+ *   s_e = sigmoid(l_e)              MOE_SCORE_SIGMOID
+ *   s_e = e^l_e / sum_f e^l_f       MOE_SCORE_SOFTMAX (over all its experts)
+ *   c_e = s_e + bias_e              the choice score (bias NULL: s_e)
+ *   Groups: the experts lie in n_group groups of E_routed / n_group
+ *   consecutive ones; a group's score is the sum of its group_top (1 or 2)
+ *   largest choice scores, and only experts of the topk_group groups with the
+ *   largest scores may be chosen (equal scores: the lower group).
+ *   Chosen: the top_k largest choice scores (equal scores: the lower expert),
+ *   listed largest first.
+ *   w_j = routed_scaling * s_j, with renorm != 0 routed_scaling * s_j / sum of
+ *   the chosen experts' s.  The bias decides who is chosen and enters no weight.
+ * Scores, group scores and weights are computed in 64 bits and weights rounded
+ * once, so that the choice is that of the formula unless scores agree to 64-bit
+ * rounding.
+ *   router_logits [M, ld_logits] of dtype MOE_DT_F32, MOE_DT_BF16 or MOE_DT_F16
+ *   (first E_routed columns); bias [E_routed] FP32 or NULL.
+ *   topk_ids [M, top_k + n_shared] int32 out, topk_weights the same FP32 out.
+ *   n_shared = 1 appends expert E_routed as route slot top_k with weight 1.
+ * An expert whose logit is -infinity or NaN, or whose bias is -infinity or NaN,
+ * is never chosen and counts in no group's score (a group without others is
+ * taken last and gives nobody); a logit of +infinity counts as the largest finite FP32
+ * value.  Slots that no expert is left for hold id -1, a masked route, with
+ * weight 0.
+ * Constraints: 1 <= E_routed, E_routed + n_shared <= 1024; n_group divides
+ * E_routed, at most 64; 1 <= topk_group <= n_group; top_k <= 32 and at most
+ * topk_group * E_routed / n_group; M <= 2^31 - 1024; ld_logits at most 2^30;
+ * everything aligned to its elements; the outputs overlap nothing.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED
+ * (ld_logits), MOE_ERR_HIP. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+moe_status moe_route_scored(const void *router_logits, int32_t dtype, int64_t M, int64_t ld_logits,
+                            int32_t E_routed, int32_t top_k, int32_t score, const float *bias,
+                            int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renorm,
+                            float routed_scaling, int32_t n_shared, int32_t *topk_ids,
+                            float *topk_weights, void *stream);
+
+/* The gradient of those weights by the logits, the choice taken as fixed:
+ *   d_logits[t, e] = sum_j d_weights[t, j] dw_j / dl_e
+ * over the slots j of the token whose id lies in [0, E_routed) (masked slots
+ * and the shared expert have constant weights).  The ids may be any choice of
+ * experts (a router held fixed): the renormalising sum is over the row's slots,
+ * and an id that a row lists twice counts twice.  An expert that moe_route_scored
+ * never chooses (logit -infinity or NaN) has weight 0 and gradient 0.
+ *   topk_ids [M, slots] int32, d_weights [M, slots] FP32 (slots = top_k +
+ *   n_shared there); d_logits [M, ld_d_logits] of dtype out: all E_routed
+ *   columns are written, 0 where there is no gradient.
+ * With MOE_SCORE_SOFTMAX and renorm = 0 every expert's logit has a gradient;
+ * otherwise the chosen ones'.  Computed in FP32, rounded once.
+ * Constraints and errors as above; 1 <= slots <= 33; d_logits is none of the
+ * inputs. */
+moe_status moe_route_scored_bwd(const void *router_logits, int32_t dtype, int64_t M, int64_t ld_logits,
+                                int32_t E_routed, int32_t slots, int32_t score, int32_t renorm,
+                                float routed_scaling, const int32_t *topk_ids, const float *d_weights,
+                                void *d_logits, int64_t ld_d_logits, void *stream);
+
+/* ------------------------------------------------- weighted sum of routes -- */
+
+/* A layer's output from its routes' rows (those of moe_group_mm or
+ * moe_i8_group_mm), and the gradient of that:
+ *   moe_combine      out[t] = residual[t] + sum_j w[t, j] y[t * top_k + j]
+ *   moe_combine_bwd  dy[t * top_k + j] = w[t, j] dout[t]
+ *                    d_weights[t, j] = sum_k dout[t, k] y[t * top_k + j, k]
+ * (the gradient by residual is dout itself).
+ *   y [M * top_k, ld_y], residual [M, ld_res] or NULL, out [M, ld_out], dout
+ *   [M, ld_dout], dy [M * top_k, ld_dy]: BF16 or FP16 (dtype), first K columns;
+ *   topk_weights and d_weights [M, top_k] FP32.
+ *   topk_ids [M, top_k] int32 or int64 (ids_dtype), or NULL: routes whose id
+ *   lies outside [0, E) are masked: their y rows are not read and add nothing,
+ *   their dy rows are left as they were, their d_weights are 0.  NULL: every
+ *   route counts (E and ids_dtype are ignored).
+ * Sums are FP32, over a token's routes in their order, with one rounding;
+ * no atomics.  Values are not screened (0 times infinity is NaN).
+ * residual may be out itself (same pointer and leading dimension).
+ * Constraints: K a multiple of 8, at most 2^20; M * top_k <= 2^31 - 1024; the
+ * 16-bit operands 16-byte aligned, leading dimensions multiples of 8 and at
+ * most 2^30; outputs overlap nothing else.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_HIP. */
+moe_status moe_combine(const void *y, int64_t ld_y, int32_t dtype, const float *topk_weights,
+                       const void *topk_ids, int32_t ids_dtype, int32_t E, const void *residual,
+                       int64_t ld_res, int64_t M, int64_t K, int32_t top_k, void *out, int64_t ld_out,
+                       void *stream);
+
+moe_status moe_combine_bwd(const void *dout, int64_t ld_dout, const void *y, int64_t ld_y, int32_t dtype,
+                           const float *topk_weights, const void *topk_ids, int32_t ids_dtype, int32_t E,
+                           int64_t M, int64_t K, int32_t top_k, void *dy, int64_t ld_dy, float *d_weights,
+                           void *stream);
+
+/* ------------------------------------------------- 8-bit integer products -- */
+
+/* Rows quantised to 8-bit integers with one scale each:
+ *   x_s[m] = max(max_k |x[m, k]| / 127, 2^-126)
+ *   x_q[m, k] = x[m, k] * (1 / x_s[m]), rounded to nearest, ties to even
+ * in FP32 with IEEE divisions: codes in [-127, 127], an all-zero row gives zeros.
+ * Activations by token, or weights [N, K] by output channel.
+ *   x [M, ld_x] BF16 or FP16 (dtype), first K columns; x_q [M, K] int8 and
+ *   x_s [M] FP32 out, dense.
+ * A row that holds an infinity or a NaN gets codes 0 and that as its scale, so
+ * that all of its products are NaN.
+ * Constraints: K a multiple of 16, at most 2^17 - 16; M <= 2^31 - 1024; x and
+ * x_q 16-byte aligned, ld_x a multiple of 8 and at most 2^30.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_HIP. */
+moe_status moe_quant_i8(const void *x, int32_t dtype, int64_t M, int64_t K, int64_t ld_x, int8_t *x_q,
+                        float *x_s, void *stream);
+
+/* The dense product of such codes with its epilogue, moe_fp8_linear's
+ * counterpart with one scale per row and channel:
+ *   z[m, n]   = x_s[m] w_s[n] sum_k x_q[m, k] w[n, k] + bias[n]
+ *   out[m, n] = act(z)[m, n] + residual[m, n]
+ * and grouped by expert over a plan, moe_group_mm's counterpart, with
+ * t(r) = r / top_k (x_per_route = 0) or r:
+ *   z[r, n]   = x_s[t(r)] w_s[e(r), n] sum_k x_q[t(r), k] w[e(r), n, k] + bias[e(r), n]
+ *   y[r, n]   = act(z)[r, n]
+ * The sums are exact 32-bit integers (any int8 codes, -128 too); scales, bias,
+ * activation (as moe_fp8_linear's: with MOE_ACT_SWIGLU rows [0, N/2) of w are the
+ * gate and rows [N/2, N) the up projection, and there are N/2 output columns)
+ * and residual are FP32, with one rounding.  Results depend on no schedule.
+ *   x_q [M, K] (per route [M * top_k, K]) int8, x_s one FP32 per row;
+ *   w [N, K] or [E, N, K] int8, w_s and bias (or NULL) [N] or [E, N] FP32;
+ *   out / y BF16 or FP16 (out_dtype / y_dtype), residual [M, ld_res] of the same
+ *   type or NULL, which may be out itself (same pointer and leading dimension).
+ *   Rows of masked routes and columns past the last are left as they were.
+ * The plan is as for moe_group_mm (sorted_cap = 0: no routes, nothing is
+ * written).
+ * Constraints: K a multiple of 16, at most 2^17 - 16 (no sum overflows); N at
+ * most 2^20, even with SwiGLU; M and M * top_k at most 2^31 - 1024; E, block_m
+ * and sorted_cap as for moe_group_mm; x_q and w 16-byte, scales and bias 4-byte,
+ * outputs and residual 2-byte aligned, leading dimensions at most 2^30; outputs
+ * overlap nothing else.  The workspace (256-byte aligned) holds
+ * the *_workspace_size bytes (0: none needed, NULL accepted; also 0 for sizes
+ * it rejects) and is written from scratch by each call: calls on one stream may
+ * share it, calls that overlap may not.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_CAPACITY
+ * (workspace), MOE_ERR_UNSUPPORTED (sizes out of range, or more output tiles
+ * than int32 counts), MOE_ERR_HIP. */
+size_t moe_i8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act);
+
+moe_status moe_i8_linear(const int8_t *x_q, const float *x_s, const int8_t *w, const float *w_s,
+                         const float *bias, const void *residual, int64_t ld_res, int64_t M, int64_t N,
+                         int64_t K, int32_t act, void *out, int32_t out_dtype, int64_t ld_out,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+size_t moe_i8_group_mm_workspace_size(int64_t M, int64_t K, int64_t N, int32_t E, int32_t top_k,
+                                      int32_t block_m, int64_t sorted_cap, int32_t act,
+                                      int32_t x_per_route);
+
+moe_status moe_i8_group_mm(const int8_t *x_q, const float *x_s, int32_t x_per_route, const int8_t *w,
+                           const float *w_s, const float *bias, const int32_t *sorted_token_ids,
+                           const int32_t *expert_ids, const int32_t *num_tokens_post_padded, int64_t M,
+                           int64_t K, int64_t N, int32_t E, int32_t top_k, int32_t block_m,
+                           int64_t sorted_cap, int32_t act, void *y, int32_t y_dtype, int64_t ld_y,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------- no-allocation variant -- */
 
 /* For callers that cannot allocate device memory (code under HIP graph

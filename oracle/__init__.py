@@ -47,7 +47,7 @@ from .plan import plan_capacity, plan_ref
 from .quant import quant_groups_ref, quant_act_ref, ue8m0_exponent
 from .experts import experts_ref, experts_w4a8_ref, ExpertsResult
 from .e2m1 import E2M1_MAX, dequant_k32, e2m1_decode, e2m1_encode, unpack_e2m1
-from .router import router_ref
+from .router import route_scored_ref, router_ref
 
 __all__ = [
     "E4M3_MAX",
@@ -70,5 +70,6 @@ __all__ = [
     "e2m1_decode",
     "e2m1_encode",
     "unpack_e2m1",
+    "route_scored_ref",
     "router_ref",
 ]
