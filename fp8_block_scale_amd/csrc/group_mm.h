@@ -46,6 +46,10 @@ struct GroupMmArgs {
 void group_divider(GroupMmArgs &g);
 // Lays the workspace out at ws (NULL: sizes only) and returns its bytes.
 size_t group_mm_workspace(GroupMmArgs &g, void *ws);
+// For another kernel over the plan's row tiles (forward): lays the list of
+// tiles of tile_rows rows out at ws and returns its bytes, and lists them.
+size_t group_tiles_workspace(GroupMmArgs &g, int tile_rows, void *ws);
+hipError_t launch_group_prep(const GroupMmArgs &g, hipStream_t st);
 hipError_t launch_group_mm(const GroupMmArgs &g, hipStream_t st);
 // dx of tokens without a route (M, K, out and ld_out are read): zeros.
 hipError_t launch_group_no_routes(GroupMmArgs g, hipStream_t st);

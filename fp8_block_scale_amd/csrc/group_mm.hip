@@ -920,6 +920,20 @@ hipError_t launch_group_no_routes(GroupMmArgs g, hipStream_t st) {
     return launch_sum<false>(g, st);
 }
 
+hipError_t launch_group_prep(const GroupMmArgs &g, hipStream_t st) {
+    group_prep_kernel<<<1, kPrepThreads, 0, st>>>(g, g.tile_rows);
+    return hipGetLastError();
+}
+
+size_t group_tiles_workspace(GroupMmArgs &g, int tile_rows, void *ws) {
+    g.tile_rows = tile_rows;
+    g.max_slots = 0;
+    g.max_tiles = (int)(g.R / tile_rows + std::min((int64_t)g.E, g.R));
+    g.meta = (int32_t *)ws;
+    g.tiles = (int4 *)((uint8_t *)ws + 256);
+    return 256 + (size_t)g.max_tiles * 16;
+}
+
 void group_divider(GroupMmArgs &g) {
     // r / top_k for 0 <= r < 2^31 by one high product: with s the least
     // number with 2^s >= top_k and m = floor(2^(31 + s) / top_k) + 1 (below

@@ -23,7 +23,8 @@ struct I8Args {
     GroupMmArgs g;           // the plan, E, R, top_k, block_m, per_route; with the tile kernel its
                              // row tiles (grouped)
     // the schedule (i8_workspace)
-    int stream_nq;           // few rows: tiles of 16 rows per pass
+    int stream_nq;           // few rows: tiles of 16 rows per pass (0: the tile kernel)
+    int tile_rows;           // rows of a tile
 };
 
 // Chooses the schedule, lays the workspace out at ws (NULL: sizes only) and

@@ -7,6 +7,7 @@
 // The sums are 32-bit integers, exact for K < 2^17 (2^17 products of at most
 // 2^14); scales, bias, activation and residual are FP32, rounded once.
 #include <algorithm>
+#include <type_traits>
 
 #include "i8_mm.h"
 #include "tiles.h"
@@ -119,19 +120,394 @@ i8_stream_kernel(I8Args a) {
     }
 }
 
+// ---------------------------------------------------------------- many rows
+
+// An item is a TQ x TP tile: TQ rows of x (B side of the MFMA) and TP weight
+// rows (A side), so that a lane's results are 8 consecutive columns of one
+// row: row i of MFMA tile 2 t + h is weight row 32 t + 8 (i / 4) + 4 h + i % 4.
+// With SwiGLU the tile holds, per 64 rows, 32 gate rows and then their 32 up
+// rows: both meet in one wave.
+//
+// A stage is 128 values of K of both operands in a ring of S slots in LDS, filled
+// by 16-byte global -> LDS copies, rows gathered by the plan on the way.  The
+// MFMAs of one half of a stage (64 values of K) run beside the LDS reads of the
+// next half, into the other register set.  A slot is free once every wave has
+// read its second half, in the middle of its own stage: the copies of the stage
+// S further on go out then, beside the second half's MFMAs.
+template <int TP, int TQ, int WP, int WQ, int S>
+struct I8Tile {
+    static constexpr int NW = WP * WQ;
+    static constexpr int PB = TP * 128, QB = TQ * 128, Stage = PB + QB;
+    static constexpr int JP = PB / 1024 / NW, JQ = QB / 1024 / NW, J = JP + JQ;
+    static constexpr int NP = TP / WP / 16, NQ = TQ / WQ / 16;
+    static constexpr size_t Smem = (size_t)S * Stage;
+    static_assert(NP % 4 == 0 && NW == 4 && JP % 2 == 0 && JQ >= 1 && Smem <= 160 * 1024, "tile");
+};
+
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
+
+// SiLU (g1 = -log2 e, g3 = 0) and GELU (g1 = -2 sqrt(2 / pi) log2 e, g3 = 0.044715 g1)
+// in one form, z / (1 + 2^(g1 z + g3 z^3)): one copy of the epilogue's code.  (z^2
+// is kept finite, so that it counts for nothing where g3 = 0.)
+__device__ __forceinline__ float gated(float z, float g1, float g3) {
+    const float e = z * fmaf(fminf(z * z, 3.402823466e38f), g3, g1);
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(e));
+}
+
+// f(0), f(1), ... f(N - 1) with constants
+template <int N, typename F, int I = 0>
+__device__ __forceinline__ void static_for(F &&f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>());
+        static_for<N, F, I + 1>(static_cast<F &&>(f));
+    }
+}
+
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef v4f v4f_any __attribute__((aligned(4)));
+
+// f[0, 8) = p[c, c + 8), 0 past n
+__device__ __forceinline__ void load8(const float *p, int c, int n, float (&f)[8]) {
+    if (c + 8 <= n) {
+        const v4f lo = *reinterpret_cast<const v4f_any *>(p + c), hi = *reinterpret_cast<const v4f_any *>(p + c + 4);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            f[v] = lo[v];
+            f[4 + v] = hi[v];
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) f[v] = c + v < n ? p[c + v] : 0.f;
+    }
+}
+
+template <int TP, int TQ, int WP, int WQ, int S, bool SW, bool GROUPED>
+__global__ void __launch_bounds__(64 * WP * WQ, 1)
+i8_tile_kernel(I8Args a) {
+    using T = I8Tile<TP, TQ, WP, WQ, S>;
+    constexpr int NW = T::NW, JP = T::JP, JQ = T::JQ, NP = T::NP, NQ = T::NQ;
+    constexpr int TC = SW ? TP / 2 : TP;                      // output columns of a tile
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6);
+    const int wp = w % WP, wq = w / WP, i16 = l & 15, grp = l >> 4;
+    const int nct = (a.n_out + TC - 1) / TC;
+    const int nrt = GROUPED ? min(uni(a.g.meta[0]), a.g.max_tiles) : (int)((a.M + TQ - 1) / TQ);
+    const int n_items = nrt * nct;
+    const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+    const int end = (int)((int64_t)(xcd + 1) * n_items / 8);
+    int lit = (int)((int64_t)xcd * n_items / 8) + (blockIdx.x >> 3), cit = lit;
+    if (cit >= end) return;
+    const int nst = (a.K + 127) >> 7;                         // stages of an item
+
+    struct Item {
+        int e, c0, row0, rows;       // expert, first column, first row (of the plan), rows
+    };
+    auto item_of = [&](int i) {
+        Item it;
+        int rt, ct;
+        panel_tile<8>(i, nrt, nct, rt, ct);
+        it.c0 = ct * TC;
+        if (GROUPED) {
+            const int4 t = a.g.tiles[rt];
+            it.row0 = uni(t.x);
+            it.rows = uni(t.y);
+            it.e = uni(t.z);
+        } else {
+            it.row0 = rt * TQ;
+            it.rows = (int)min((int64_t)TQ, a.M - it.row0);
+            it.e = 0;
+        }
+        return it;
+    };
+    // the output row of a tile's row, -1 if none
+    auto out_row = [&](const Item &it, int row) {
+        if (row >= it.rows) return -1;
+        if (!GROUPED) return it.row0 + row;
+        const int r = a.g.sorted[it.row0 + row];
+        return (uint32_t)r < (uint32_t)a.g.R ? r : -1;
+    };
+    auto x_row = [&](int r) { return GROUPED && !a.g.per_route ? a.g.token_of(r) : r; };
+
+    // ---- load side: a copy of a wave fills 8 rows of 128 bytes.  An address of
+    // weights is a uniform base, stepped from stage to stage, and a lane offset
+    // that holds the row (past the last: the last one); one of x the row's own.
+    const int lrow = l >> 3;
+    const int kc_p = (l & 7) ^ ((lrow & 3) | ((w & 1) << 2)), kc_q = (l & 7) ^ lrow;      // chunks of the rows
+    const int8_t *pbase = nullptr;           // the tile's first weight row, the stage's values of K
+    const int64_t up = SW ? (int64_t)a.n_out * a.K : 0;       // from a gate row to its up row
+    uint32_t poff[JP];
+    const int8_t *qptr[JQ];
+    int lkt = 0;                             // stage of the item
+    auto load_setup = [&]() {
+        const Item it = item_of(lit);
+        lkt = 0;
+        pbase = a.w + ((int64_t)it.e * a.N + it.c0) * a.K;
+        const int last = min(TC, a.n_out - it.c0) - 1;
+#pragma unroll
+        for (int j = 0; j < JP; ++j) {
+            const int c = (SW ? (j >> 1) * 32 + 8 * w : 8 * (j * NW + w)) + lrow;
+            poff[j] = (uint32_t)min(c, last) * (uint32_t)a.K + (uint32_t)kc_p * 16u;
+        }
+#pragma unroll
+        for (int j = 0; j < JQ; ++j) {
+            // a row that has no route reads row 0 of x, one past the last row
+            // that: their results are not stored
+            int r = out_row(it, 8 * (j * NW + w) + lrow);
+            if (r < 0) r = GROUPED ? 0 : it.row0 + it.rows - 1;
+            qptr[j] = a.xq + (int64_t)x_row(r) * a.K + kc_q * 16;
+        }
+    };
+    // Copy c of the load side's stage to the slot.  `any`: the stage may reach past
+    // the end of K or lie past the last item, and is read as zeros there.
+    auto issue_copy = [&](auto any, int c, uint8_t *slot) __attribute__((always_inline)) {
+        const int left = a.K - lkt * 128;
+        const void *zero = kZeros;
+        if (c < JP) {
+            const void *p = pbase + (SW && (c & 1) ? up : 0) + poff[c];
+            if (decltype(any)::value && kc_p * 16 >= left) p = zero;
+            lds_dma16(p, slot + (c * NW + w) * 1024);
+        } else {
+            const void *p = qptr[c - JP];
+            if (decltype(any)::value && kc_q * 16 >= left) p = zero;
+            lds_dma16(p, slot + T::PB + ((c - JP) * NW + w) * 1024);
+        }
+    };
+    auto next_k = [&]() {
+        ++lkt;
+        pbase += 128;
+#pragma unroll
+        for (int j = 0; j < JQ; ++j) qptr[j] += 128;
+    };
+    auto stage_issued = [&]() {
+        next_k();
+        if (lkt == nst) {
+            lit += step;
+            if (lit < end) load_setup();
+        }
+    };
+
+    // ---- compute side
+    v4i acc[NP][NQ];
+    auto clear = [&]() {
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) acc[m][n] = v4i{0, 0, 0, 0};
+    };
+    // (emits nothing: tells the compiler that the sums stay in accumulation
+    // registers, which it would copy to vector registers and back every stage)
+    auto keep = [&]() {
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) asm volatile("" : "+a"(acc[m][n]));
+    };
+    const int pf = (i16 & 3) | (((i16 >> 2) & 1) << 2);
+    const int p_off = (wp * (TP / WP) + 8 * (i16 >> 2) + (i16 & 3)) * 128 + ((grp ^ pf) << 4);
+    const int q_off = T::PB + (wq * (TQ / WQ) + i16) * 128 + ((grp ^ (i16 & 7)) << 4);
+    u32x4 pa[2][NP], qb[2][NQ];
+    auto read_op = [&](const uint8_t *slot, int h, int i) {   // operand i of half h: columns', then rows'
+        if (i < NP) pa[h][i] = lds_read16(slot + (p_off ^ (h << 6)) + (i >> 1) * 32 * 128 + (i & 1) * 4 * 128);
+        else qb[h][i - NP] = lds_read16(slot + (q_off ^ (h << 6)) + (i - NP) * 16 * 128);
+    };
+    // The products of a stage in two halves of K, beside them the reads of the
+    // next half (the second half's from rd, then the next stage's first from nx)
+    // and in the second half the copies of the stage S further on to wr, which
+    // is rd's slot: `arrive` lies between.  (The pointers are declared not to
+    // alias: the compiler would wait for the copies in flight before each read.)
+    auto multiply = [&](auto any, const uint8_t *__restrict__ rd, const uint8_t *__restrict__ nx,
+                        uint8_t *__restrict__ wr, auto arrive) __attribute__((always_inline)) {
+        constexpr int kReads = NP + NQ, kPer = (4 * kReads + 3 * NQ - 1) / (3 * NQ);      // in three quarters of the units
+        constexpr int kCopy = (T::J + NQ - 1) / NQ;
+        __builtin_amdgcn_s_waitcnt(0xC07F);                   // lgkmcnt(0): the first half's operands
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h == 1) arrive();
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+                for (int i = n * kPer; i < (n + 1) * kPer && i < kReads; ++i) read_op(h ? nx : rd, h ^ 1, i);
+                if (h == 1) {
+#pragma unroll
+                    for (int c = n * kCopy; c < (n + 1) * kCopy && c < T::J; ++c) issue_copy(any, c, wr);
+                }
+#pragma unroll
+                for (int m = 0; m < NP; ++m) acc[m][n] = mfma64(pa[h][m], qb[h][n], acc[m][n]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+    // (emits no more than the wait for a load: one that some path leaves pending
+    // would be waited for in the loop over the stages, together with all copies)
+    const float g1 = a.act == kActGelu ? -2.30220818f : -1.44269504f, g3 = a.act == kActGelu ? -0.10294324f : 0.f;
+    auto arrived = [](float v) { asm volatile("" : : "v"(v)); };
+    auto epilogue = [&](const Item &it) __attribute__((always_inline)) {
+        const float *ws = a.ws + (int64_t)it.e * a.N, *bias = a.bias ? a.bias + (int64_t)it.e * a.N : nullptr;
+        int rr[NQ];
+        float xs[NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            rr[n] = out_row(it, wq * (TQ / WQ) + 16 * n + i16);
+            xs[n] = rr[n] < 0 ? 0.f : a.xs[x_row(rr[n])];
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) arrived(xs[n]);
+        static_for<NP / (SW ? 4 : 2)>([&](auto tc) __attribute__((always_inline)) {
+            constexpr int ct = decltype(tc)::value, t = SW ? 2 * ct : ct;
+            const int c = it.c0 + wp * (TC / WP) + ct * 32 + 8 * grp;
+            if (c >= a.n_out) return;
+            float s[8], b[8], su[8], bu[8];
+            load8(ws, c, a.n_out, s);
+            if (SW) load8(ws + a.n_out, c, a.n_out, su);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) b[v] = bu[v] = 0.f;
+            if (bias) {
+                load8(bias, c, a.n_out, b);
+                if (SW) load8(bias + a.n_out, c, a.n_out, bu);
+            }
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                arrived(s[v]);
+                arrived(b[v]);
+                if (SW) arrived(su[v]);
+                if (SW) arrived(bu[v]);
+            }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                __builtin_amdgcn_sched_barrier(0);
+                // (emits nothing: not moved to vector registers before)
+#pragma unroll
+                for (int m = 0; m < (SW ? 4 : 2); ++m) asm volatile("" : "+a"(acc[2 * t + m][n]));
+                if (rr[n] < 0) continue;
+                float z[8];
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    z[v] = (float)acc[2 * t + (v >> 2)][n][v & 3] * xs[n] * s[v] + b[v];
+                    if (SW)
+                        z[v] = silu(z[v]) * ((float)acc[2 * t + 2 + (v >> 2)][n][v & 3] * xs[n] * su[v] + bu[v]);
+                }
+                if (!SW && a.act != kActNone) {
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) z[v] = gated(z[v], g1, g3);
+                }
+                uint16_t *d = a.out + (int64_t)rr[n] * a.ld_out + c;
+                const uint16_t *res = a.res ? a.res + (int64_t)rr[n] * a.ld_res + c : nullptr;
+                if (c + 8 <= a.n_out) {
+                    if (res) {
+                        const u32x4 q = *reinterpret_cast<const u32x4_any *>(res);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) z[v] += widen16(a.f16, v & 1 ? q[v >> 1] >> 16 : q[v >> 1]);
+                    }
+                    u32x4 o;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        o[v] = a.f16 ? to16x2<true>(z[2 * v], z[2 * v + 1]) : to16x2<false>(z[2 * v], z[2 * v + 1]);
+                    *reinterpret_cast<u32x4_any *>(d) = o;
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        if (c + v < a.n_out) d[v] = narrow16(a.f16, res ? z[v] + widen16(a.f16, res[v]) : z[v]);
+                }
+            }
+        });
+    };
+
+    // ---- the pipeline: S stages are in flight or being multiplied at any time
+    // (past the last they are copies of zeros: the count of copies to wait for
+    // stays the same, and no branch comes between the MFMAs)
+    load_setup();
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+        for (int c = 0; c < T::J; ++c) issue_copy(std::true_type(), c, smem + s * T::Stage);
+        stage_issued();
+    }
+    // the next stage's copies have landed for this wave, then for all; every
+    // wave has read the slot that the next copies overwrite
+    auto arrive = [&](auto ahead) {          // `ahead` stages may stay in flight
+        constexpr int n = decltype(ahead)::value * T::J;
+        wait_vmcnt<(n < 63 ? n : 63)>();
+        __builtin_amdgcn_s_waitcnt(0xC07F);                   // lgkmcnt(0)
+        stage_barrier();
+    };
+    int slot = 0;                            // of the stage that is being multiplied
+    arrive(std::integral_constant<int, S - 1>());
+#pragma unroll
+    for (int i = 0; i < NP + NQ; ++i) read_op(smem, 0, i);
+    auto stage = [&](auto any) __attribute__((always_inline)) {
+        uint8_t *const sp = smem + slot * T::Stage;
+        slot = slot + 1 == S ? 0 : slot + 1;
+        multiply(any, sp, smem + slot * T::Stage, sp, [&]() __attribute__((always_inline)) {
+            arrive(std::integral_constant<int, S - 2>());
+        });
+        keep();
+    };
+    const int nsame = max(0, nst - S - 1);
+    for (; cit < end; cit += step) {
+        clear();
+        keep();
+        // stages beside which a whole stage of the same item is copied that is
+        // not its last, then the rest
+        for (int k = 0; k < nsame; ++k) {
+            stage(std::false_type());
+            next_k();
+        }
+        for (int k = nsame; k < nst; ++k) {
+            stage(std::true_type());
+            stage_issued();
+        }
+        epilogue(item_of(cit));
+    }
+    wait_vmcnt<0>();                         // no copy into LDS outlives the workgroup
+}
+
+template <int TP, int TQ, int WP, int WQ, int S, bool SW, bool GROUPED>
+hipError_t launch_tile(const I8Args &a, hipStream_t st) {
+    using T = I8Tile<TP, TQ, WP, WQ, S>;
+    static std::atomic<uint64_t> done{0};
+    auto fn = i8_tile_kernel<TP, TQ, WP, WQ, S, SW, GROUPED>;
+    hipError_t e = raise_lds_limit(done, (const void *)fn, (int)T::Smem);
+    if (e != hipSuccess) return e;
+    constexpr int TC = SW ? TP / 2 : TP;
+    const int64_t rows = GROUPED ? a.g.max_tiles : (a.M + TQ - 1) / TQ;
+    const int64_t items = rows * ((a.n_out + TC - 1) / TC);
+    int64_t grid = (int64_t)device_cu_count() * (2 * T::Smem <= 160 * 1024 ? 2 : 1);
+    if (grid > items) grid = items;
+    grid = (grid + 7) / 8 * 8;
+    fn<<<(unsigned)grid, 64 * WP * WQ, T::Smem, st>>>(a);
+    return hipGetLastError();
+}
+
 template <bool SW, bool GROUPED>
 hipError_t launch(const I8Args &a, hipStream_t st) {
-    const int64_t rows = GROUPED ? a.g.sorted_cap / a.g.block_m : (a.M + 31) / 32;
-    const dim3 grid((a.n_out + (SW ? 7 : 15)) / (SW ? 8 : 16), (unsigned)rows);
-    i8_stream_kernel<2, 8, SW, GROUPED><<<grid, 512, 0, st>>>(a);
-    return hipGetLastError();
+    if (a.stream_nq) {
+        const int64_t rows = GROUPED ? a.g.sorted_cap / a.g.block_m : (a.M + 31) / 32;
+        const dim3 grid((a.n_out + (SW ? 7 : 15)) / (SW ? 8 : 16), (unsigned)rows);
+        i8_stream_kernel<2, 8, SW, GROUPED><<<grid, 512, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    if (GROUPED) {
+        hipError_t e = launch_group_prep(a.g, st);
+        if (e != hipSuccess) return e;
+    }
+    switch (a.tile_rows) {
+        case 256: return launch_tile<256, 256, 2, 2, 2, SW, GROUPED>(a, st);
+        case 128: return launch_tile<256, 128, 2, 2, 3, SW, GROUPED>(a, st);
+        case 64: return launch_tile<256, 64, 4, 1, 4, SW, GROUPED>(a, st);
+        default: return launch_tile<256, 32, 4, 1, 4, SW, GROUPED>(a, st);
+    }
 }
 
 }  // namespace
 
 size_t i8_workspace(I8Args &a, void *ws) {
-    if (a.grouped) group_divider(a.g);
-    return 0;
+    const int64_t rows = a.grouped ? a.g.R : a.M;
+    a.stream_nq = rows <= 64 || (a.grouped && a.g.R <= 16 * a.g.E) ? 2 : 0;
+    const int64_t per = a.grouped ? (a.g.R + a.g.E - 1) / a.g.E : a.M;
+    a.tile_rows = per > 128 ? 256 : per > 64 ? 128 : per > 32 ? 64 : 32;
+    if (!a.grouped) return 0;
+    group_divider(a.g);
+    if (a.stream_nq) return 0;
+    return group_tiles_workspace(a.g, a.tile_rows, ws);
 }
 
 hipError_t launch_i8(const I8Args &a, hipStream_t st) {

@@ -663,7 +663,7 @@ moe_status moe_quant_i8(const void *x, int32_t dtype, int64_t M, int64_t K, int6
  * The sums are exact 32-bit integers (any int8 codes, -128 too); scales, bias,
  * activation (as moe_fp8_linear's: with MOE_ACT_SWIGLU rows [0, N/2) of w are the
  * gate and rows [N/2, N) the up projection, and there are N/2 output columns)
- * and residual are FP32, with one rounding.  Results depend on no schedule.
+ * and residual are FP32, with one rounding.
  *   x_q [M, K] (per route [M * top_k, K]) int8, x_s one FP32 per row;
  *   w [N, K] or [E, N, K] int8, w_s and bias (or NULL) [N] or [E, N] FP32;
  *   out / y BF16 or FP16 (out_dtype / y_dtype), residual [M, ld_res] of the same

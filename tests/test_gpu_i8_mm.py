@@ -192,6 +192,13 @@ def test_linear_larger(M, N, K, act):
     p.check(p())
 
 
+@pytest.mark.parametrize("M,N,K,act", [(3000, 5000, 2064, "none"), (700, 20000, 1024, "swiglu"), (300, 30000, 1040, "silu"),
+                                       (5000, 4000, 640, "swiglu")])
+def test_several_tiles_a_workgroup(M, N, K, act):
+    p = Linear(M, N, K, act)
+    p.check(p())
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 16, 131056), (40, 64, 131056), (300, 70, 131056)])
 def test_largest_sums(M, N, K):
     """-128 times -128 over the longest contraction: 2147221504, no overflow."""
