@@ -22,20 +22,13 @@ __device__ __forceinline__ v4i mfma64(const u32x4 &a, const u32x4 &b, const v4i 
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a), __builtin_bit_cast(v4i, b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ float widen16(bool f16, uint32_t v) {
-    return f16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)v) : bf16_bits_to_f32(v & 0xffffu);
-}
-__device__ __forceinline__ uint16_t narrow16(bool f16, float v) {
-    return (uint16_t)(f16 ? to16x2<true>(v, 0.f) : to16x2<false>(v, 0.f));
-}
-
 // ----------------------------------------------------------------- few rows
 
 // 16 weight rows (with SwiGLU 8 gate and their 8 up rows) x 16 NQ rows of x;
 // wave w takes the steps of 128 values of K w, w + NW, ...; the waves' sums
 // are added in LDS.  Rows past the end read another row: their results are
 // not stored.  Values past the end of K are zeros on the weights' side.
-template <int NQ, int NW, bool SW, bool GROUPED>
+template <int NQ, int NW, bool F16, bool SW, bool GROUPED>
 __global__ void __launch_bounds__(64 * NW)
 i8_stream_kernel(I8Args a) {
     __shared__ int sums[NW][16 * NQ * 17];
@@ -112,8 +105,8 @@ i8_stream_kernel(I8Args a) {
             } else {
                 z = act1(z, a.act);
             }
-            if (a.res) z += widen16(a.f16, a.res[r * a.ld_res + col]);
-            a.out[r * a.ld_out + col] = narrow16(a.f16, z);
+            if (a.res) z += widen<F16>(a.res[r * a.ld_res + col]);
+            a.out[r * a.ld_out + col] = (uint16_t)to16x2<F16>(z, 0.f);
         }
         __syncthreads();
         if (!GROUPED) break;
@@ -141,6 +134,7 @@ struct I8Tile {
     static constexpr int JP = PB / 1024 / NW, JQ = QB / 1024 / NW, J = JP + JQ;
     static constexpr int NP = TP / WP / 16, NQ = TQ / WQ / 16;
     static constexpr size_t Smem = (size_t)S * Stage;
+    static constexpr bool Ragged = TP * TQ < 256 * 256;      // output columns no multiple of 8
     static_assert(NP % 4 == 0 && NW == 4 && JP % 2 == 0 && JQ >= 1 && Smem <= 160 * 1024, "tile");
 };
 
@@ -181,7 +175,7 @@ __device__ __forceinline__ void load8(const float *p, int c, int n, float (&f)[8
     }
 }
 
-template <int TP, int TQ, int WP, int WQ, int S, bool SW, bool GROUPED>
+template <int TP, int TQ, int WP, int WQ, int S, bool F16, bool SW, bool GROUPED>
 __global__ void __launch_bounds__(64 * WP * WQ, 1)
 i8_tile_kernel(I8Args a) {
     using T = I8Tile<TP, TQ, WP, WQ, S>;
@@ -339,74 +333,102 @@ i8_tile_kernel(I8Args a) {
     };
     // (emits no more than the wait for a load: one that some path leaves pending
     // would be waited for in the loop over the stages, together with all copies)
-    const float g1 = a.act == kActGelu ? -2.30220818f : -1.44269504f, g3 = a.act == kActGelu ? -0.10294324f : 0.f;
     auto arrived = [](float v) { asm volatile("" : : "v"(v)); };
+    const float g1 = a.act == kActGelu ? -2.30220818f : -1.44269504f, g3 = a.act == kActGelu ? -0.10294324f : 0.f;
+    // Everything is read before the first store, the residual in batches of NB
+    // rows: loads and stores are counted together, so a wait for a load waits for
+    // every store before it.  The code is unrolled (registers have no index) and
+    // kept small: beyond the instruction cache it costs its misses on every tile
+    // (with both output types and ragged ends 80 KB, 17 us a tile of 256 x 256).
+    constexpr int NT = NP / (SW ? 4 : 2), NB = NQ < 4 || NT > 2 ? 2 : 4;     // column groups of 32; rows of a batch
     auto epilogue = [&](const Item &it) __attribute__((always_inline)) {
         const float *ws = a.ws + (int64_t)it.e * a.N, *bias = a.bias ? a.bias + (int64_t)it.e * a.N : nullptr;
+        const int c0 = it.c0 + wp * (TC / WP) + 8 * grp;      // the lane's columns: c0 + 32 t + [0, 8)
         int rr[NQ];
-        float xs[NQ];
+        float xs[NQ], s[NT][8], b[NT][8], su[SW ? NT : 1][8], bu[SW ? NT : 1][8];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            rr[n] = out_row(it, wq * (TQ / WQ) + 16 * n + i16);
-            xs[n] = rr[n] < 0 ? 0.f : a.xs[x_row(rr[n])];
-        }
+        for (int n = 0; n < NQ; ++n) rr[n] = out_row(it, wq * (TQ / WQ) + 16 * n + i16);
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) arrived(xs[n]);
-        static_for<NP / (SW ? 4 : 2)>([&](auto tc) __attribute__((always_inline)) {
-            constexpr int ct = decltype(tc)::value, t = SW ? 2 * ct : ct;
-            const int c = it.c0 + wp * (TC / WP) + ct * 32 + 8 * grp;
-            if (c >= a.n_out) return;
-            float s[8], b[8], su[8], bu[8];
-            load8(ws, c, a.n_out, s);
-            if (SW) load8(ws + a.n_out, c, a.n_out, su);
-#pragma unroll
-            for (int v = 0; v < 8; ++v) b[v] = bu[v] = 0.f;
-            if (bias) {
-                load8(bias, c, a.n_out, b);
-                if (SW) load8(bias + a.n_out, c, a.n_out, bu);
-            }
+        for (int t = 0; t < NT; ++t) {
+            load8(ws, c0 + 32 * t, a.n_out, s[t]);
+            if (SW) load8(ws + a.n_out, c0 + 32 * t, a.n_out, su[t]);
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
-                arrived(s[v]);
-                arrived(b[v]);
-                if (SW) arrived(su[v]);
-                if (SW) arrived(bu[v]);
+                b[t][v] = 0.f;
+                if (SW) bu[t][v] = 0.f;
+            }
+            if (bias) {
+                load8(bias, c0 + 32 * t, a.n_out, b[t]);
+                if (SW) load8(bias + a.n_out, c0 + 32 * t, a.n_out, bu[t]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) xs[n] = rr[n] < 0 ? 0.f : a.xs[x_row(rr[n])];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) arrived(xs[n]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                arrived(s[t][v]);
+                arrived(b[t][v]);
+                if (SW) arrived(su[t][v]);
+                if (SW) arrived(bu[t][v]);
+            }
+        static_for<NQ / NB>([&](auto nc) __attribute__((always_inline)) {
+            constexpr int n0 = decltype(nc)::value * NB;
+            u32x4 q[NB][NT];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) q[n][t] = u32x4{0u, 0u, 0u, 0u};
+            if (a.res) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const uint16_t *res = a.res + (int64_t)rr[n0 + n] * a.ld_res + c0;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (rr[n0 + n] >= 0 && c0 + 32 * t + 8 <= a.n_out)
+                            q[n][t] = *reinterpret_cast<const u32x4_any *>(res + 32 * t);
+                }
             }
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
+            for (int n = 0; n < NB; ++n) {
                 __builtin_amdgcn_sched_barrier(0);
                 // (emits nothing: not moved to vector registers before)
 #pragma unroll
-                for (int m = 0; m < (SW ? 4 : 2); ++m) asm volatile("" : "+a"(acc[2 * t + m][n]));
-                if (rr[n] < 0) continue;
-                float z[8];
+                for (int m = 0; m < NP; ++m) asm volatile("" : "+a"(acc[m][n0 + n]));
+                uint16_t *d = a.out + (int64_t)rr[n0 + n] * a.ld_out + c0;
 #pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                    z[v] = (float)acc[2 * t + (v >> 2)][n][v & 3] * xs[n] * s[v] + b[v];
-                    if (SW)
-                        z[v] = silu(z[v]) * ((float)acc[2 * t + 2 + (v >> 2)][n][v & 3] * xs[n] * su[v] + bu[v]);
-                }
-                if (!SW && a.act != kActNone) {
+                for (int t = 0; t < NT; ++t) {
+                    const int c = c0 + 32 * t;
+                    float z[8], r[8];
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) z[v] = gated(z[v], g1, g3);
-                }
-                uint16_t *d = a.out + (int64_t)rr[n] * a.ld_out + c;
-                const uint16_t *res = a.res ? a.res + (int64_t)rr[n] * a.ld_res + c : nullptr;
-                if (c + 8 <= a.n_out) {
-                    if (res) {
-                        const u32x4 q = *reinterpret_cast<const u32x4_any *>(res);
-#pragma unroll
-                        for (int v = 0; v < 8; ++v) z[v] += widen16(a.f16, v & 1 ? q[v >> 1] >> 16 : q[v >> 1]);
+                    for (int v = 0; v < 8; ++v) {
+                        const int m = (SW ? 4 : 2) * t + (v >> 2);
+                        z[v] = (float)acc[m][n0 + n][v & 3] * xs[n0 + n] * s[t][v] + b[t][v];
+                        if (SW) z[v] = silu(z[v]) * ((float)acc[m + (SW ? 2 : 0)][n0 + n][v & 3] * xs[n0 + n] *
+                                                         su[SW ? t : 0][v] + bu[SW ? t : 0][v]);
                     }
-                    u32x4 o;
+                    if (!SW && a.act != kActNone) {
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        o[v] = a.f16 ? to16x2<true>(z[2 * v], z[2 * v + 1]) : to16x2<false>(z[2 * v], z[2 * v + 1]);
-                    *reinterpret_cast<u32x4_any *>(d) = o;
-                } else {
+                        for (int v = 0; v < 8; ++v) z[v] = gated(z[v], g1, g3);
+                    }
+                    if (a.res) {
+                        widen8<F16>(q[n][t], r);
 #pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        if (c + v < a.n_out) d[v] = narrow16(a.f16, res ? z[v] + widen16(a.f16, res[v]) : z[v]);
+                        for (int v = 0; v < 8; ++v) z[v] += r[v];
+                    }
+                    if (rr[n0 + n] < 0) continue;
+                    if (c + 8 <= a.n_out) {
+                        *reinterpret_cast<u32x4_any *>(d + 32 * t) = narrow8<F16>(z);
+                    } else if (T::Ragged) {
+                        const uint16_t *res = a.res ? a.res + (int64_t)rr[n0 + n] * a.ld_res + c : nullptr;
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            if (c + v < a.n_out)
+                                d[32 * t + v] = (uint16_t)to16x2<F16>(res ? z[v] + widen<F16>(res[v]) : z[v], 0.f);
+                    }
                 }
             }
         });
@@ -460,11 +482,11 @@ i8_tile_kernel(I8Args a) {
     wait_vmcnt<0>();                         // no copy into LDS outlives the workgroup
 }
 
-template <int TP, int TQ, int WP, int WQ, int S, bool SW, bool GROUPED>
+template <int TP, int TQ, int WP, int WQ, int S, bool F16, bool SW, bool GROUPED>
 hipError_t launch_tile(const I8Args &a, hipStream_t st) {
     using T = I8Tile<TP, TQ, WP, WQ, S>;
     static std::atomic<uint64_t> done{0};
-    auto fn = i8_tile_kernel<TP, TQ, WP, WQ, S, SW, GROUPED>;
+    auto fn = i8_tile_kernel<TP, TQ, WP, WQ, S, F16, SW, GROUPED>;
     hipError_t e = raise_lds_limit(done, (const void *)fn, (int)T::Smem);
     if (e != hipSuccess) return e;
     constexpr int TC = SW ? TP / 2 : TP;
@@ -477,12 +499,12 @@ hipError_t launch_tile(const I8Args &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <bool SW, bool GROUPED>
+template <bool F16, bool SW, bool GROUPED>
 hipError_t launch(const I8Args &a, hipStream_t st) {
     if (a.stream_nq) {
         const int64_t rows = GROUPED ? a.g.sorted_cap / a.g.block_m : (a.M + 31) / 32;
         const dim3 grid((a.n_out + (SW ? 7 : 15)) / (SW ? 8 : 16), (unsigned)rows);
-        i8_stream_kernel<2, 8, SW, GROUPED><<<grid, 512, 0, st>>>(a);
+        i8_stream_kernel<2, 8, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a);
         return hipGetLastError();
     }
     if (GROUPED) {
@@ -490,11 +512,18 @@ hipError_t launch(const I8Args &a, hipStream_t st) {
         if (e != hipSuccess) return e;
     }
     switch (a.tile_rows) {
-        case 256: return launch_tile<256, 256, 2, 2, 2, SW, GROUPED>(a, st);
-        case 128: return launch_tile<256, 128, 2, 2, 3, SW, GROUPED>(a, st);
-        case 64: return launch_tile<256, 64, 4, 1, 4, SW, GROUPED>(a, st);
-        default: return launch_tile<256, 32, 4, 1, 4, SW, GROUPED>(a, st);
+        case 256: return launch_tile<256, 256, 2, 2, 2, F16, SW, GROUPED>(a, st);
+        case 128: return launch_tile<256, 128, 2, 2, 3, F16, SW, GROUPED>(a, st);
+        case 64: return launch_tile<256, 64, 4, 1, 4, F16, SW, GROUPED>(a, st);
+        default: return launch_tile<256, 32, 4, 1, 4, F16, SW, GROUPED>(a, st);
     }
+}
+
+template <bool F16>
+hipError_t launch_type(const I8Args &a, hipStream_t st) {
+    const bool sw = a.act == kActSwiglu;
+    if (a.grouped) return sw ? launch<F16, true, true>(a, st) : launch<F16, false, true>(a, st);
+    return sw ? launch<F16, true, false>(a, st) : launch<F16, false, false>(a, st);
 }
 
 }  // namespace
@@ -503,17 +532,13 @@ size_t i8_workspace(I8Args &a, void *ws) {
     const int64_t rows = a.grouped ? a.g.R : a.M;
     a.stream_nq = rows <= 64 || (a.grouped && a.g.R <= 16 * a.g.E) ? 2 : 0;
     const int64_t per = a.grouped ? (a.g.R + a.g.E - 1) / a.g.E : a.M;
-    a.tile_rows = per > 128 ? 256 : per > 64 ? 128 : per > 32 ? 64 : 32;
+    a.tile_rows = per > 128 && a.n_out % 8 == 0 ? 256 : per > 64 ? 128 : per > 32 ? 64 : 32;
     if (!a.grouped) return 0;
     group_divider(a.g);
     if (a.stream_nq) return 0;
     return group_tiles_workspace(a.g, a.tile_rows, ws);
 }
 
-hipError_t launch_i8(const I8Args &a, hipStream_t st) {
-    const bool sw = a.act == kActSwiglu;
-    if (a.grouped) return sw ? launch<true, true>(a, st) : launch<false, true>(a, st);
-    return sw ? launch<true, false>(a, st) : launch<false, false>(a, st);
-}
+hipError_t launch_i8(const I8Args &a, hipStream_t st) { return a.f16 ? launch_type<true>(a, st) : launch_type<false>(a, st); }
 
 }  // namespace moe

@@ -11,27 +11,6 @@ namespace moe {
 
 namespace {
 
-template <bool F16>
-__device__ __forceinline__ float widen(uint32_t v) {
-    if constexpr (F16) return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
-    else return bf16_bits_to_f32(v & 0xffffu);
-}
-template <bool F16>
-__device__ __forceinline__ void widen8(const u32x4 &r, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = widen<F16>(r[i]);
-        f[2 * i + 1] = widen<F16>(r[i] >> 16);
-    }
-}
-template <bool F16>
-__device__ __forceinline__ u32x4 narrow8(const float (&f)[8]) {
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = to16x2<F16>(f[2 * i], f[2 * i + 1]);
-    return o;
-}
-
 // ----------------------------------------------------------- codes of rows
 //   s = max(max |x| / 127, 2^-126),  code = round(x * (1 / s)), ties to even
 // with IEEE divisions.  The largest magnitude is found on the bits, where a

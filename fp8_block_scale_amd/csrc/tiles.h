@@ -18,6 +18,28 @@ __device__ __forceinline__ uint32_t to16x2(float lo, float hi) {
     else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2bf));
 }
 
+// 16-bit values (FP16, else BF16) and FP32, one and eight at once.
+template <bool F16>
+__device__ __forceinline__ float widen(uint32_t v) {
+    if constexpr (F16) return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
+    else return bf16_bits_to_f32(v & 0xffffu);
+}
+template <bool F16>
+__device__ __forceinline__ void widen8(const u32x4 &r, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = widen<F16>(r[i]);
+        f[2 * i + 1] = widen<F16>(r[i] >> 16);
+    }
+}
+template <bool F16>
+__device__ __forceinline__ u32x4 narrow8(const float (&f)[8]) {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = to16x2<F16>(f[2 * i], f[2 * i + 1]);
+    return o;
+}
+
 // Activations of the products' epilogues (FP32; the reciprocal and exp2
 // instructions are within one unit in the last place).
 __device__ __forceinline__ float silu(float z) {
