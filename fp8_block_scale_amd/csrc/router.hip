@@ -8,6 +8,7 @@
 // One wave routes one token.
 #include "common.h"
 #include "router.h"
+#include "wave.h"
 
 namespace moe {
 
@@ -56,42 +57,32 @@ __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(
 
 // Lane layout: a group's experts lie with 2^sh lanes; lane p of group g holds
 // experts g n + p, g n + p + 2^sh, ... (n experts a group).
-template <int DT, int NPL>
-__global__ void __launch_bounds__(256)
-route_scored_kernel(ScoreArgs a, int sh) {
+struct Lanes {
+    int n, g, p, sh;
+    __device__ __forceinline__ int expert(int i) const { return g * n + p + (i << sh); }
+    __device__ __forceinline__ bool holds(int i) const { return p + (i << sh) < n; }
+};
+
+// Chooses in 64 bits: lane r < top_k gets the expert of rank r (-1: none is
+// left).  mx: the largest logit; total: the softmax's denominator (0: to be
+// computed).
+template <int NPL>
+__device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, const float (&l)[NPL], float mx,
+                                        double total) {
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= a.M) return;
-    const int n = a.E / a.n_group, g = lane >> sh, p = lane & ((1 << sh) - 1);
-    const int64_t row = t * a.ld;
-    auto expert = [&](int i) { return g * n + p + (i << sh); };
-    float l[NPL];
-    float mx = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        l[i] = -INFINITY;
-        if (g < a.n_group && p + (i << sh) < n) {
-            l[i] = load_logit<DT>(a.logits, row + expert(i));
-            l[i] = usable(l[i]) ? finite(l[i]) : -INFINITY;
-        }
-        mx = fmaxf(mx, l[i]);
-    }
-    double total = 0.0;
-    if (a.score == kScoreSoftmax) {
-        mx = wave_max(mx);
+    if (a.score == kScoreSoftmax && total == 0.0) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
             if (usable(l[i])) total += exp((double)l[i] - (double)mx);
         total = wave_sum(total);
     }
-    // choice keys; 0: not to be chosen
-    uint64_t key[NPL];
+    uint64_t key[NPL];                           // 0: not to be chosen
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         key[i] = 0;
         if (!usable(l[i])) continue;
         double c = a.score == kScoreSoftmax ? exp((double)l[i] - (double)mx) / total : sigmoid64(l[i]);
-        if (a.bias) c += (double)a.bias[expert(i)];
+        if (a.bias) c += (double)a.bias[ln.expert(i)];
         if (c > -INFINITY) key[i] = ordered64(c);
     }
     auto value = [](uint64_t k) {
@@ -109,7 +100,7 @@ route_scored_kernel(ScoreArgs a, int sh) {
         };
 #pragma unroll
         for (int i = 0; i < NPL; ++i) merge(key[i]);
-        for (int d = 1; d < 1 << sh; d <<= 1) {
+        for (int d = 1; d < 1 << ln.sh; d <<= 1) {
             const uint64_t o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
             merge(o1);
             merge(o2);
@@ -118,8 +109,8 @@ route_scored_kernel(ScoreArgs a, int sh) {
         if (b1) sc = a.group_top == 2 && b2 ? ordered64(value(b1) + value(b2)) : b1;
         int rank = 0;
         for (int h = 0; h < a.n_group; ++h) {
-            const uint64_t o = __shfl(sc, h << sh, 64);
-            rank += o > sc || (o == sc && h < g);
+            const uint64_t o = __shfl(sc, h << ln.sh, 64);
+            rank += o > sc || (o == sc && h < ln.g);
         }
         if (rank >= a.topk_group) {
 #pragma unroll
@@ -134,7 +125,7 @@ route_scored_kernel(ScoreArgs a, int sh) {
         for (int i = 0; i < NPL; ++i)
             if (key[i] > bk) {
                 bk = key[i];
-                be = expert(i);
+                be = ln.expert(i);
             }
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) {
@@ -149,23 +140,202 @@ route_scored_kernel(ScoreArgs a, int sh) {
         if (lane == r) sel = be;
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
-            if (expert(i) == be && p + (i << sh) < n) key[i] = 0;
+            if (ln.expert(i) == be && ln.holds(i)) key[i] = 0;
     }
+    return sel;
+}
+
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// The two largest of a group's values in every lane of the group (v1 >= v2 are
+// the lane's own): in rows of 16 lanes by DPP, beyond by permutes.
+__device__ __forceinline__ void group_top2(float &v1, float &v2, int sh) {
+    auto merge = [&](float o1, float o2) {
+        const float lo = fminf(v1, o1);
+        v1 = fmaxf(v1, o1);
+        v2 = fmaxf(lo, fmaxf(v2, o2));
+    };
+#define MOE_TOP2(ctrl)                                                                                          \
+    merge(__uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v1), ctrl, 0xF, 0xF, false)),          \
+          __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v2), ctrl, 0xF, 0xF, false)))
+    if (sh > 0) MOE_TOP2(0xB1);                  // quad [1,0,3,2]
+    if (sh > 1) MOE_TOP2(0x4E);                  // quad [2,3,0,1]
+    if (sh > 2) MOE_TOP2(0x141);                 // half-row mirror
+    if (sh > 3) MOE_TOP2(0x140);                 // row mirror
+#undef MOE_TOP2
+    for (int d = 16; d < 1 << sh; d <<= 1) {
+        const float o1 = __shfl_xor(v1, d, 64), o2 = __shfl_xor(v2, d, 64);
+        merge(o1, o2);
+    }
+}
+
+// The same choice in FP32 where it is sure to be the one in 64 bits; `sure` says
+// whether it is.  Two cases:
+//   plain  no bias and no sums of scores: larger logits have larger scores, so the
+//          logits themselves are compared.  Sure if the logits lie where 64 bits
+//          tell the scores of different ones apart ([-700, 20], and a softmax's
+//          within 700 of the largest) and those compared are equal or 2^-40 apart.
+//   else   choice scores in FP32.  A sigmoid is off by less than 8 * 2^-24 of itself
+//          (its exponent is exact; exp, sum and quotient), a softmax's score by
+//          less than (D + NPL + 16) 2^-24 (the exponent, up to D, is rounded; NPL + 6
+//          additions of the denominator), the sum with the bias by 2^-24 more of the
+//          result, and a score is at most |c| + |bias|.  Sure if those compared are
+//          further apart than both errors (a group's score has two of each).
+// Compared are neighbours in the ranking, the last one chosen and the best one
+// not chosen, and the worst group kept and the best one not kept.
+template <int NPL>
+__device__ __forceinline__ int choose32(const ScoreArgs &a, const Lanes &ln, const float (&l)[NPL], float mx,
+                                        bool &sure) {
+    const int lane = threadIdx.x & 63;
+    const bool grouped = a.topk_group < a.n_group;
+    const bool plain = !a.bias && !(grouped && a.group_top == 2);
+    const bool soft = a.score == kScoreSoftmax;
+    float c[NPL], bmax = 0.f, tol = 0x1p-20f;
+    sure = true;
+    float low = 0.f;                             // the smallest usable logit
+    if (plain || soft) {
+        low = INFINITY;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (usable(l[i])) low = fminf(low, l[i]);
+        low = unordered(wave_min_u32(ordered_bits(low)));
+    }
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) c[i] = l[i];
+        // (nobody usable: mx = -inf)
+        sure = soft ? mx - low < 700.f || mx == -INFINITY : mx <= 20.f && low >= -700.f;
+    } else {
+        float inv = 0.f;
+        float e[NPL];
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            e[i] = usable(l[i]) ? (soft ? expf(l[i] - mx) : 1.0f / (1.0f + expf(-l[i]))) : 0.f;
+        if (soft) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) sum += e[i];
+            inv = 1.0f / wave_sum(sum);
+            tol = (fminf(mx - low, 104.f) + (float)(NPL + 16)) * 0x1p-23f;
+        }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            c[i] = -INFINITY;
+            if (!usable(l[i])) continue;
+            const float b = a.bias ? a.bias[ln.expert(i)] : 0.f;
+            c[i] = (soft ? e[i] * inv : e[i]) + b;
+            if (!(c[i] > -INFINITY)) c[i] = -INFINITY;
+            else bmax = fmaxf(bmax, fabsf(b));
+        }
+        bmax = unordered(wave_max_u32(ordered_bits(bmax)));
+        // (an infinite bias: bmax = inf, nothing is sure)
+        sure = bmax < INFINITY;
+    }
+    auto apart = [&](float hi, float lo, float biases) {     // hi >= lo; a negative one is at most its biases
+        const float gap = hi - lo;
+        return plain ? gap == 0.f || gap >= 0x1p-40f : gap > tol * (fabsf(hi) + biases * bmax) + 0x1p-120f;
+    };
+    if (grouped) {
+        float v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            v2 = fmaxf(v2, fminf(v1, c[i]));
+            v1 = fmaxf(v1, c[i]);
+        }
+        group_top2(v1, v2, ln.sh);
+        const float sc = a.group_top == 2 && v2 > -INFINITY ? v1 + v2 : v1;
+        int rank = 0;
+        for (int h = 0; h < a.n_group; ++h) {
+            const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sc), h << ln.sh));
+            rank += o > sc || (o == sc && h < ln.g);
+        }
+        const bool there = ln.g < a.n_group, kept = rank < a.topk_group;
+        const float worst = unordered(wave_min_u32(ordered_bits(there && kept ? sc : INFINITY)));
+        const float best = unordered(wave_max_u32(ordered_bits(there && !kept ? sc : -INFINITY)));
+        if (best > -INFINITY) sure = sure && apart(worst, best, 4.f);
+        if (!kept) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) c[i] = -INFINITY;
+        }
+    }
+    uint32_t key[NPL];                           // 0: not to be chosen
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) key[i] = c[i] > -INFINITY ? ordered_bits(c[i] + 0.0f) : 0u;
+    int sel = -1;
+    float above = 0.f;
+    for (int r = 0; r <= a.top_k; ++r) {         // (one past the last, to compare)
+        uint32_t bk = 0;
+        int be = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (key[i] > bk) {
+                bk = key[i];
+                be = ln.expert(i);
+            }
+        const uint32_t top = wave_max_u32(bk);
+        if (top == 0) break;
+        const float v = unordered(top);
+        if (r > 0) sure = sure && apart(above, v, 2.f);
+        above = v;
+        if (r == a.top_k) break;
+        const uint64_t who = __ballot(bk == top);
+        int e;
+        if ((who & (who - 1)) == 0) e = __builtin_amdgcn_readlane(be, __builtin_ctzll(who));
+        else e = (int)wave_min_u32(bk == top ? (uint32_t)be : 0xFFFFFFFFu);
+        if (lane == r) sel = e;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (ln.expert(i) == e && ln.holds(i)) key[i] = 0;
+    }
+    return sel;
+}
+
+template <int DT, int NPL>
+__global__ void __launch_bounds__(256)
+route_scored_kernel(ScoreArgs a, int sh) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= a.M) return;
+    const Lanes ln = {a.E / a.n_group, lane >> sh, lane & ((1 << sh) - 1), sh};
+    const int64_t row = t * a.ld;
+    float l[NPL];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+        l[i] = ln.g < a.n_group && ln.holds(i) ? load_logit<DT>(a.logits, row + ln.expert(i)) : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        l[i] = usable(l[i]) ? finite(l[i]) : -INFINITY;
+        mx = fmaxf(mx, l[i]);
+    }
+    mx = unordered(wave_max_u32(ordered_bits(mx)));
+    double total = 0.0;
+    if (a.score == kScoreSoftmax && !a.renorm) {             // (renormalised weights need no denominator)
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (usable(l[i])) total += exp((double)l[i] - (double)mx);
+        total = wave_sum(total);
+    }
+    bool sure;
+    int sel = choose32(a, ln, l, mx, sure);
+    if (!sure) sel = choose64(a, ln, l, mx, total);
     // weights: lane j holds slot j
     double s = 0.0;
     const float ls = sel >= 0 ? finite(load_logit<DT>(a.logits, row + sel)) : -INFINITY;
     if (a.renorm) {
         // up to a factor that renormalising takes out, so that not all underflow
-        const float m = a.score == kScoreSoftmax ? wave_max(ls) : fminf(wave_max(ls), 0.f);
+        const float top = unordered(wave_max_u32(ordered_bits(ls)));
+        const float m = a.score == kScoreSoftmax ? top : fminf(top, 0.f);
         if (sel >= 0)
             s = a.score == kScoreSoftmax ? exp((double)ls - (double)m)
                                          : 1.0 / (exp((double)m) + exp((double)m - (double)ls));
+        double sum = s;                          // over the lanes that hold a slot
+        for (int d = 1; d < a.top_k; d <<= 1) sum += __shfl_xor(sum, d, 64);
+        s = sum > 0.0 ? s / sum : 0.0;
     } else if (sel >= 0) {
         s = a.score == kScoreSoftmax ? exp((double)ls - (double)mx) / total : sigmoid64(ls);
-    }
-    if (a.renorm) {
-        const double sum = wave_sum(s);
-        s = sum > 0.0 ? s / sum : 0.0;
     }
     const int kk = a.top_k + a.n_shared;
     if (lane < a.top_k) {

@@ -105,6 +105,36 @@ def test_ties_go_to_the_lowest(score, E, k, G, tg, gt):
     check_route(torch.zeros((3, E), device=DEV), k, score, n_group=G, topk_group=tg, group_top=gt)
 
 
+@pytest.mark.parametrize("score", list(SCORE))
+@pytest.mark.parametrize("E,k,G,tg,gt", [(64, 8, 1, 1, 2), (128, 6, 8, 4, 2), (128, 6, 8, 4, 1), (288, 16, 1, 1, 1)])
+@pytest.mark.parametrize("gap", [0.0, 1e-12, 1e-9, 1e-7, 1e-5])
+def test_choices_that_nearly_agree(score, E, k, G, tg, gt, gap):
+    """Choice scores within some gaps of each other, by a bias that evens the
+    scores out as far as FP32 goes, and by logits that differ by little."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(E + k)
+    l = torch.randn((1, E), generator=g, device=DEV) * 2
+    s = torch.sigmoid(l.double()) if score == "sigmoid" else torch.softmax(l.double(), 1)
+    bias = (0.5 - s + gap * torch.randn((1, E), generator=g, device=DEV).double())[0].float()
+    kw = dict(n_group=G, topk_group=tg, group_top=gt)
+    check_route(l, k, score, bias, **kw)
+    for base in (0.0, 1.0, -30.0):
+        near = (base + gap * torch.randn((40, E), generator=g, device=DEV).double()).float()
+        check_route(near, k, score, **kw)
+        check_route(near, k, score, torch.zeros(E, device=DEV), **kw)
+
+
+@pytest.mark.parametrize("score", list(SCORE))
+def test_wide_logits(score):
+    """Far apart: scores that underflow in FP32, and beyond where 64 bits tell them apart."""
+    for spread in (15.0, 80.0, 300.0, 900.0):
+        l = torch.linspace(-1, 1, 96, device=DEV).repeat(3, 1) * spread
+        l = l[:, torch.randperm(96, generator=torch.Generator().manual_seed(3)).to(DEV)].contiguous()
+        check_route(l, 12, score)
+        check_route(l, 12, score, n_group=8, topk_group=2)
+        check_route(l, 12, score, bias_of(96, 1), n_group=8, topk_group=4)
+
+
 def test_softmax_renormalised_is_the_plan_router():
     l = logits_of(500, 288, 4)
     ids, w = route(l, 8, "softmax", n_shared=1, routed_scaling=2.5)
