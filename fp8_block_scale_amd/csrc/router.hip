@@ -63,25 +63,37 @@ struct Lanes {
     __device__ __forceinline__ bool holds(int i) const { return p + (i << sh) < n; }
 };
 
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, 0xF, 0xF, false);
+    return (uint64_t)hi << 32 | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+
+// The lowest expert e that the lanes `who` (one at least) hold.
+__device__ __forceinline__ int pick(uint64_t who, int e) {
+    if ((who & (who - 1)) == 0) return __builtin_amdgcn_readlane(e, __builtin_ctzll(who));
+    return (int)wave_min_u32((who >> (threadIdx.x & 63)) & 1 ? (uint32_t)e : 0xFFFFFFFFu);
+}
+
 // Chooses in 64 bits: lane r < top_k gets the expert of rank r (-1: none is
-// left).  mx: the largest logit; total: the softmax's denominator (0: to be
-// computed).
+// left).  mx: the largest logit.
 template <int NPL>
-__device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, const float (&l)[NPL], float mx,
-                                        double total) {
+__device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, const float (&l)[NPL], float mx) {
     const int lane = threadIdx.x & 63;
-    if (a.score == kScoreSoftmax && total == 0.0) {
+    const bool soft = a.score == kScoreSoftmax;
+    double s[NPL], total = 0.0;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (usable(l[i])) total += exp((double)l[i] - (double)mx);
-        total = wave_sum(total);
+    for (int i = 0; i < NPL; ++i) {
+        s[i] = usable(l[i]) ? exp(soft ? (double)l[i] - (double)mx : -(double)l[i]) : 0.0;
+        total += s[i];
     }
+    if (soft) total = wave_sum(total);
     uint64_t key[NPL];                           // 0: not to be chosen
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         key[i] = 0;
         if (!usable(l[i])) continue;
-        double c = a.score == kScoreSoftmax ? exp((double)l[i] - (double)mx) / total : sigmoid64(l[i]);
+        double c = (soft ? s[i] : 1.0) / (soft ? total : 1.0 + s[i]);
         if (a.bias) c += (double)a.bias[ln.expert(i)];
         if (c > -INFINITY) key[i] = ordered64(c);
     }
@@ -90,26 +102,27 @@ __device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, con
     };
     if (a.topk_group < a.n_group) {
         uint64_t b1 = 0, b2 = 0;                 // the two largest of the group
-        auto merge = [&](uint64_t x) {
-            if (x > b1) {
-                b2 = b1;
-                b1 = x;
-            } else if (x > b2) {
-                b2 = x;
-            }
+        auto merge = [&](uint64_t o1, uint64_t o2) {
+            const uint64_t lo = b1 < o1 ? b1 : o1, hi = b1 < o1 ? o1 : b1, two = b2 < o2 ? o2 : b2;
+            b1 = hi;
+            b2 = lo < two ? two : lo;
         };
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) merge(key[i]);
-        for (int d = 1; d < 1 << ln.sh; d <<= 1) {
+        for (int i = 0; i < NPL; ++i) merge(key[i], 0);
+        if (ln.sh > 0) merge(dpp64<0xB1>(b1), dpp64<0xB1>(b2));       // quad [1,0,3,2]
+        if (ln.sh > 1) merge(dpp64<0x4E>(b1), dpp64<0x4E>(b2));       // quad [2,3,0,1]
+        if (ln.sh > 2) merge(dpp64<0x141>(b1), dpp64<0x141>(b2));     // half-row mirror
+        if (ln.sh > 3) merge(dpp64<0x140>(b1), dpp64<0x140>(b2));     // row mirror
+        for (int d = 16; d < 1 << ln.sh; d <<= 1) {
             const uint64_t o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
-            merge(o1);
-            merge(o2);
+            merge(o1, o2);
         }
         uint64_t sc = 0;
         if (b1) sc = a.group_top == 2 && b2 ? ordered64(value(b1) + value(b2)) : b1;
         int rank = 0;
         for (int h = 0; h < a.n_group; ++h) {
-            const uint64_t o = __shfl(sc, h << ln.sh, 64);
+            const uint64_t o = (uint64_t)__builtin_amdgcn_readlane((uint32_t)(sc >> 32), h << ln.sh) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((uint32_t)sc, h << ln.sh);
             rank += o > sc || (o == sc && h < ln.g);
         }
         if (rank >= a.topk_group) {
@@ -127,20 +140,20 @@ __device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, con
                 bk = key[i];
                 be = ln.expert(i);
             }
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) {
-            const uint64_t ok = __shfl_xor(bk, d, 64);
-            const int oe = __shfl_xor(be, d, 64);
-            if (ok > bk || (ok == bk && oe < be)) {
-                bk = ok;
-                be = oe;
-            }
+        // the largest high halves, of those the largest low halves, of those the
+        // lowest expert
+        const uint32_t hi = (uint32_t)(bk >> 32), top = wave_max_u32(hi);
+        if (top == 0) break;                     // nobody is left
+        uint64_t who = __ballot(hi == top);
+        if (who & (who - 1)) {
+            const uint32_t lo = hi == top ? (uint32_t)bk : 0u, low = wave_max_u32(lo);
+            who = __ballot(hi == top && lo == low);
         }
-        if (bk == 0) break;                      // the wave agrees: nobody is left
-        if (lane == r) sel = be;
+        const int e = pick(who, be);
+        if (lane == r) sel = e;
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
-            if (ln.expert(i) == be && ln.holds(i)) key[i] = 0;
+            if (ln.expert(i) == e && ln.holds(i)) key[i] = 0;
     }
     return sel;
 }
@@ -280,10 +293,7 @@ __device__ __forceinline__ int choose32(const ScoreArgs &a, const Lanes &ln, con
         if (r > 0) sure = sure && apart(above, v, 2.f);
         above = v;
         if (r == a.top_k) break;
-        const uint64_t who = __ballot(bk == top);
-        int e;
-        if ((who & (who - 1)) == 0) e = __builtin_amdgcn_readlane(be, __builtin_ctzll(who));
-        else e = (int)wave_min_u32(bk == top ? (uint32_t)be : 0xFFFFFFFFu);
+        const int e = pick(__ballot(bk == top), be);
         if (lane == r) sel = e;
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
@@ -320,7 +330,7 @@ route_scored_kernel(ScoreArgs a, int sh) {
     }
     bool sure;
     int sel = choose32(a, ln, l, mx, sure);
-    if (!sure) sel = choose64(a, ln, l, mx, total);
+    if (!sure) sel = choose64(a, ln, l, mx);
     // weights: lane j holds slot j
     double s = 0.0;
     const float ls = sel >= 0 ? finite(load_logit<DT>(a.logits, row + sel)) : -INFINITY;
