@@ -8,6 +8,7 @@
 // One wave routes one token.
 #include "common.h"
 #include "router.h"
+#include "tiles.h"
 #include "wave.h"
 
 namespace moe {
@@ -439,6 +440,103 @@ route_scored_bwd_kernel(ScoreArgs a) {
     }
 }
 
+// The same for weights whose gradient is 0 outside the slots, up to 16 of them: a
+// row of 16 lanes takes a token (its sums are DPP steps), a wave four.  The rows
+// of d_logits are put together in LDS and stored 16 bytes a lane: it is their
+// writing that bounds the kernel (16384 tokens of 256 experts, FP32: 16.8 MB).
+constexpr int kRowWaves = 2;
+
+// The sum over the lane's row of 16.
+__device__ __forceinline__ float row_sum(float v) {
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0xB1, 0xF, 0xF, false));
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x4E, 0xF, 0xF, false));
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x141, 0xF, 0xF, false));
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x140, 0xF, 0xF, false));
+    return v;
+}
+
+// s += v of row lane J where that holds the same expert; up to lane 15
+template <int J>
+__device__ __forceinline__ void add_same(int id, float v, int slots, float &s) {
+    if constexpr (J < 16) {
+        if (J < slots) {
+            const int ej = __builtin_amdgcn_update_dpp(0, id, 0x150 + J, 0xF, 0xF, false);      // row broadcast
+            const float vj =
+                __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x150 + J, 0xF, 0xF, false));
+            s += ej == id ? vj : 0.f;
+            add_same<J + 1>(id, v, slots, s);
+        }
+    }
+}
+
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+template <int DT>
+__global__ void __launch_bounds__(64 * kRowWaves)
+route_scored_bwd_rows_kernel(ScoreArgs a, int pitch) {
+    extern __shared__ __attribute__((aligned(16))) float rows[];      // [4 kRowWaves][pitch], pitch >= E, a multiple of 8
+    const int lane = threadIdx.x & 63, j = lane & 15;
+    const int64_t t0 = ((int64_t)blockIdx.x * kRowWaves + (threadIdx.x >> 6)) * 4, t = t0 + (lane >> 4);
+    float *const mine = rows + (threadIdx.x >> 6) * 4 * pitch;
+    for (int i = lane * 4; i < 4 * pitch; i += 256) *reinterpret_cast<v4f *>(mine + i) = v4f{0.f, 0.f, 0.f, 0.f};
+    int id = -1;
+    float av = 0.f, ls = -INFINITY;
+    if (t < a.M && j < a.slots) {
+        id = a.ids[t * a.slots + j];
+        av = a.dw[t * a.slots + j] * a.scale;
+        if (id < 0 || id >= a.E) id = -1;
+        if (id >= 0) ls = load_logit<DT>(a.logits, t * a.ld + id);
+    }
+    if (!usable(ls)) id = -1;                    // never chosen: weight 0, whatever its logit
+    ls = id >= 0 ? finite(ls) : -INFINITY;
+    if (id < 0) av = 0.f;
+    const float top = unordered(row_max_u32(ordered_bits(ls)));
+    float v;
+    if (a.score == kScoreSoftmax) {
+        const float ex = id >= 0 ? expf(ls - top) : 0.f;
+        const float sum = row_sum(ex);
+        const float q = sum > 0.f ? ex / sum : 0.f;
+        v = q * (av - row_sum(av * q));
+    } else {
+        // renormalised: s up to a factor, which cancels, so that not all underflow
+        const float m = a.renorm ? fminf(top, 0.f) : 0.f;
+        const float s = id >= 0 ? 1.0f / (expf(m) + expf(m - ls)) : 0.f;
+        const float rest = id >= 0 ? 1.0f / (1.0f + expf(ls)) : 0.f;
+        if (a.renorm) {
+            const float S = row_sum(s), as = row_sum(av * s);
+            av = S > 0.f ? (av - as / S) / S : 0.f;
+        }
+        v = s * rest * av;
+    }
+    // an expert listed twice: both lanes hold the same sum
+    float d = 0.f;
+    add_same<0>(id, v, a.slots, d);
+    __builtin_amdgcn_s_waitcnt(0xC07F);          // the zeros are written
+    __builtin_amdgcn_wave_barrier();
+    if (id >= 0) mine[(lane >> 4) * pitch + id] = d;
+    __builtin_amdgcn_wave_barrier();
+    constexpr int per = DT == kDtF32 ? 4 : 8;    // values of a 16-byte store
+    for (int r = 0; r < 4 && t0 + r < a.M; ++r)
+        for (int e = lane * per; e < a.E; e += 64 * per) {
+            const float *p = mine + r * pitch + e;
+            const int64_t at = (t0 + r) * a.ld_dl + e;
+            if (e + per <= a.E) {
+                u32x4 o;
+                if constexpr (DT == kDtF32) {
+                    o = *reinterpret_cast<const u32x4 *>(p);
+                    *reinterpret_cast<u32x4_any *>(static_cast<float *>(a.dl) + at) = o;
+                } else {
+                    float f[8];
+                    for (int i = 0; i < 8; ++i) f[i] = p[i];
+                    o = narrow8<DT == kDtF16>(f);
+                    *reinterpret_cast<u32x4_any *>(static_cast<uint16_t *>(a.dl) + at) = o;
+                }
+            } else {
+                for (int i = 0; e + i < a.E; ++i) store_grad<DT>(a.dl, at + i, p[i]);
+            }
+        }
+}
+
 template <int DT, int NPL>
 hipError_t launch_fwd(const ScoreArgs &a, int sh, hipStream_t st) {
     route_scored_kernel<DT, NPL><<<(unsigned)((a.M + 3) / 4), 256, 0, st>>>(a, sh);
@@ -464,6 +562,12 @@ hipError_t fwd(const ScoreArgs &a, hipStream_t st) {
 }
 template <int DT>
 hipError_t bwd(const ScoreArgs &a, hipStream_t st) {
+    if (!(a.score == kScoreSoftmax && !a.renorm) && a.slots <= 16) {
+        const int pitch = (a.E + 7) / 8 * 8;
+        const int64_t wgs = (a.M + 4 * kRowWaves - 1) / (4 * kRowWaves);
+        route_scored_bwd_rows_kernel<DT><<<(unsigned)wgs, 64 * kRowWaves, (size_t)pitch * 16 * kRowWaves, st>>>(a, pitch);
+        return hipGetLastError();
+    }
     if (a.E <= 128) return launch_bwd<DT, 2>(a, st);
     if (a.E <= 256) return launch_bwd<DT, 4>(a, st);
     if (a.E <= 512) return launch_bwd<DT, 8>(a, st);
