@@ -450,6 +450,7 @@ def moe_fp8_down_reduce(w2, w2_s, topk_weights, sorted_token_ids, expert_ids,
 # ------------------------------------------------- 16-bit grouped products --
 
 _DT = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
+_DT16 = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 
 
 def _need(cond, where, what):
@@ -464,6 +465,7 @@ def _need(cond, where, what):
 # call of a few microseconds).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launch(where, stream, tensors, *args):
@@ -482,7 +484,7 @@ def _launch(where, stream, tensors, *args):
         if stream.device_index != dev:
             raise MoeError(MOE_ERR_SHAPE, where, "the stream is on another device than the tensors")
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = _c[where](*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -648,9 +650,18 @@ def moe_fp8_linear(x_q, x_s, w, w_s, out, bias=None, residual=None, act=MOE_ACT_
 # ------------------------------------------------------ routing by scores --
 
 def _slots(where, name, t, dtype, shape):
-    _need(t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == shape, where,
-          f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    """The pointer of a dense operand of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise MoeError(MOE_ERR_SHAPE, where, f"{name} must be a contiguous {dtype} tensor of shape {shape}")
     return t.data_ptr()
+
+
+def _16bit(where, name, t):
+    """(rows, columns, pointer, leading dimension) of a bf16 or fp16 operand."""
+    if t.dim() != 2 or t.dtype not in _DT16:
+        raise MoeError(MOE_ERR_SHAPE, where, f"{name} must be a 2-d bf16 or fp16 tensor")
+    rows, cols = t.shape
+    return rows, cols, *_rows_arg(where, name, t, t.dtype, cols)
 
 
 def moe_route_scored(router_logits, top_k, topk_ids, topk_weights, score=MOE_SCORE_SIGMOID, bias=None,
@@ -704,17 +715,17 @@ _IDS = {torch.int32: MOE_IDS_I32, torch.int64: MOE_IDS_I64}
 
 def _combine_args(where, y, topk_weights, topk_ids, E):
     """(M, top_k, K, y's pointer and leading dimension, ids' pointer and type)"""
-    _need(y.dim() == 2 and y.dtype in (torch.bfloat16, torch.float16), where, "y must be a 2-d bf16 or fp16 tensor")
+    R, K, yp, ld_y = _16bit(where, "y", y)
     _need(topk_weights.dim() == 2, where, "topk_weights must be [M, top_k]")
     M, k = topk_weights.shape
-    _need(y.shape[0] == M * k, where, "y must have one row per route")
-    yp, ld_y = _rows_arg(where, "y", y, y.dtype, y.shape[1])
+    _need(R == M * k, where, "y must have one row per route")
     ip, dt = None, MOE_IDS_I32
     if topk_ids is not None:
-        _need(topk_ids.dtype in _IDS, where, "topk_ids must be int32 or int64")
+        dt = _IDS.get(topk_ids.dtype)
+        _need(dt is not None, where, "topk_ids must be int32 or int64")
         _need(E is not None, where, "topk_ids need E")
-        ip, dt = _slots(where, "topk_ids", topk_ids, topk_ids.dtype, (M, k)), _IDS[topk_ids.dtype]
-    return M, k, y.shape[1], yp, ld_y, ip, dt
+        ip = _slots(where, "topk_ids", topk_ids, topk_ids.dtype, (M, k))
+    return M, k, K, yp, ld_y, ip, dt
 
 
 def moe_combine(y, topk_weights, out, topk_ids=None, E=None, residual=None, stream=None):
@@ -758,9 +769,7 @@ def moe_quant_i8(x, x_q, x_s, stream=None):
     one scale a row, x_s fp32 [M]: s = max(amax / 127, 2^-126), codes rounded
     to nearest even.  Activations by token, or weights [N, K] by channel."""
     where = "moe_quant_i8"
-    _need(x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float16), where, "x must be a 2-d bf16 or fp16 tensor")
-    M, K = x.shape
-    xp, ld = _rows_arg(where, "x", x, x.dtype, K)
+    M, K, xp, ld = _16bit(where, "x", x)
     qp = _slots(where, "x_q", x_q, torch.int8, (M, K))
     sp = _slots(where, "x_s", x_s, torch.float32, (M,))
     _launch(where, stream, (x, x_q, x_s), xp, _DT[x.dtype], M, K, ld, qp, sp)
@@ -780,21 +789,22 @@ def moe_i8_linear(x_q, x_s, w, w_s, out, bias=None, residual=None, act=MOE_ACT_N
     _need(x_q.dim() == 2 and w.dim() == 2, where, "x_q and w must be 2-d")
     M, K = x_q.shape
     N = w.shape[0]
+    ot = out.dtype
     qp = _slots(where, "x_q", x_q, torch.int8, (M, K))
     wp = _slots(where, "w", w, torch.int8, (N, K))
     xsp = _slots(where, "x_s", x_s, torch.float32, (M,))
     wsp = _slots(where, "w_s", w_s, torch.float32, (N,))
     bp = None if bias is None else _slots(where, "bias", bias, torch.float32, (N,))
-    _need(out.dtype in (torch.bfloat16, torch.float16), where, "out must be bf16 or fp16")
+    _need(ot in _DT16, where, "out must be bf16 or fp16")
     n_out = N // 2 if act == MOE_ACT_SWIGLU else N
-    op, ld_out = _rows_arg(where, "out", out, out.dtype, n_out)
+    op, ld_out = _rows_arg(where, "out", out, ot, n_out)
     _need(out.shape[0] == M, where, "out and x_q disagree on M")
     rp, ld_res = None, 0
     if residual is not None:
-        rp, ld_res = _rows_arg(where, "residual", residual, out.dtype, n_out)
+        rp, ld_res = _rows_arg(where, "residual", residual, ot, n_out)
         _need(residual.shape[0] == M, where, "residual and x_q disagree on M")
     _launch(where, stream, (x_q, x_s, w, w_s, out, bias, residual, workspace), qp, xsp, wp, wsp, bp, rp, ld_res,
-            M, N, K, act, op, _DT[out.dtype], ld_out, *_ws(where, workspace))
+            M, N, K, act, op, _DT16[ot], ld_out, *_ws(where, workspace))
 
 
 def moe_i8_group_mm_workspace_size(M, K, N, E, top_k, block_m, sorted_cap, act=MOE_ACT_NONE,
@@ -817,16 +827,18 @@ def moe_i8_group_mm(x_q, x_s, w, w_s, sorted_token_ids, expert_ids, num_tokens_p
     wp = _slots(where, "w", w, torch.int8, (E, N, K))
     wsp = _slots(where, "w_s", w_s, torch.float32, (E, N))
     bp = None if bias is None else _slots(where, "bias", bias, torch.float32, (E, N))
-    qp = _slots(where, "x_q", x_q, torch.int8, (x_q.shape[0], K))
-    xsp = _slots(where, "x_s", x_s, torch.float32, (x_q.shape[0],))
-    _need(out.dtype in (torch.bfloat16, torch.float16), where, "out must be bf16 or fp16")
-    op, ld_out = _rows_arg(where, "out", out, out.dtype, N // 2 if act == MOE_ACT_SWIGLU else N)
+    rows = x_q.shape[0]
+    qp = _slots(where, "x_q", x_q, torch.int8, (rows, K))
+    xsp = _slots(where, "x_s", x_s, torch.float32, (rows,))
+    ot = out.dtype
+    _need(ot in _DT16, where, "out must be bf16 or fp16")
+    op, ld_out = _rows_arg(where, "out", out, ot, N // 2 if act == MOE_ACT_SWIGLU else N)
     R = out.shape[0]
     plan, cap = _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m)
     per_route = _x_rows(where, "x_q", x_q, R, top_k, x_per_route)
     _launch(where, stream, (x_q, x_s, w, w_s, out, bias, sorted_token_ids, expert_ids, num_tokens_post_padded,
                             workspace), qp, xsp, per_route, wp, wsp, bp, *plan, R // top_k, K, N, E, top_k,
-            block_m, cap, act, op, _DT[out.dtype], ld_out, *_ws(where, workspace))
+            block_m, cap, act, op, _DT16[ot], ld_out, *_ws(where, workspace))
 
 
 def moe_status_str(status):

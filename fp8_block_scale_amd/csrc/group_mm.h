@@ -42,6 +42,9 @@ struct GroupMmArgs {
     }
 };
 
+// Parts of at most `size` rows that an expert's rows give on average, for routes
+// spread evenly over the experts (rows of one: about normal, variance `rows`).
+double group_parts(double rows, int size);
 // Sets div_m and div_s (token_of) from top_k.
 void group_divider(GroupMmArgs &g);
 // Lays the workspace out at ws (NULL: sizes only) and returns its bytes.

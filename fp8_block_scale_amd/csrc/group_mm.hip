@@ -934,6 +934,15 @@ size_t group_tiles_workspace(GroupMmArgs &g, int tile_rows, void *ws) {
     return 256 + (size_t)g.max_tiles * 16;
 }
 
+double group_parts(double rows, int size) {
+    double per = 0;
+    if (rows > 32.0 * size) per = rows / size + 0.5;
+    else
+        for (int i = 0; i * size < rows + 5 * std::sqrt(rows) + 1; ++i)
+            per += 0.5 * std::erfc((i * size + 0.5 - rows) / std::sqrt(2 * rows));
+    return std::max(per, 1.0);
+}
+
 void group_divider(GroupMmArgs &g) {
     // r / top_k for 0 <= r < 2^31 by one high product: with s the least
     // number with 2^s >= top_k and m = floor(2^(31 + s) / top_k) + 1 (below
@@ -970,14 +979,7 @@ size_t group_mm_workspace(GroupMmArgs &g, void *ws) {
         double step;
     };
     static const Form forms[4] = {{256, 2.1}, {128, 0.95}, {64, 0.65}, {32, 0.55}};
-    auto parts = [&](int size) {                          // of at most `size` rows, of an expert
-        double per = 0;
-        if (rows > 32.0 * size) per = rows / size + 0.5;
-        else
-            for (int i = 0; i * size < rows + 5 * std::sqrt(rows) + 1; ++i)
-                per += 0.5 * std::erfc((i * size + 0.5 - rows) / std::sqrt(2 * rows));
-        return std::max(per, 1.0);
-    };
+    auto parts = [&](int size) { return group_parts(rows, size); };
     double t_tile = 1e300;
     g.tile_rows = 32;
     for (const Form &f : forms) {

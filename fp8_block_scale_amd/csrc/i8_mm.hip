@@ -7,6 +7,7 @@
 // The sums are 32-bit integers, exact for K < 2^17 (2^17 products of at most
 // 2^14); scales, bias, activation and residual are FP32, rounded once.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "i8_mm.h"
@@ -22,17 +23,27 @@ __device__ __forceinline__ v4i mfma64(const u32x4 &a, const u32x4 &b, const v4i 
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a), __builtin_bit_cast(v4i, b), c, 0, 0, 0);
 }
 
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
+
 // ----------------------------------------------------------------- few rows
 
-// 16 weight rows (with SwiGLU 8 gate and their 8 up rows) x 16 NQ rows of x;
-// wave w takes the steps of 128 values of K w, w + NW, ...; the waves' sums
-// are added in LDS.  Rows past the end read another row: their results are
-// not stored.  Values past the end of K are zeros on the weights' side.
-template <int NQ, int NW, bool F16, bool SW, bool GROUPED>
+// 16 weight rows (with SwiGLU 8 gate and their 8 up rows) x 16 NQ rows of x a
+// workgroup; grouped, a plan block's rows, 16 NQ at a time.  Wave w takes the
+// steps of 128 values of K w, w + NW, ...; U of them are loaded, straight into
+// registers, before the first is multiplied, and the waves' sums are added in
+// LDS.  Rows of x that differ (XL) go through the wave's share of LDS, 8 whole
+// rows of 128 bytes a copy: register loads touch 16 rows, 64 bytes of each.
+// Rows past the end read another row: their results are not stored.  Values past
+// the end of K are zeros on one side at least.
+template <int NQ, int NW, int U, bool XL, bool F16, bool SW, bool GROUPED>
 __global__ void __launch_bounds__(64 * NW)
 i8_stream_kernel(I8Args a) {
-    __shared__ int sums[NW][16 * NQ * 17];
+    // a wave's share of LDS: its rows of x (XL), then its sums [16 NQ][17]
+    constexpr int kSums = (NQ * 16 * 17 * 4 + 15) / 16 * 16, kRows = XL ? U * NQ * 2048 : 0;
+    constexpr int kWave = kRows > kSums ? kRows : kSums;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[NW * kWave];
     const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6), i16 = l & 15, grp = l >> 4;
+    uint8_t *const lds = smem + w * kWave;
     const int c0 = blockIdx.x * (SW ? 8 : 16);
     int row0 = blockIdx.y * (16 * NQ), rows_end = (int)a.M, e = 0;
     if (GROUPED) {
@@ -48,63 +59,103 @@ i8_stream_kernel(I8Args a) {
         const int c = c0 + (SW ? i & 7 : i);
         return (c < a.n_out ? c : a.n_out - 1) + (SW && i >= 8 ? a.n_out : 0);
     };
-    const int8_t *we = a.w + (int64_t)e * a.N * a.K;
-    const int8_t *ap = we + (int64_t)wrow(i16) * a.K + grp * 16;
+    const int8_t *ap = a.w + ((int64_t)e * a.N + wrow(i16)) * a.K + grp * 16;
     const u32x4 zero = {0u, 0u, 0u, 0u};
-    // the output row of row i of the pass (-1: none) and its row of x
+    // the output row of row i (-1: none) and its row of x
     auto out_row = [&](int i) -> int64_t {
         if (!GROUPED) return i < rows_end ? i : -1;
         const int r = i < rows_end ? a.g.sorted[i] : -1;
         return (uint32_t)r < (uint32_t)a.g.R ? r : -1;
     };
     auto x_row = [&](int64_t r) -> int64_t { return GROUPED && !a.g.per_route ? a.g.token_of((int)r) : r; };
+    constexpr int NR = XL ? 2 * NQ : NQ;         // the lane's rows of x
+    const int x_off = i16 * 128 + ((grp ^ (i16 & 7)) << 4);
     for (; row0 < rows_end; row0 += 16 * NQ) {
         const int64_t r0 = out_row(row0);
         if (r0 < 0) break;                       // sentinels end the segment
-        const int8_t *bp[NQ];
+        const int8_t *bp[NR];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            const int64_t r = out_row(row0 + 16 * n + i16);
-            bp[n] = a.xq + x_row(r < 0 ? r0 : r) * a.K + grp * 16;
+        for (int n = 0; n < NR; ++n) {
+            const int64_t r = out_row(row0 + (XL ? 8 * n + (l >> 3) : 16 * n + i16));
+            // (chunk c of row r lies at c ^ (r & 7) in LDS)
+            bp[n] = a.xq + x_row(r < 0 ? r0 : r) * a.K + (XL ? ((l & 7) ^ (l >> 3)) * 16 : grp * 16);
         }
         v4i acc[NQ];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) acc[n] = v4i{0, 0, 0, 0};
-        for (int k = w * 128; k < a.K; k += NW * 128) {
+        for (int k0 = w * 128; k0 < a.K; k0 += NW * U * 128) {
+            u32x4 av[U][2], x[U][NQ][2];
+            bool ok[U][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool ok = k + 64 * h + grp * 16 < a.K;
-                const int o = ok ? k + 64 * h : 0;
-                const u32x4 av = ok ? *reinterpret_cast<const u32x4 *>(ap + o) : zero;
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * NW * 128;
+                if (k >= a.K) break;
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
-                    acc[n] = mfma64(av, ok ? *reinterpret_cast<const u32x4 *>(bp[n] + o) : zero, acc[n]);
+                for (int h = 0; h < 2; ++h) {
+                    ok[u][h] = k + 64 * h + grp * 16 < a.K;
+                    const int o = ok[u][h] ? k + 64 * h : 0;
+                    av[u][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(ap + o));
+                    if (!XL) {
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) x[u][n][h] = *reinterpret_cast<const u32x4 *>(bp[n] + o);
+                    }
+                }
+                if (XL) {
+                    const bool in = k + ((l & 7) ^ (l >> 3)) * 16 < a.K;
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        lds_dma16(in ? (const void *)(bp[n] + k) : (const void *)kZeros, lds + (u * NR + n) * 1024);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);   // every load above is issued first
+            if (XL) {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the wave's own copies
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (k0 + u * NW * 128 >= a.K) break;
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        x[u][n][0] = lds_read16(lds + (u * NQ + n) * 2048 + x_off);
+                        x[u][n][1] = lds_read16(lds + (u * NQ + n) * 2048 + (x_off ^ 64));
+                    }
+                }
+                // read before the next steps' copies write there
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (k0 + u * NW * 128 >= a.K) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 v = ok[u][h] ? av[u][h] : zero;
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) acc[n] = mfma64(v, x[u][n][h], acc[n]);
+                }
             }
         }
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) sums[w][(n * 16 + i16) * 17 + 4 * grp + v] = acc[n][v];
+            for (int v = 0; v < 4; ++v) reinterpret_cast<int *>(lds)[(n * 16 + i16) * 17 + 4 * grp + v] = acc[n][v];
         __syncthreads();
         constexpr int COLS = SW ? 8 : 16;
         for (int i = tid; i < 16 * NQ * COLS; i += 64 * NW) {
             const int c = i % COLS, q = i / COLS, col = c0 + c;
             const int64_t r = out_row(row0 + q);
             if (r < 0 || col >= a.n_out) continue;
-            int s = 0, u = 0;
-            for (int k = 0; k < NW; ++k) {
-                s += sums[k][q * 17 + c];
-                if (SW) u += sums[k][q * 17 + c + 8];
-            }
             const float xs = a.xs[x_row(r)];
             const float *ws = a.ws + (int64_t)e * a.N, *bias = a.bias ? a.bias + (int64_t)e * a.N : nullptr;
-            float z = (float)s * xs * ws[col] + (bias ? bias[col] : 0.f);
-            if (SW) {
-                const int cu = col + a.n_out;
-                z = silu(z) * ((float)u * xs * ws[cu] + (bias ? bias[cu] : 0.f));
-            } else {
-                z = act1(z, a.act);
+            const float sc = ws[col], scu = SW ? ws[col + a.n_out] : 0.f;
+            const float b = bias ? bias[col] : 0.f, bu = SW && bias ? bias[col + a.n_out] : 0.f;
+            int s = 0, u = 0;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                const int *d = reinterpret_cast<const int *>(smem + k * kWave) + q * 17 + c;
+                s += d[0];
+                if (SW) u += d[8];
             }
+            float z = (float)s * xs * sc + b;
+            z = SW ? silu(z) * ((float)u * xs * scu + bu) : act1(z, a.act);
             if (a.res) z += widen<F16>(a.res[r * a.ld_res + col]);
             a.out[r * a.ld_out + col] = (uint16_t)to16x2<F16>(z, 0.f);
         }
@@ -137,8 +188,6 @@ struct I8Tile {
     static constexpr bool Ragged = TP * TQ < 256 * 256;      // output columns no multiple of 8
     static_assert(NP % 4 == 0 && NW == 4 && JP % 2 == 0 && JQ >= 1 && Smem <= 160 * 1024, "tile");
 };
-
-__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 0u};
 
 // SiLU (g1 = -log2 e, g3 = 0) and GELU (g1 = -2 sqrt(2 / pi) log2 e, g3 = 0.044715 g1)
 // in one form, z / (1 + 2^(g1 z + g3 z^3)): one copy of the epilogue's code.  (z^2
@@ -502,9 +551,14 @@ hipError_t launch_tile(const I8Args &a, hipStream_t st) {
 template <bool F16, bool SW, bool GROUPED>
 hipError_t launch(const I8Args &a, hipStream_t st) {
     if (a.stream_nq) {
-        const int64_t rows = GROUPED ? a.g.sorted_cap / a.g.block_m : (a.M + 31) / 32;
+        const int64_t rows = GROUPED ? a.g.sorted_cap / a.g.block_m : (a.M + 16 * a.stream_nq - 1) / (16 * a.stream_nq);
         const dim3 grid((a.n_out + (SW ? 7 : 15)) / (SW ? 8 : 16), (unsigned)rows);
-        i8_stream_kernel<2, 8, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a);
+        switch (a.stream_nq) {
+            case 1: i8_stream_kernel<1, 8, 2, true, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a); break;
+            case 2: i8_stream_kernel<2, 8, 2, true, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a); break;
+            case 3: i8_stream_kernel<3, 8, 1, true, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a); break;
+            default: i8_stream_kernel<4, 8, 1, true, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a);
+        }
         return hipGetLastError();
     }
     if (GROUPED) {
@@ -529,14 +583,64 @@ hipError_t launch_type(const I8Args &a, hipStream_t st) {
 }  // namespace
 
 size_t i8_workspace(I8Args &a, void *ws) {
-    const int64_t rows = a.grouped ? a.g.R : a.M;
-    a.stream_nq = rows <= 64 || (a.grouped && a.g.R <= 16 * a.g.E) ? 2 : 0;
-    const int64_t per = a.grouped ? (a.g.R + a.g.E - 1) / a.g.E : a.M;
-    a.tile_rows = per > 128 && a.n_out % 8 == 0 ? 256 : per > 64 ? 128 : per > 32 ? 64 : 32;
+    // The form by estimated time (us), the smallest first.  All constants are
+    // measured with weights from HBM where there are more than the caches hold.
+    const double steps = (a.K + 127) / 128;
+    const bool sw = a.act == kActSwiglu;
+    const double R = (double)(a.grouped ? a.g.R : a.M), E = a.grouped ? a.g.E : 1;
+    const double hit = E > 1 ? E * -std::expm1(R * std::log1p(-1.0 / E)) : 1;         // experts with a route
+    const double rows = R / hit, wbytes = hit * (double)a.N * (double)a.K;
+    auto parts = [&](int size) {                          // of at most `size` rows, of an expert
+        return a.grouped ? group_parts(rows, size) : std::ceil(rows / size);
+    };
+    // Few rows: a workgroup takes about 0.10, 0.13, 0.16 or 0.18 us for a step and 16,
+    // 32, 48 or 64 rows; with start and end 3.3.  Measured (us, by rows of a pass):
+    // K = 4096, N = 2048, 16 / 64 / 256 rows 6.2, 6.5, 7.2, 7.5 / 9.4, 7.4, 8.0, 9.8 /
+    // 29, 20, 19, 16; K = 1024, N = 8192, 64 rows 10.3, 8.9, 9.4, 6.9.
+    static const double few[4] = {0.10, 0.13, 0.16, 0.18};
+    double best = 1e300;
+    a.stream_nq = 0;
+    const int64_t blocks = a.grouped ? a.g.sorted_cap / a.g.block_m : 0;
+    for (int nq = 1; nq <= 4; ++nq) {
+        if (a.grouped ? blocks > 65535 : a.M > 1024) break;
+        const double wgs = hit * parts(a.grouped ? std::min(a.g.block_m, 16 * nq) : 16 * nq) *
+                           ((a.n_out + (sw ? 7 : 15)) / (sw ? 8 : 16));
+        const double t = 3.3 + std::max(std::max(wgs / 256, 1.0) * steps * few[nq - 1], wbytes / 4.3e6);
+        if (t < best) {
+            best = t;
+            a.stream_nq = nq;
+        }
+    }
+    // Tiles of 256 weight rows: a step of 128 of K takes `idle` us alone and `busy`
+    // with every CU at work, a tile's first copies and its epilogue `ends`; every
+    // row tile reads its weights, 5.4 TB/s of them.  Grouped, the set-up launch
+    // before takes 5.  Measured (us, 32 / 64 / 128 / 256 rows): K = 2048, N = 1000, 1000
+    // rows 11.4, 13.9, 18.1, 27.1; K = 7168, N = 4096, 512 and 2048 rows 39, 44, 52, 83
+    // and 147, 87, 59, 91; E = 288, K = 4096, N = 2048 with 14, 57, 114, 228 rows an
+    // expert 435, 426, 441, 583; 744, 510, 474, 608; 1193, 645, 528, 628; 1928, 1003,
+    // 773, 711.
+    struct Form {
+        int rows;
+        double idle, busy, ends;
+    };
+    static const Form forms[4] = {{32, 0.38, 0.60, 4}, {64, 0.39, 0.70, 5.5}, {128, 0.62, 0.98, 6}, {256, 1.04, 1.36, 9}};
+    a.tile_rows = 0;
+    for (const Form &f : forms) {
+        if (f.rows == 256 && a.n_out % 8 != 0) continue;      // (no code for ragged ends)
+        const double per = parts(f.rows), items = hit * per * ((a.N + 255) / 256);
+        const double step = f.idle + (f.busy - f.idle) * std::min(items / 256, 1.0), rounds = items / 256;
+        const double busy = (rounds < 4 ? std::ceil(rounds) : rounds + 0.5) * (steps * step + f.ends);
+        const double mem = per * wbytes / 5.4e6;
+        const double t = std::max(busy, mem) + 0.1 * std::min(busy, mem) + (a.grouped ? 5 : 0);
+        if (t < best) {
+            best = t;
+            a.tile_rows = f.rows;
+        }
+    }
+    if (a.tile_rows) a.stream_nq = 0;
     if (!a.grouped) return 0;
     group_divider(a.g);
-    if (a.stream_nq) return 0;
-    return group_tiles_workspace(a.g, a.tile_rows, ws);
+    return a.stream_nq ? 0 : group_tiles_workspace(a.g, a.tile_rows, ws);
 }
 
 hipError_t launch_i8(const I8Args &a, hipStream_t st) { return a.f16 ? launch_type<true>(a, st) : launch_type<false>(a, st); }
