@@ -172,21 +172,23 @@ i8_stream_kernel(I8Args a) {
 // With SwiGLU the tile holds, per 64 rows, 32 gate rows and then their 32 up
 // rows: both meet in one wave.
 //
-// A stage is 128 values of K of both operands in a ring of S slots in LDS, filled
-// by 16-byte global -> LDS copies, rows gathered by the plan on the way.  The
-// MFMAs of one half of a stage (64 values of K) run beside the LDS reads of the
-// next half, into the other register set.  A slot is free once every wave has
-// read its second half, in the middle of its own stage: the copies of the stage
-// S further on go out then, beside the second half's MFMAs.
-template <int TP, int TQ, int WP, int WQ, int S>
+// A stage is 128 values of K of both operands, in rings of SP slots (weights) and
+// SQ slots (rows of x) in LDS, filled by 16-byte global -> LDS copies, rows
+// gathered by the plan on the way.  The MFMAs of one half of a stage (64 values
+// of K) run beside the LDS reads of the next half, into the other register set.
+// A slot is free once every wave has read its second half, in the middle of its
+// own stage: the copies of the stages SQ and SP further on go out then, beside the
+// second half's MFMAs.  Weights, which come from HBM, are given the more time
+// where the LDS does not hold another slot of both.
+template <int TP, int TQ, int WP, int WQ, int SP, int SQ>
 struct I8Tile {
     static constexpr int NW = WP * WQ;
-    static constexpr int PB = TP * 128, QB = TQ * 128, Stage = PB + QB;
+    static constexpr int PB = TP * 128, QB = TQ * 128;
     static constexpr int JP = PB / 1024 / NW, JQ = QB / 1024 / NW, J = JP + JQ;
     static constexpr int NP = TP / WP / 16, NQ = TQ / WQ / 16;
-    static constexpr size_t Smem = (size_t)S * Stage;
+    static constexpr size_t Smem = (size_t)SP * PB + (size_t)SQ * QB;
     static constexpr bool Ragged = TP * TQ < 256 * 256;      // output columns no multiple of 8
-    static_assert(NP % 4 == 0 && NW == 4 && JP % 2 == 0 && JQ >= 1 && Smem <= 160 * 1024, "tile");
+    static_assert(NP % 4 == 0 && NW == 4 && JP % 2 == 0 && JQ >= 1 && Smem <= 160 * 1024 && SP >= SQ && SQ >= 2, "tile");
 };
 
 // SiLU (g1 = -log2 e, g3 = 0) and GELU (g1 = -2 sqrt(2 / pi) log2 e, g3 = 0.044715 g1)
@@ -224,10 +226,10 @@ __device__ __forceinline__ void load8(const float *p, int c, int n, float (&f)[8
     }
 }
 
-template <int TP, int TQ, int WP, int WQ, int S, bool F16, bool SW, bool GROUPED>
+template <int TP, int TQ, int WP, int WQ, int SP, int SQ, bool F16, bool SW, bool GROUPED>
 __global__ void __launch_bounds__(64 * WP * WQ, 1)
 i8_tile_kernel(I8Args a) {
-    using T = I8Tile<TP, TQ, WP, WQ, S>;
+    using T = I8Tile<TP, TQ, WP, WQ, SP, SQ>;
     constexpr int NW = T::NW, JP = T::JP, JQ = T::JQ, NP = T::NP, NQ = T::NQ;
     constexpr int TC = SW ? TP / 2 : TP;                      // output columns of a tile
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -238,7 +240,8 @@ i8_tile_kernel(I8Args a) {
     const int n_items = nrt * nct;
     const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
     const int end = (int)((int64_t)(xcd + 1) * n_items / 8);
-    int lit = (int)((int64_t)xcd * n_items / 8) + (blockIdx.x >> 3), cit = lit;
+    const int lit = (int)((int64_t)xcd * n_items / 8) + (blockIdx.x >> 3);
+    int cit = lit;
     if (cit >= end) return;
     const int nst = (a.K + 127) >> 7;                         // stages of an item
 
@@ -280,10 +283,10 @@ i8_tile_kernel(I8Args a) {
     const int64_t up = SW ? (int64_t)a.n_out * a.K : 0;       // from a gate row to its up row
     uint32_t poff[JP];
     const int8_t *qptr[JQ];
-    int lkt = 0;                             // stage of the item
-    auto load_setup = [&]() {
-        const Item it = item_of(lit);
-        lkt = 0;
+    int pit = lit, qit = lit, pkt = 0, qkt = 0;               // items of the copies, their stages
+    auto setup_p = [&]() {
+        const Item it = item_of(pit);
+        pkt = 0;
         pbase = a.w + ((int64_t)it.e * a.N + it.c0) * a.K;
         const int last = min(TC, a.n_out - it.c0) - 1;
 #pragma unroll
@@ -291,6 +294,10 @@ i8_tile_kernel(I8Args a) {
             const int c = (SW ? (j >> 1) * 32 + 8 * w : 8 * (j * NW + w)) + lrow;
             poff[j] = (uint32_t)min(c, last) * (uint32_t)a.K + (uint32_t)kc_p * 16u;
         }
+    };
+    auto setup_q = [&]() {
+        const Item it = item_of(qit);
+        qkt = 0;
 #pragma unroll
         for (int j = 0; j < JQ; ++j) {
             // a row that has no route reads row 0 of x, one past the last row
@@ -300,32 +307,39 @@ i8_tile_kernel(I8Args a) {
             qptr[j] = a.xq + (int64_t)x_row(r) * a.K + kc_q * 16;
         }
     };
-    // Copy c of the load side's stage to the slot.  `any`: the stage may reach past
-    // the end of K or lie past the last item, and is read as zeros there.
-    auto issue_copy = [&](auto any, int c, uint8_t *slot) __attribute__((always_inline)) {
-        const int left = a.K - lkt * 128;
-        const void *zero = kZeros;
-        if (c < JP) {
-            const void *p = pbase + (SW && (c & 1) ? up : 0) + poff[c];
-            if (decltype(any)::value && kc_p * 16 >= left) p = zero;
-            lds_dma16(p, slot + (c * NW + w) * 1024);
-        } else {
-            const void *p = qptr[c - JP];
-            if (decltype(any)::value && kc_q * 16 >= left) p = zero;
-            lds_dma16(p, slot + T::PB + ((c - JP) * NW + w) * 1024);
-        }
+    // Copy j of the next stage of weights or rows of x to its slot.  `any`: the stage
+    // may reach past the end of K or lie past the last item: zeros there.
+    auto copy_p = [&](auto any, int j, uint8_t *slot) __attribute__((always_inline)) {
+        const void *p = pbase + (SW && (j & 1) ? up : 0) + poff[j];
+        if (decltype(any)::value && kc_p * 16 >= a.K - pkt * 128) p = kZeros;
+        lds_dma16(p, slot + (j * NW + w) * 1024);
     };
-    auto next_k = [&]() {
-        ++lkt;
+    auto copy_q = [&](auto any, int j, uint8_t *slot) __attribute__((always_inline)) {
+        const void *p = qptr[j];
+        if (decltype(any)::value && kc_q * 16 >= a.K - qkt * 128) p = kZeros;
+        lds_dma16(p, slot + (j * NW + w) * 1024);
+    };
+    auto next_p = [&]() {
+        ++pkt;
         pbase += 128;
+    };
+    auto next_q = [&]() {
+        ++qkt;
 #pragma unroll
         for (int j = 0; j < JQ; ++j) qptr[j] += 128;
     };
-    auto stage_issued = [&]() {
-        next_k();
-        if (lkt == nst) {
-            lit += step;
-            if (lit < end) load_setup();
+    auto issued_p = [&]() {
+        next_p();
+        if (pkt == nst) {
+            pit += step;
+            if (pit < end) setup_p();
+        }
+    };
+    auto issued_q = [&]() {
+        next_q();
+        if (qkt == nst) {
+            qit += step;
+            if (qit < end) setup_q();
         }
     };
 
@@ -347,19 +361,18 @@ i8_tile_kernel(I8Args a) {
     };
     const int pf = (i16 & 3) | (((i16 >> 2) & 1) << 2);
     const int p_off = (wp * (TP / WP) + 8 * (i16 >> 2) + (i16 & 3)) * 128 + ((grp ^ pf) << 4);
-    const int q_off = T::PB + (wq * (TQ / WQ) + i16) * 128 + ((grp ^ (i16 & 7)) << 4);
+    const int q_off = (wq * (TQ / WQ) + i16) * 128 + ((grp ^ (i16 & 7)) << 4);
     u32x4 pa[2][NP], qb[2][NQ];
-    auto read_op = [&](const uint8_t *slot, int h, int i) {   // operand i of half h: columns', then rows'
-        if (i < NP) pa[h][i] = lds_read16(slot + (p_off ^ (h << 6)) + (i >> 1) * 32 * 128 + (i & 1) * 4 * 128);
-        else qb[h][i - NP] = lds_read16(slot + (q_off ^ (h << 6)) + (i - NP) * 16 * 128);
+    auto read_op = [&](const uint8_t *ps, const uint8_t *qs, int h, int i) {      // operand i of half h: weights, then x
+        if (i < NP) pa[h][i] = lds_read16(ps + (p_off ^ (h << 6)) + (i >> 1) * 32 * 128 + (i & 1) * 4 * 128);
+        else qb[h][i - NP] = lds_read16(qs + (q_off ^ (h << 6)) + (i - NP) * 16 * 128);
     };
     // The products of a stage in two halves of K, beside them the reads of the
-    // next half (the second half's from rd, then the next stage's first from nx)
-    // and in the second half the copies of the stage S further on to wr, which
-    // is rd's slot: `arrive` lies between.  (The pointers are declared not to
-    // alias: the compiler would wait for the copies in flight before each read.)
-    auto multiply = [&](auto any, const uint8_t *__restrict__ rd, const uint8_t *__restrict__ nx,
-                        uint8_t *__restrict__ wr, auto arrive) __attribute__((always_inline)) {
+    // next half (the second half's from ps and qs, then the next stage's first from
+    // pn and qn) and in the second half the copies, into the same ps and qs:
+    // `arrive` lies between.  Rows of x go first: they have less time.
+    auto multiply = [&](auto any, uint8_t *ps, uint8_t *qs, const uint8_t *pn, const uint8_t *qn, auto arrive)
+                        __attribute__((always_inline)) {
         constexpr int kReads = NP + NQ, kPer = (4 * kReads + 3 * NQ - 1) / (3 * NQ);      // in three quarters of the units
         constexpr int kCopy = (T::J + NQ - 1) / NQ;
         __builtin_amdgcn_s_waitcnt(0xC07F);                   // lgkmcnt(0): the first half's operands
@@ -369,10 +382,14 @@ i8_tile_kernel(I8Args a) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-                for (int i = n * kPer; i < (n + 1) * kPer && i < kReads; ++i) read_op(h ? nx : rd, h ^ 1, i);
+                for (int i = n * kPer; i < (n + 1) * kPer && i < kReads; ++i)
+                    read_op(h ? pn : ps, h ? qn : qs, h ^ 1, i);
                 if (h == 1) {
 #pragma unroll
-                    for (int c = n * kCopy; c < (n + 1) * kCopy && c < T::J; ++c) issue_copy(any, c, wr);
+                    for (int c = n * kCopy; c < (n + 1) * kCopy && c < T::J; ++c) {
+                        if (c < JQ) copy_q(any, c, qs);
+                        else copy_p(any, c - JQ, ps);
+                    }
                 }
 #pragma unroll
                 for (int m = 0; m < NP; ++m) acc[m][n] = mfma64(pa[h][m], qb[h][n], acc[m][n]);
@@ -483,36 +500,47 @@ i8_tile_kernel(I8Args a) {
         });
     };
 
-    // ---- the pipeline: S stages are in flight or being multiplied at any time
-    // (past the last they are copies of zeros: the count of copies to wait for
-    // stays the same, and no branch comes between the MFMAs)
-    load_setup();
-    for (int s = 0; s < S; ++s) {
+    // ---- the pipeline: SP stages of weights and SQ of rows of x are in flight or
+    // being multiplied at any time (past the last they are copies of zeros: the
+    // count of copies to wait for stays the same, and no branch comes between the
+    // MFMAs).  In each stage the copies of x go out before those of weights, so
+    // that those of weights alone may stay in flight beyond the next stage's.
+    uint8_t *const pring = smem, *const qring = smem + SP * T::PB;
+    setup_p();
+    setup_q();
+#pragma unroll 1
+    for (int s = 0; s < SP; ++s) {
 #pragma unroll
-        for (int c = 0; c < T::J; ++c) issue_copy(std::true_type(), c, smem + s * T::Stage);
-        stage_issued();
+        for (int j = 0; j < JP; ++j) copy_p(std::true_type(), j, pring + s * T::PB);
+        issued_p();
+        if (s < SQ) {
+#pragma unroll
+            for (int j = 0; j < JQ; ++j) copy_q(std::true_type(), j, qring + s * T::QB);
+            issued_q();
+        }
     }
     // the next stage's copies have landed for this wave, then for all; every
-    // wave has read the slot that the next copies overwrite
+    // wave has read the slots that the next copies overwrite
     auto arrive = [&](auto ahead) {          // `ahead` stages may stay in flight
-        constexpr int n = decltype(ahead)::value * T::J;
+        constexpr int n = decltype(ahead)::value * T::J + (SP - SQ) * JP;
         wait_vmcnt<(n < 63 ? n : 63)>();
         __builtin_amdgcn_s_waitcnt(0xC07F);                   // lgkmcnt(0)
         stage_barrier();
     };
-    int slot = 0;                            // of the stage that is being multiplied
-    arrive(std::integral_constant<int, S - 1>());
+    int pslot = 0, qslot = 0;                // of the stage that is being multiplied
+    arrive(std::integral_constant<int, SQ - 1>());
 #pragma unroll
-    for (int i = 0; i < NP + NQ; ++i) read_op(smem, 0, i);
+    for (int i = 0; i < NP + NQ; ++i) read_op(pring, qring, 0, i);
     auto stage = [&](auto any) __attribute__((always_inline)) {
-        uint8_t *const sp = smem + slot * T::Stage;
-        slot = slot + 1 == S ? 0 : slot + 1;
-        multiply(any, sp, smem + slot * T::Stage, sp, [&]() __attribute__((always_inline)) {
-            arrive(std::integral_constant<int, S - 2>());
+        uint8_t *const ps = pring + pslot * T::PB, *const qs = qring + qslot * T::QB;
+        pslot = pslot + 1 == SP ? 0 : pslot + 1;
+        qslot = qslot + 1 == SQ ? 0 : qslot + 1;
+        multiply(any, ps, qs, pring + pslot * T::PB, qring + qslot * T::QB, [&]() __attribute__((always_inline)) {
+            arrive(std::integral_constant<int, SQ - 2>());
         });
         keep();
     };
-    const int nsame = max(0, nst - S - 1);
+    const int nsame = max(0, nst - SP - 1);
     for (; cit < end; cit += step) {
         clear();
         keep();
@@ -520,22 +548,24 @@ i8_tile_kernel(I8Args a) {
         // not its last, then the rest
         for (int k = 0; k < nsame; ++k) {
             stage(std::false_type());
-            next_k();
+            next_p();
+            next_q();
         }
         for (int k = nsame; k < nst; ++k) {
             stage(std::true_type());
-            stage_issued();
+            issued_q();
+            issued_p();
         }
         epilogue(item_of(cit));
     }
     wait_vmcnt<0>();                         // no copy into LDS outlives the workgroup
 }
 
-template <int TP, int TQ, int WP, int WQ, int S, bool F16, bool SW, bool GROUPED>
+template <int TP, int TQ, int WP, int WQ, int SP, int SQ, bool F16, bool SW, bool GROUPED>
 hipError_t launch_tile(const I8Args &a, hipStream_t st) {
-    using T = I8Tile<TP, TQ, WP, WQ, S>;
+    using T = I8Tile<TP, TQ, WP, WQ, SP, SQ>;
     static std::atomic<uint64_t> done{0};
-    auto fn = i8_tile_kernel<TP, TQ, WP, WQ, S, F16, SW, GROUPED>;
+    auto fn = i8_tile_kernel<TP, TQ, WP, WQ, SP, SQ, F16, SW, GROUPED>;
     hipError_t e = raise_lds_limit(done, (const void *)fn, (int)T::Smem);
     if (e != hipSuccess) return e;
     constexpr int TC = SW ? TP / 2 : TP;
@@ -566,10 +596,10 @@ hipError_t launch(const I8Args &a, hipStream_t st) {
         if (e != hipSuccess) return e;
     }
     switch (a.tile_rows) {
-        case 256: return launch_tile<256, 256, 2, 2, 2, F16, SW, GROUPED>(a, st);
-        case 128: return launch_tile<256, 128, 2, 2, 3, F16, SW, GROUPED>(a, st);
-        case 64: return launch_tile<256, 64, 4, 1, 4, F16, SW, GROUPED>(a, st);
-        default: return launch_tile<256, 32, 4, 1, 4, F16, SW, GROUPED>(a, st);
+        case 256: return launch_tile<256, 256, 2, 2, 3, 2, F16, SW, GROUPED>(a, st);
+        case 128: return launch_tile<256, 128, 2, 2, 3, 3, F16, SW, GROUPED>(a, st);
+        case 64: return launch_tile<256, 64, 4, 1, 4, 4, F16, SW, GROUPED>(a, st);
+        default: return launch_tile<256, 32, 4, 1, 4, 4, F16, SW, GROUPED>(a, st);
     }
 }
 
