@@ -513,28 +513,33 @@ def _rows_arg(where, name, t, dtype, cols):
 def _group_plan(where, sorted_token_ids, expert_ids, num_tokens_post_padded, R, top_k, E, block_m):
     """The plan's pointers and the length that the kernels may trust."""
     for t in (sorted_token_ids, expert_ids, num_tokens_post_padded):
-        _need(t.dtype == torch.int32 and t.is_contiguous(), where, "the plan must be contiguous int32")
-    _need(num_tokens_post_padded.numel() >= 1, where, "num_tokens_post_padded is empty")
-    _need(top_k >= 1 and R % top_k == 0, where, "the routes are no multiple of top_k")
+        if t.dtype is not torch.int32 or not t.is_contiguous():
+            raise MoeError(MOE_ERR_SHAPE, where, "the plan must be contiguous int32")
+    if num_tokens_post_padded.numel() < 1:
+        raise MoeError(MOE_ERR_SHAPE, where, "num_tokens_post_padded is empty")
+    if top_k < 1 or R % top_k != 0:
+        raise MoeError(MOE_ERR_SHAPE, where, "the routes are no multiple of top_k")
     # A block's expert is read wherever the device's plan length says there is
     # one, within sorted_cap: so that is cut to the blocks that expert_ids has.
     # No plan is longer than any routing of these routes needs.
     cap = sorted_token_ids.numel()
     if block_m > 0 and cap % block_m == 0:
-        need = min(cap // block_m, -(-(R + min(E, R) * (block_m - 1)) // block_m))
-        _need(expert_ids.numel() >= need, where, "expert_ids shorter than the plan can need")
-        cap = min(cap, expert_ids.numel() * block_m)
+        have = expert_ids.numel()
+        if have < min(cap // block_m, -(-(R + min(E, R) * (block_m - 1)) // block_m)):
+            raise MoeError(MOE_ERR_SHAPE, where, "expert_ids shorter than the plan can need")
+        cap = min(cap, have * block_m)
     return (sorted_token_ids.data_ptr(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr()), cap
 
 
 def _x_rows(where, name, t, R, top_k, per_route):
     """Whether x / dx has one row per route (else one per token): as told, or
     (None) as its rows say, one per token if top_k is 1."""
+    rows = t.shape[0]
     if per_route is None:
-        per_route = t.shape[0] * top_k != R
-    _need(t.shape[0] == (R if per_route else R // top_k), where,
-          name + " must have one row per token or per route")
-    return int(bool(per_route))
+        per_route = rows * top_k != R
+    if rows != (R if per_route else R // top_k):
+        raise MoeError(MOE_ERR_SHAPE, where, name + " must have one row per token or per route")
+    return 1 if per_route else 0
 
 
 def _ws(where, workspace):
