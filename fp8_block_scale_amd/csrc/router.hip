@@ -6,6 +6,8 @@
 //   chosen: the top_k largest c; w_j = scale s_j, or scale s_j / sum of the chosen s
 //
 // One wave routes one token.
+#include <algorithm>
+
 #include "common.h"
 #include "router.h"
 #include "tiles.h"
@@ -576,11 +578,37 @@ hipError_t bwd(const ScoreArgs &a, hipStream_t st) {
 
 }  // namespace
 
+namespace {
+
+// A launch counts its threads in 32 bits: at most 2^25 tokens each.
+template <typename F>
+hipError_t in_parts(ScoreArgs a, F launch) {
+    const int64_t M = a.M, part = (int64_t)1 << 25, size = a.dtype == kDtF32 ? 4 : 2;
+    const int64_t slots = a.slots ? a.slots : a.top_k + a.n_shared;
+    for (int64_t t = 0; t < M; t += part) {
+        a.M = std::min(part, M - t);
+        const hipError_t e = launch(a);
+        if (e != hipSuccess) return e;
+        a.logits = static_cast<const uint8_t *>(a.logits) + part * a.ld * size;
+        a.ids += part * slots;
+        if (a.w) a.w += part * slots;
+        if (a.dw) a.dw += part * slots;
+        if (a.dl) a.dl = static_cast<uint8_t *>(a.dl) + part * a.ld_dl * size;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
 hipError_t launch_route_scored(const ScoreArgs &a, hipStream_t st) {
-    return a.dtype == kDtF32 ? fwd<kDtF32>(a, st) : a.dtype == kDtF16 ? fwd<kDtF16>(a, st) : fwd<kDtBf16>(a, st);
+    return in_parts(a, [st](const ScoreArgs &p) {
+        return p.dtype == kDtF32 ? fwd<kDtF32>(p, st) : p.dtype == kDtF16 ? fwd<kDtF16>(p, st) : fwd<kDtBf16>(p, st);
+    });
 }
 hipError_t launch_route_scored_bwd(const ScoreArgs &a, hipStream_t st) {
-    return a.dtype == kDtF32 ? bwd<kDtF32>(a, st) : a.dtype == kDtF16 ? bwd<kDtF16>(a, st) : bwd<kDtBf16>(a, st);
+    return in_parts(a, [st](const ScoreArgs &p) {
+        return p.dtype == kDtF32 ? bwd<kDtF32>(p, st) : p.dtype == kDtF16 ? bwd<kDtF16>(p, st) : bwd<kDtBf16>(p, st);
+    });
 }
 
 }  // namespace moe

@@ -24,52 +24,55 @@ __global__ void __launch_bounds__(256)
 quant_i8_kernel(QuantI8Args a) {
     __shared__ uint32_t part[4];
     const int tid = threadIdx.x % T;
-    const int64_t m = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
     const int nch = a.K >> 3;
-    const bool there = m < a.M;
-    const uint16_t *x = a.x + (there ? m : 0) * a.ld;
-    u32x4 r[CH];
-    uint32_t top = 0;
-    auto largest = [&](const u32x4 &v) {
+    for (int64_t m0 = (int64_t)blockIdx.x * (256 / T); m0 < a.M; m0 += (int64_t)gridDim.x * (256 / T)) {
+        const int64_t m = m0 + threadIdx.x / T;
+        const bool there = m < a.M;
+        const uint16_t *x = a.x + (there ? m : 0) * a.ld;
+        u32x4 r[CH];
+        uint32_t top = 0;
+        auto largest = [&](const u32x4 &v) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(v[i] & 0x7fffu, (v[i] >> 16) & 0x7fffu));
-    };
+            for (int i = 0; i < 4; ++i) top = max(top, max(v[i] & 0x7fffu, (v[i] >> 16) & 0x7fffu));
+        };
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int i = c * T + tid;
-        r[c] = i < nch ? *reinterpret_cast<const u32x4 *>(x + (int64_t)i * 8) : u32x4{0u, 0u, 0u, 0u};
+        for (int c = 0; c < CH; ++c) {
+            const int i = c * T + tid;
+            r[c] = i < nch ? *reinterpret_cast<const u32x4 *>(x + (int64_t)i * 8) : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) largest(r[c]);
+        if (LONG)
+            for (int i = CH * T + tid; i < nch; i += T) largest(*reinterpret_cast<const u32x4 *>(x + (int64_t)i * 8));
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
+        if constexpr (T > 64) {
+            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+            __syncthreads();
+            top = max(max(part[0], part[1]), max(part[2], part[3]));
+        }
+        if (T > 64) __syncthreads();             // (part is read before the next row writes it)
+        if (!there) continue;
+        const float amax = widen<F16>(top);
+        const float s = amax < INFINITY ? fmaxf(__fdiv_rn(amax, 127.0f), kFltMin) : amax;
+        const bool fin = s < INFINITY;               // else the codes are 0
+        const float inv = __fdiv_rn(1.0f, s);
+        if (tid == 0) a.xs[m] = s;
+        auto codes = [&](const u32x4 &v, int i) {
+            float f[8];
+            widen8<F16>(v, f);
+            uint32_t o[2] = {0u, 0u};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                o[j >> 2] |= ((uint32_t)(fin ? (int)rintf(f[j] * inv) : 0) & 0xffu) << (8 * (j & 3));
+            *reinterpret_cast<uint2 *>(a.xq + m * a.K + (int64_t)i * 8) = uint2{o[0], o[1]};
+        };
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (c * T + tid < nch) codes(r[c], c * T + tid);
+        if (LONG)
+            for (int i = CH * T + tid; i < nch; i += T) codes(*reinterpret_cast<const u32x4 *>(x + (int64_t)i * 8), i);
     }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) largest(r[c]);
-    if (LONG)
-        for (int i = CH * T + tid; i < nch; i += T) largest(*reinterpret_cast<const u32x4 *>(x + (int64_t)i * 8));
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
-    if constexpr (T > 64) {
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-        __syncthreads();
-        top = max(max(part[0], part[1]), max(part[2], part[3]));
-    }
-    if (!there) return;
-    const float amax = widen<F16>(top);
-    const float s = amax < INFINITY ? fmaxf(__fdiv_rn(amax, 127.0f), kFltMin) : amax;
-    const bool fin = s < INFINITY;               // else the codes are 0
-    const float inv = __fdiv_rn(1.0f, s);
-    if (tid == 0) a.xs[m] = s;
-    auto codes = [&](const u32x4 &v, int i) {
-        float f[8];
-        widen8<F16>(v, f);
-        uint32_t o[2] = {0u, 0u};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            o[j >> 2] |= ((uint32_t)(fin ? (int)rintf(f[j] * inv) : 0) & 0xffu) << (8 * (j & 3));
-        *reinterpret_cast<uint2 *>(a.xq + m * a.K + (int64_t)i * 8) = uint2{o[0], o[1]};
-    };
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-        if (c * T + tid < nch) codes(r[c], c * T + tid);
-    if (LONG)
-        for (int i = CH * T + tid; i < nch; i += T) codes(*reinterpret_cast<const u32x4 *>(x + (int64_t)i * 8), i);
 }
 
 // ---------------------------------------------------------------- combine
@@ -124,41 +127,45 @@ template <bool F16>
 __global__ void __launch_bounds__(256)
 combine_bwd_kernel(CombineArgs a, int64_t R) {
     const int lane = threadIdx.x & 63;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (r >= R) return;
-    if (!a.counts(r)) {
-        if (lane == 0) a.dw[r] = 0.f;
-        return;
-    }
-    const uint16_t *g = a.dout + r / a.top_k * a.ld_out, *y = a.y + r * a.ld_y;
-    uint16_t *dy = a.dy + r * a.ld_dy;
-    const float w = a.w[r];
-    const int nch = a.K >> 3;
-    float s[8];
-#pragma unroll
-    for (int v = 0; v < 8; ++v) s[v] = 0.f;
-    for (int i = lane; i < nch; i += 64) {
-        float gf[8], yf[8], d[8];
-        widen8<F16>(*reinterpret_cast<const u32x4 *>(g + (int64_t)i * 8), gf);
-        widen8<F16>(*reinterpret_cast<const u32x4 *>(y + (int64_t)i * 8), yf);
-#pragma unroll
-        for (int v = 0; v < 8; ++v) {
-            d[v] = w * gf[v];
-            s[v] = fmaf(gf[v], yf[v], s[v]);
+    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < R; r += (int64_t)gridDim.x * 4) {
+        if (!a.counts(r)) {
+            if (lane == 0) a.dw[r] = 0.f;
+            continue;
         }
-        *reinterpret_cast<u32x4 *>(dy + (int64_t)i * 8) = narrow8<F16>(d);
-    }
-    float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+        const uint16_t *g = a.dout + r / a.top_k * a.ld_out, *y = a.y + r * a.ld_y;
+        uint16_t *dy = a.dy + r * a.ld_dy;
+        const float w = a.w[r];
+        const int nch = a.K >> 3;
+        float s[8];
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
-    if (lane == 0) a.dw[r] = sum;
+        for (int v = 0; v < 8; ++v) s[v] = 0.f;
+        for (int i = lane; i < nch; i += 64) {
+            float gf[8], yf[8], d[8];
+            widen8<F16>(*reinterpret_cast<const u32x4 *>(g + (int64_t)i * 8), gf);
+            widen8<F16>(*reinterpret_cast<const u32x4 *>(y + (int64_t)i * 8), yf);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                d[v] = w * gf[v];
+                s[v] = fmaf(gf[v], yf[v], s[v]);
+            }
+            *reinterpret_cast<u32x4 *>(dy + (int64_t)i * 8) = narrow8<F16>(d);
+        }
+        float sum = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+        if (lane == 0) a.dw[r] = sum;
+    }
 }
+
+// Workgroups of a launch: they go round for more than 2^23 (a launch counts its
+// threads in 32 bits).
+unsigned blocks(int64_t n) { return (unsigned)std::min(n, (int64_t)1 << 23); }
 
 template <bool F16>
 hipError_t quant(const QuantI8Args &a, hipStream_t st) {
-    if (a.K <= 2048) quant_i8_kernel<F16, 64, 4, false><<<(unsigned)((a.M + 3) / 4), 256, 0, st>>>(a);
-    else if (a.K <= 8192) quant_i8_kernel<F16, 256, 4, false><<<(unsigned)a.M, 256, 0, st>>>(a);
-    else quant_i8_kernel<F16, 256, 4, true><<<(unsigned)a.M, 256, 0, st>>>(a);
+    if (a.K <= 2048) quant_i8_kernel<F16, 64, 4, false><<<blocks((a.M + 3) / 4), 256, 0, st>>>(a);
+    else if (a.K <= 8192) quant_i8_kernel<F16, 256, 4, false><<<blocks(a.M), 256, 0, st>>>(a);
+    else quant_i8_kernel<F16, 256, 4, true><<<blocks(a.M), 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -170,7 +177,7 @@ hipError_t launch_quant_i8(const QuantI8Args &a, hipStream_t st) {
 
 hipError_t launch_combine(const CombineArgs &a, hipStream_t st) {
     const int64_t chunks = a.M * (a.K >> 3);
-    const unsigned grid = (unsigned)std::min((chunks + 255) / 256, (int64_t)1 << 23);
+    const unsigned grid = blocks((chunks + 255) / 256);
     if (a.f16) combine_kernel<true><<<grid, 256, 0, st>>>(a, chunks);
     else combine_kernel<false><<<grid, 256, 0, st>>>(a, chunks);
     return hipGetLastError();
@@ -178,7 +185,7 @@ hipError_t launch_combine(const CombineArgs &a, hipStream_t st) {
 
 hipError_t launch_combine_bwd(const CombineArgs &a, hipStream_t st) {
     const int64_t R = a.M * a.top_k;
-    const unsigned grid = (unsigned)((R + 3) / 4);
+    const unsigned grid = blocks((R + 3) / 4);
     if (a.f16) combine_bwd_kernel<true><<<grid, 256, 0, st>>>(a, R);
     else combine_bwd_kernel<false><<<grid, 256, 0, st>>>(a, R);
     return hipGetLastError();

@@ -216,3 +216,15 @@ def test_more_than_2_to_32_elements():
     moe.moe_combine_bwd(out, y, w, dy, dw)
     assert torch.equal(dw[-1], K * torch.arange(1, k + 1, device=DEV, dtype=torch.float32)) and (dw[:-1] == 0).all()
     assert (dy[-k:] == 1).all() and (dy[:16] == 1).all()
+
+
+def test_more_rows_than_a_launch_counts():
+    """More workgroups than a launch takes: the kernel goes round (33.6 million
+    routes whose rows repeat every 2000)."""
+    p = Problem(1000, 8, 2, "bf16", ids=None, residual=False)
+    out, (dy, dw) = p.forward(), p.backward()
+    n = 16800
+    p.y, p.w, p.dout, p.M = p.y.repeat(n, 1), p.w.repeat(n, 1), p.dout.repeat(n, 1), 1000 * n
+    assert (p.forward().view(n, -1) == out.reshape(1, -1)).all()
+    bdy, bdw = p.backward()
+    assert (bdy.view(n, -1) == dy.reshape(1, -1)).all() and (bdw.view(n, -1) == dw.view(1, -1)).all()

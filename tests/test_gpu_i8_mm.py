@@ -95,6 +95,15 @@ def test_rows_that_are_not_finite():
     assert torch.isnan(out[1:4]).all() and torch.isfinite(out[0]).all() and torch.isfinite(out[4]).all()
 
 
+def test_more_rows_than_a_launch_counts():
+    """More workgroups than a launch takes: the kernel goes round (33.6 million rows
+    that repeat every 1000)."""
+    x = torch.randn((1000, 16), generator=gen(1), device=DEV).to(torch.bfloat16)
+    q, s = quant(x)
+    bq, bs = quant(x.repeat(33600, 1))
+    assert (bq.view(33600, -1) == q.view(1, -1)).all() and (bs.view(33600, -1) == s.view(1, -1)).all()
+
+
 # ----------------------------------------------------------------- products --
 
 def codes(shape, g):

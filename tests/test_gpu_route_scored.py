@@ -347,3 +347,20 @@ def test_no_tokens():
     l = torch.empty((0, 8), device=DEV)
     ids, w = route(l, 2, "sigmoid")
     moe.moe_route_scored_bwd(l, ids, w, torch.empty((0, 8), device=DEV))
+
+
+def test_more_tokens_than_a_launch_counts():
+    """More workgroups than a launch takes: the kernels go round (67.2 million tokens
+    whose logits repeat every 1000)."""
+    n, times = 1000, 67200
+    l = logits_of(n, 8, 17, "bf16")
+    ids, w = route(l, 2, "sigmoid")
+    dw = torch.randn(ids.shape, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    d = bwd(l, ids, dw, "sigmoid", True, 1.0)
+    dd = bwd(l, ids, dw, "softmax", False, 1.0)
+    big = l.repeat(times, 1)
+    bi, bw = route(big, 2, "sigmoid")
+    assert (bi.view(times, -1) == ids.view(1, -1)).all() and (bw.view(times, -1) == w.view(1, -1)).all()
+    bdw = dw.repeat(times, 1)
+    assert (bwd(big, bi, bdw, "sigmoid", True, 1.0).view(times, -1) == d.reshape(1, -1)).all()
+    assert (bwd(big, bi, bdw, "softmax", False, 1.0).view(times, -1) == dd.reshape(1, -1)).all()
