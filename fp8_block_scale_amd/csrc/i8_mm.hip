@@ -31,15 +31,15 @@ __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 
 // workgroup; grouped, a plan block's rows, 16 NQ at a time.  Wave w takes the
 // steps of 128 values of K w, w + NW, ...; U of them are loaded, straight into
 // registers, before the first is multiplied, and the waves' sums are added in
-// LDS.  Rows of x that differ (XL) go through the wave's share of LDS, 8 whole
-// rows of 128 bytes a copy: register loads touch 16 rows, 64 bytes of each.
+// LDS.  Rows of x go through the wave's share of LDS, 8 whole rows of 128 bytes a
+// copy: register loads touch 16 rows, 64 bytes of each.
 // Rows past the end read another row: their results are not stored.  Values past
 // the end of K are zeros on one side at least.
-template <int NQ, int NW, int U, bool XL, bool F16, bool SW, bool GROUPED>
+template <int NQ, int NW, int U, bool F16, bool SW, bool GROUPED>
 __global__ void __launch_bounds__(64 * NW)
 i8_stream_kernel(I8Args a) {
-    // a wave's share of LDS: its rows of x (XL), then its sums [16 NQ][17]
-    constexpr int kSums = (NQ * 16 * 17 * 4 + 15) / 16 * 16, kRows = XL ? U * NQ * 2048 : 0;
+    // a wave's share of LDS: its rows of x, then its sums [16 NQ][17]
+    constexpr int kSums = (NQ * 16 * 17 * 4 + 15) / 16 * 16, kRows = U * NQ * 2048;
     constexpr int kWave = kRows > kSums ? kRows : kSums;
     __shared__ __attribute__((aligned(16))) uint8_t smem[NW * kWave];
     const int tid = threadIdx.x, l = tid & 63, w = uni(tid >> 6), i16 = l & 15, grp = l >> 4;
@@ -68,7 +68,7 @@ i8_stream_kernel(I8Args a) {
         return (uint32_t)r < (uint32_t)a.g.R ? r : -1;
     };
     auto x_row = [&](int64_t r) -> int64_t { return GROUPED && !a.g.per_route ? a.g.token_of((int)r) : r; };
-    constexpr int NR = XL ? 2 * NQ : NQ;         // the lane's rows of x
+    constexpr int NR = 2 * NQ;                   // the lane's rows of x
     const int x_off = i16 * 128 + ((grp ^ (i16 & 7)) << 4);
     for (; row0 < rows_end; row0 += 16 * NQ) {
         const int64_t r0 = out_row(row0);
@@ -76,9 +76,9 @@ i8_stream_kernel(I8Args a) {
         const int8_t *bp[NR];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const int64_t r = out_row(row0 + (XL ? 8 * n + (l >> 3) : 16 * n + i16));
+            const int64_t r = out_row(row0 + 8 * n + (l >> 3));
             // (chunk c of row r lies at c ^ (r & 7) in LDS)
-            bp[n] = a.xq + x_row(r < 0 ? r0 : r) * a.K + (XL ? ((l & 7) ^ (l >> 3)) * 16 : grp * 16);
+            bp[n] = a.xq + x_row(r < 0 ? r0 : r) * a.K + ((l & 7) ^ (l >> 3)) * 16;
         }
         v4i acc[NQ];
 #pragma unroll
@@ -95,33 +95,25 @@ i8_stream_kernel(I8Args a) {
                     ok[u][h] = k + 64 * h + grp * 16 < a.K;
                     const int o = ok[u][h] ? k + 64 * h : 0;
                     av[u][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(ap + o));
-                    if (!XL) {
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n) x[u][n][h] = *reinterpret_cast<const u32x4 *>(bp[n] + o);
-                    }
                 }
-                if (XL) {
-                    const bool in = k + ((l & 7) ^ (l >> 3)) * 16 < a.K;
+                const bool in = k + ((l & 7) ^ (l >> 3)) * 16 < a.K;
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
-                        lds_dma16(in ? (const void *)(bp[n] + k) : (const void *)kZeros, lds + (u * NR + n) * 1024);
-                }
+                for (int n = 0; n < NR; ++n)
+                    lds_dma16(in ? (const void *)(bp[n] + k) : (const void *)kZeros, lds + (u * NR + n) * 1024);
             }
             __builtin_amdgcn_sched_barrier(0);   // every load above is issued first
-            if (XL) {
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the wave's own copies
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the wave's own copies
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (k0 + u * NW * 128 >= a.K) break;
+            for (int u = 0; u < U; ++u) {
+                if (k0 + u * NW * 128 >= a.K) break;
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        x[u][n][0] = lds_read16(lds + (u * NQ + n) * 2048 + x_off);
-                        x[u][n][1] = lds_read16(lds + (u * NQ + n) * 2048 + (x_off ^ 64));
-                    }
+                for (int n = 0; n < NQ; ++n) {
+                    x[u][n][0] = lds_read16(lds + (u * NQ + n) * 2048 + x_off);
+                    x[u][n][1] = lds_read16(lds + (u * NQ + n) * 2048 + (x_off ^ 64));
                 }
-                // read before the next steps' copies write there
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             }
+            // read before the next steps' copies write there
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (k0 + u * NW * 128 >= a.K) break;
@@ -584,10 +576,10 @@ hipError_t launch(const I8Args &a, hipStream_t st) {
         const int64_t rows = GROUPED ? a.g.sorted_cap / a.g.block_m : (a.M + 16 * a.stream_nq - 1) / (16 * a.stream_nq);
         const dim3 grid((a.n_out + (SW ? 7 : 15)) / (SW ? 8 : 16), (unsigned)rows);
         switch (a.stream_nq) {
-            case 1: i8_stream_kernel<1, 8, 2, true, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a); break;
-            case 2: i8_stream_kernel<2, 8, 2, true, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a); break;
-            case 3: i8_stream_kernel<3, 8, 1, true, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a); break;
-            default: i8_stream_kernel<4, 8, 1, true, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a);
+            case 1: i8_stream_kernel<1, 8, 2, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a); break;
+            case 2: i8_stream_kernel<2, 8, 2, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a); break;
+            case 3: i8_stream_kernel<3, 8, 1, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a); break;
+            default: i8_stream_kernel<4, 8, 1, F16, SW, GROUPED><<<grid, 512, 0, st>>>(a);
         }
         return hipGetLastError();
     }
@@ -624,10 +616,13 @@ size_t i8_workspace(I8Args &a, void *ws) {
         return a.grouped ? group_parts(rows, size) : std::ceil(rows / size);
     };
     // Few rows: a workgroup takes about 0.10, 0.13, 0.16 or 0.18 us for a step and 16,
-    // 32, 48 or 64 rows; with start and end 3.3.  Measured (us, by rows of a pass):
-    // K = 4096, N = 2048, 16 / 64 / 256 rows 6.2, 6.5, 7.2, 7.5 / 9.4, 7.4, 8.0, 9.8 /
-    // 29, 20, 19, 16; K = 1024, N = 8192, 64 rows 10.3, 8.9, 9.4, 6.9.
-    static const double few[4] = {0.10, 0.13, 0.16, 0.18};
+    // 32, 48 or 64 rows; start and end take 3.3, and over a plan each workgroup 0.8 to
+    // 2.4 more (it reads which expert and rows are its own before it begins).
+    // Measured (us, by rows of a pass): K = 4096, N = 2048, 16 / 64 / 256 rows 6.2, 6.5,
+    // 7.2, 7.5 / 9.4, 7.4, 8.0, 9.8 / 29, 20, 19, 16; K = 1024, N = 8192, 64 rows 10.3,
+    // 8.9, 9.4, 6.9; E = 14, K = 832, N = 392, 364 rows an expert 53, 42, 37, 35.
+    static const double few[4] = {0.10, 0.13, 0.16, 0.18}, begin[4] = {0.8, 1.4, 2.0, 2.4};
+    auto whole = [](double rounds) { return rounds < 4 ? std::ceil(rounds) : rounds; };
     double best = 1e300;
     a.stream_nq = 0;
     const int64_t blocks = a.grouped ? a.g.sorted_cap / a.g.block_m : 0;
@@ -635,7 +630,8 @@ size_t i8_workspace(I8Args &a, void *ws) {
         if (a.grouped ? blocks > 65535 : a.M > 1024) break;
         const double wgs = hit * parts(a.grouped ? std::min(a.g.block_m, 16 * nq) : 16 * nq) *
                            ((a.n_out + (sw ? 7 : 15)) / (sw ? 8 : 16));
-        const double t = 3.3 + std::max(std::max(wgs / 256, 1.0) * steps * few[nq - 1], wbytes / 4.3e6);
+        const double each = steps * few[nq - 1] + (a.grouped ? begin[nq - 1] : 0);
+        const double t = 3.3 + std::max(whole(wgs / 256) * each, wbytes / 4.3e6);
         if (t < best) {
             best = t;
             a.stream_nq = nq;

@@ -257,6 +257,7 @@ def test_i8_workspace():
         assert _grp(**a, sc=sc, ldo=2048, wsp=None) == "MOE_ERR_NULL"
         assert _grp(**a, sc=sc, ldo=2048, wsb=n - 1) == "MOE_ERR_CAPACITY"
         assert _grp(**a, sc=sc, ldo=2048, wsp=OFF8) == "MOE_ERR_ALIGN"
+    assert seen
     assert moe.moe_i8_linear_workspace_size(4, 32, 72) == 0
     assert moe.moe_i8_group_mm_workspace_size(8, 64, 32, 2000, 2, 16, 128) == 0
 
