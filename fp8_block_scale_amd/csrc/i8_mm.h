@@ -25,6 +25,7 @@ struct I8Args {
     // the schedule (i8_workspace)
     int stream_nq;           // few rows: tiles of 16 rows per pass (0: the tile kernel)
     int tile_rows;           // rows of a tile
+    int tile_cols;           // its weight rows
 };
 
 // Chooses the schedule, lays the workspace out at ws (NULL: sizes only) and

@@ -398,7 +398,7 @@ i8_tile_kernel(I8Args a) {
     // every store before it.  The code is unrolled (registers have no index) and
     // kept small: beyond the instruction cache it costs its misses on every tile
     // (with both output types and ragged ends 80 KB, 17 us a tile of 256 x 256).
-    constexpr int NT = NP / (SW ? 4 : 2), NB = NQ < 4 || NT > 2 ? 2 : 4;     // column groups of 32; rows of a batch
+    constexpr int NT = NP / (SW ? 4 : 2), NB = NQ == 1 ? 1 : NQ < 4 || NT > 2 ? 2 : 4;     // column groups of 32; rows of a batch
     auto epilogue = [&](const Item &it) __attribute__((always_inline)) {
         const float *ws = a.ws + (int64_t)it.e * a.N, *bias = a.bias ? a.bias + (int64_t)it.e * a.N : nullptr;
         const int c0 = it.c0 + wp * (TC / WP) + 8 * grp;      // the lane's columns: c0 + 32 t + [0, 8)
@@ -587,12 +587,11 @@ hipError_t launch(const I8Args &a, hipStream_t st) {
         hipError_t e = launch_group_prep(a.g, st);
         if (e != hipSuccess) return e;
     }
-    switch (a.tile_rows) {
-        case 256: return launch_tile<256, 256, 2, 2, 3, 2, F16, SW, GROUPED>(a, st);
-        case 128: return launch_tile<256, 128, 2, 2, 3, 3, F16, SW, GROUPED>(a, st);
-        case 64: return launch_tile<256, 64, 4, 1, 4, 4, F16, SW, GROUPED>(a, st);
-        default: return launch_tile<256, 32, 4, 1, 4, 4, F16, SW, GROUPED>(a, st);
-    }
+    if (a.tile_rows == 256) return launch_tile<256, 256, 2, 2, 3, 2, F16, SW, GROUPED>(a, st);
+    if (a.tile_cols == 256) return launch_tile<256, 128, 2, 2, 3, 3, F16, SW, GROUPED>(a, st);
+    if (a.tile_rows == 128) return launch_tile<128, 128, 2, 2, 3, 2, F16, SW, GROUPED>(a, st);
+    if (a.tile_cols == 128) return launch_tile<128, 64, 2, 2, 3, 3, F16, SW, GROUPED>(a, st);
+    return launch_tile<64, 64, 1, 4, 5, 5, F16, SW, GROUPED>(a, st);
 }
 
 template <bool F16>
@@ -616,12 +615,15 @@ size_t i8_workspace(I8Args &a, void *ws) {
         return a.grouped ? group_parts(rows, size) : std::ceil(rows / size);
     };
     // Few rows: a workgroup takes about 0.10, 0.13, 0.16 or 0.18 us for a step and 16,
-    // 32, 48 or 64 rows; start and end take 3.3, and over a plan each workgroup 0.8 to
-    // 2.4 more (it reads which expert and rows are its own before it begins).
+    // 32, 48 or 64 rows, 0.7 to 2.0 at least (a wave's loads, the sum over waves) and
+    // over a plan 0.4 to 1.6 more (it reads which expert and rows are its own before
+    // it begins); start and end of the launch take 3.3.
     // Measured (us, by rows of a pass): K = 4096, N = 2048, 16 / 64 / 256 rows 6.2, 6.5,
     // 7.2, 7.5 / 9.4, 7.4, 8.0, 9.8 / 29, 20, 19, 16; K = 1024, N = 8192, 64 rows 10.3,
-    // 8.9, 9.4, 6.9; E = 14, K = 832, N = 392, 364 rows an expert 53, 42, 37, 35.
-    static const double few[4] = {0.10, 0.13, 0.16, 0.18}, begin[4] = {0.8, 1.4, 2.0, 2.4};
+    // 8.9, 9.4, 6.9; K = 352, N = 5830, 173 rows 14.7, 14.7, 11.5, 13.3; E = 14, K = 832,
+    // N = 392, 364 rows an expert 53, 42, 37, 35.
+    static const double few[4] = {0.10, 0.13, 0.16, 0.18}, least[4] = {0.7, 1.2, 1.5, 2.0},
+                        begin[4] = {0.4, 0.8, 1.2, 1.6};
     auto whole = [](double rounds) { return rounds < 4 ? std::ceil(rounds) : rounds; };
     double best = 1e300;
     a.stream_nq = 0;
@@ -630,37 +632,52 @@ size_t i8_workspace(I8Args &a, void *ws) {
         if (a.grouped ? blocks > 65535 : a.M > 1024) break;
         const double wgs = hit * parts(a.grouped ? std::min(a.g.block_m, 16 * nq) : 16 * nq) *
                            ((a.n_out + (sw ? 7 : 15)) / (sw ? 8 : 16));
-        const double each = steps * few[nq - 1] + (a.grouped ? begin[nq - 1] : 0);
+        const double each = std::max(steps * few[nq - 1], least[nq - 1]) + (a.grouped ? begin[nq - 1] : 0);
         const double t = 3.3 + std::max(whole(wgs / 256) * each, wbytes / 4.3e6);
         if (t < best) {
             best = t;
             a.stream_nq = nq;
         }
     }
-    // Tiles of 256 weight rows: a step of 128 of K takes `idle` us alone and `busy`
-    // with every CU at work, a tile's first copies and its epilogue `ends`; every
-    // row tile reads its weights, 5.4 TB/s of them.  Grouped, the set-up launch
-    // before takes 5.  Measured (us, 32 / 64 / 128 / 256 rows): K = 2048, N = 1000, 1000
-    // rows 11.4, 13.9, 18.1, 27.1; K = 7168, N = 4096, 512 and 2048 rows 39, 44, 52, 83
-    // and 147, 87, 59, 91; E = 288, K = 4096, N = 2048 with 14, 57, 114, 228 rows an
-    // expert 435, 426, 441, 583; 744, 510, 474, 608; 1193, 645, 528, 628; 1928, 1003,
-    // 773, 711.
+    // Tiles: launch and first copies take about 3.5 us, over a plan the set-up launch
+    // before 5; a step of 128 of K `idle` alone and `busy` with a tile on every CU, a
+    // tile's end `ends`.  HBM gives 5.4 TB/s of the weights, which a row tile finds in
+    // the caches in part where another one has read them; `mix` of the shorter of both
+    // times adds to the longer.
+    // Measured (us; rows x columns 64 x 64 / 64 x 128 / 128 x 128 / 128 x 256 / 256 x 256):
+    //   K = 2048, N = 1000, 1000 rows    8.6,  9.8, 13.2, 18.3, 27.9
+    //   K = 4096, N = 2048, 1000 rows   19.1, 15.0, 20.2, 27.4, 44.8
+    //                       4096 rows   64.3, 52.3, 41.0, 37.7, 54.0
+    //   K = 7168, N = 4096, 512 rows    33.4, 29.4, 36.4, 51.7, 71.7
+    //                       2048 rows    107, 87.6, 61.2, 57.8, 85.0
+    //                       4096 rows    204,  170,  119,  111, 95.3
+    //   E = 288, K = 4096, N = 2048, SwiGLU, by rows an expert
+    //                       14           457,  434,  448,  438,  564
+    //                       57           596,  515,  480,  467,  574
+    //                       114          887,  692,  585,  539,  592
+    //                       228         1450, 1095,  848,  766,  668
+    // (32 and 64 rows x 256 columns measured no faster anywhere.)
     struct Form {
-        int rows;
-        double idle, busy, ends;
+        int rows, cols;
+        double idle, busy, ends, mix;
     };
-    static const Form forms[4] = {{32, 0.38, 0.60, 4}, {64, 0.39, 0.70, 5.5}, {128, 0.62, 0.98, 6}, {256, 1.04, 1.36, 9}};
+    static const Form forms[5] = {{64, 64, 0.21, 0.22, 0.9, 0.3},
+                                  {64, 128, 0.28, 0.35, 1.4, 0.15},
+                                  {128, 128, 0.42, 0.48, 2.2, 0.17},
+                                  {128, 256, 0.60, 0.84, 6.3, 0.1},
+                                  {256, 256, 1.04, 1.36, 9.5, 0.1}};
     a.tile_rows = 0;
     for (const Form &f : forms) {
         if (f.rows == 256 && a.n_out % 8 != 0) continue;      // (no code for ragged ends)
-        const double per = parts(f.rows), items = hit * per * ((a.N + 255) / 256);
+        const double per = parts(f.rows), items = hit * per * ((a.N + f.cols - 1) / f.cols);
         const double step = f.idle + (f.busy - f.idle) * std::min(items / 256, 1.0), rounds = items / 256;
         const double busy = (rounds < 4 ? std::ceil(rounds) : rounds + 0.5) * (steps * step + f.ends);
-        const double mem = per * wbytes / 5.4e6;
-        const double t = std::max(busy, mem) + 0.1 * std::min(busy, mem) + (a.grouped ? 5 : 0);
+        const double mem = (1 + (per - 1) * (a.grouped ? 0.35 : 0.1)) * wbytes / 5.4e6;
+        const double t = 3.5 + std::max(busy, mem) + f.mix * std::min(busy, mem) + (a.grouped ? 5 : 0);
         if (t < best) {
             best = t;
             a.tile_rows = f.rows;
+            a.tile_cols = f.cols;
         }
     }
     if (a.tile_rows) a.stream_nq = 0;
