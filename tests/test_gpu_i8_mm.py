@@ -319,6 +319,27 @@ def test_group(M, E, N, K, k, bm, act, per_route, routing, dtype):
     p.check(p())
 
 
+@pytest.mark.parametrize("M,N,K,act", [(142, 1920, 1536, "none"), (229, 704, 720, "swiglu"), (213, 920, 1280, "silu"),
+                                       (232, 1000, 1232, "swiglu"), (142, 1914, 1552, "gelu"), (231, 1002, 1232, "swiglu")])
+def test_linear_between(M, N, K, act):
+    """Between few rows and many: passes of 48 and 64 rows."""
+    p = Linear(M, N, K, act, dtype="f16" if M % 2 else "bf16")
+    p.check(p())
+
+
+@pytest.mark.parametrize("per_route", [False, True])
+@pytest.mark.parametrize("M,E,N,K,k,bm,act", [
+    (63, 9, 464, 1472, 4, 64, "none"), (270, 5, 128, 256, 2, 128, "swiglu"), (329, 6, 336, 2736, 3, 128, "gelu"),
+    (131, 8, 1392, 960, 2, 64, "swiglu"), (308, 1, 1264, 2640, 1, 128, "silu"), (461, 9, 880, 384, 1, 128, "swiglu"),
+    (844, 6, 3104, 1968, 2, 128, "swiglu"), (1163, 3, 3680, 816, 3, 16, "silu"), (1278, 3, 2720, 2944, 3, 64, "swiglu"),
+    (461, 9, 890, 384, 1, 128, "swiglu"), (844, 6, 3106, 1968, 2, 128, "swiglu")])
+def test_group_between(M, E, N, K, k, bm, act, per_route):
+    """Few-rows passes of 32 to 64 rows over plan blocks, and the tiles' sizes with
+    either kind of activation."""
+    p = Group(M, E, N, K, k, bm, act, bias=M % 2 == 0, dtype="f16" if K % 32 else "bf16", per_route=per_route, pad=2)
+    p.check(p())
+
+
 def test_group_of_one_is_the_dense_product():
     p = Group(700, 1, 320, 512, 1, 64, "swiglu")
     d = Linear(700, 320, 512, "swiglu", residual=False)
