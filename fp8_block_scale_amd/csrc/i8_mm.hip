@@ -35,6 +35,9 @@ __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0u, 0u, 0u, 
 // copy: register loads touch 16 rows, 64 bytes of each.
 // Rows past the end read another row: their results are not stored.  Values past
 // the end of K are zeros on one side at least.
+// Bound by the weights from HBM where they are many (4 tokens of 9 routes, 257
+// experts, K = 7168, N = 512: 125 MB in 29 us, 4.3 TB/s), by its latency else (48
+// rows, K = 4096, N = 2048, SwiGLU: 5.5 us, 8.4 MB).
 template <int NQ, int NW, int U, bool F16, bool SW, bool GROUPED>
 __global__ void __launch_bounds__(64 * NW)
 i8_stream_kernel(I8Args a) {
@@ -172,6 +175,17 @@ i8_stream_kernel(I8Args a) {
 // own stage: the copies of the stages SQ and SP further on go out then, beside the
 // second half's MFMAs.  Weights, which come from HBM, are given the more time
 // where the LDS does not hold another slot of both.
+//
+// Four waves of 128 x 128 sums each (256 x 256): a stage's LDS reads take half the
+// time of its MFMAs, with eight waves of 64 x 128 three quarters.  A stage takes
+// 1.02 us on zeros and 1.36 on random values, where the card's power limits the
+// matrix cores (56% busy at 2.03 GHz, 8192 x 4096 x 7168 in 200 us: 2.4 PFLOP/s; a
+// library's 8-bit product reaches 2.1), the epilogue 9.5: some twenty vector
+// instructions for each of 256 results a lane, and no other wave's MFMAs beside
+// them.  Over a plan with few rows an expert weights from HBM are the bound (8192
+// tokens of 8 routes, 288 experts, K = 4096, N = 2048: 640 us, 3.3 GB, 5.1 TB/s).
+// Smaller tiles, down to 64 x 64, two workgroups to a CU, are for what gives the
+// CUs too few large ones.
 template <int TP, int TQ, int WP, int WQ, int SP, int SQ>
 struct I8Tile {
     static constexpr int NW = WP * WQ;

@@ -5,7 +5,14 @@
 //   (1 or 2) largest c; only the topk_group best groups are kept
 //   chosen: the top_k largest c; w_j = scale s_j, or scale s_j / sum of the chosen s
 //
-// One wave routes one token.
+// One wave routes one token: the choice is top_k + 1 dependent reductions, and a
+// reduction over 64 lanes by DPP and scalar registers costs what one over 16 does.
+// What bounds it: instructions (about 900 a wave), at few tokens their latency.
+// Measured: 16 tokens of 256 experts in 8 groups 7.4 us (decided in 64 bits
+// throughout 13.9), 8192 tokens of 288 experts, softmax with a bias, 18.4 (25.5):
+// 13.4 and the about 20 tokens that FP32 does not decide, whose waves end last; of
+// the 13.4 the rounds take 4 and the weights in 64 bits 1.6.  Reading the logits
+// (4.7 MB) takes 1.
 #include <algorithm>
 
 #include "common.h"
@@ -368,6 +375,8 @@ route_scored_kernel(ScoreArgs a, int sh) {
 //   sigmoid                dl_e = sum_{j: e_j = e} s_j (1 - s_j) a_j
 //   sigmoid, renormalised  ... with (a_j - sum a s / S) / S in the place of a_j, S = sum s
 // (1 - s is the sigmoid of -l: no cancellation where s is near 1.)
+// One wave a token, for gradients that every logit has (2048 tokens of 512
+// experts, BF16: 6.1 us, 4.2 MB, bound by its latency) and for more than 16 slots.
 template <int DT, int NPL>
 __global__ void __launch_bounds__(256)
 route_scored_bwd_kernel(ScoreArgs a) {
@@ -445,7 +454,8 @@ route_scored_bwd_kernel(ScoreArgs a) {
 // The same for weights whose gradient is 0 outside the slots, up to 16 of them: a
 // row of 16 lanes takes a token (its sums are DPP steps), a wave four.  The rows
 // of d_logits are put together in LDS and stored 16 bytes a lane: it is their
-// writing that bounds the kernel (16384 tokens of 256 experts, FP32: 16.8 MB).
+// writing that bounds the kernel (16384 tokens of 256 experts, FP32, 16.8 MB: 6.3 us;
+// one wave a token took 12.9).
 constexpr int kRowWaves = 2;
 
 // The sum over the lane's row of 16.
