@@ -1486,15 +1486,20 @@ moe_status check_i8_n(int64_t N, int32_t act) {
     return MOE_OK;
 }
 
+// Output tiles are of at least 64 rows x 64 columns (of w) and numbered in int32;
+// the walk over them may step past the last by the grid.
+moe_status check_i8_tiles(int64_t row_tiles, int64_t N) {
+    if (row_tiles * ((N + 63) / 64) >= ((int64_t)1 << 31) - ((int64_t)1 << 21))
+        return fail(MOE_ERR_UNSUPPORTED, "more output tiles than int32 counts");
+    return MOE_OK;
+}
+
 moe_status check_i8_linear(int64_t M, int64_t N, int64_t K, int32_t act) {
     moe_status st = check_i8_k(M, K);
     if (st == MOE_OK) st = check_i8_n(N, act);
     if (st != MOE_OK) return st;
     if (M > ((int64_t)1 << 31) - 1024) return fail(MOE_ERR_SHAPE, "M must not exceed 2^31 - 1024");
-    // output tiles of at least 32 rows x 64 columns, numbered in int32
-    if (((M + 31) / 32) * ((N + 63) / 64) >= ((int64_t)1 << 31) - ((int64_t)1 << 21))
-        return fail(MOE_ERR_UNSUPPORTED, "more output tiles than int32 counts");
-    return MOE_OK;
+    return check_i8_tiles((M + 63) / 64, N);
 }
 
 moe::I8Args i8_args(int64_t M, int64_t N, int64_t K, int32_t act) {
@@ -1513,6 +1518,7 @@ moe_status check_i8_group(int64_t M, int64_t K, int64_t N, int32_t E, int32_t to
     if (st == MOE_OK) st = check_i8_n(N, act);
     // (multiples of 8, with the same number of tiles)
     if (st == MOE_OK) st = check_group_shape(M, K, (N + 7) / 8 * 8, E, top_k, block_m, sorted_cap);
+    if (st == MOE_OK) st = check_i8_tiles(M * top_k / 64 + E, N);
     return st;
 }
 

@@ -217,6 +217,12 @@ def test_i8_refusals(f):
     assert f(M=1 << 30, k=1, N=1 << 20, ldo=1 << 20, ldr=1 << 20) == "MOE_ERR_UNSUPPORTED"
 
 
+@pytest.mark.parametrize("f", [_lin, _grp])
+def test_i8_tiles_of_64_by_64_are_counted(f):
+    """2^43 outputs in tiles of 64 x 64 are 2^31."""
+    assert f(M=1 << 24, k=1, N=1 << 19, ldo=1 << 20, ldr=1 << 20) == "MOE_ERR_UNSUPPORTED"
+
+
 def test_i8_residual():
     assert _lin(res=I8["out"], ldr=40) == "MOE_ERR_SHAPE"
     assert _lin(ldr=31) == "MOE_ERR_SHAPE"
