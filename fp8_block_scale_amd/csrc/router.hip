@@ -7,12 +7,11 @@
 //
 // One wave routes one token: the choice is top_k + 1 dependent reductions, and a
 // reduction over 64 lanes by DPP and scalar registers costs what one over 16 does.
-// What bounds it: instructions (about 900 a wave), at few tokens their latency.
-// Measured: 16 tokens of 256 experts in 8 groups 7.4 us (decided in 64 bits
-// throughout 13.9), 8192 tokens of 288 experts, softmax with a bias, 18.4 (25.5):
-// 13.4 and the about 20 tokens that FP32 does not decide, whose waves end last; of
-// the 13.4 the rounds take 4 and the weights in 64 bits 1.6.  Reading the logits
-// (4.7 MB) takes 1.
+// What bounds it: instructions, at few tokens their latency.  Measured: 16 tokens
+// of 256 experts in 8 groups 6.9 us (decided in 64 bits throughout 13.9), 8192
+// tokens of 288 experts, softmax with a bias, 17.4 (25.5): 13.2 and the about 20
+// tokens that FP32 does not decide, whose waves end last; the weights in 64 bits
+// take 1.4 of it.  Reading the logits (4.7 MB) takes 1.
 #include <algorithm>
 
 #include "common.h"
@@ -88,7 +87,8 @@ __device__ __forceinline__ int pick(uint64_t who, int e) {
 // Chooses in 64 bits: lane r < top_k gets the expert of rank r (-1: none is
 // left).  mx: the largest logit.
 template <int NPL>
-__device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, const float (&l)[NPL], float mx) {
+__device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, const float (&l)[NPL],
+                                        const float (&bias)[NPL], float mx) {
     const int lane = threadIdx.x & 63;
     const bool soft = a.score == kScoreSoftmax;
     double s[NPL], total = 0.0;
@@ -104,7 +104,7 @@ __device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, con
         key[i] = 0;
         if (!usable(l[i])) continue;
         double c = (soft ? s[i] : 1.0) / (soft ? total : 1.0 + s[i]);
-        if (a.bias) c += (double)a.bias[ln.expert(i)];
+        c += (double)bias[i];
         if (c > -INFINITY) key[i] = ordered64(c);
     }
     auto value = [](uint64_t k) {
@@ -209,8 +209,8 @@ __device__ __forceinline__ void group_top2(float &v1, float &v2, int sh) {
 // Compared are neighbours in the ranking, the last one chosen and the best one
 // not chosen, and the worst group kept and the best one not kept.
 template <int NPL>
-__device__ __forceinline__ int choose32(const ScoreArgs &a, const Lanes &ln, const float (&l)[NPL], float mx,
-                                        bool &sure) {
+__device__ __forceinline__ int choose32(const ScoreArgs &a, const Lanes &ln, const float (&l)[NPL],
+                                        const float (&bias)[NPL], float mx, bool &sure) {
     const int lane = threadIdx.x & 63;
     const bool grouped = a.topk_group < a.n_group;
     const bool plain = !a.bias && !(grouped && a.group_top == 2);
@@ -247,10 +247,9 @@ __device__ __forceinline__ int choose32(const ScoreArgs &a, const Lanes &ln, con
         for (int i = 0; i < NPL; ++i) {
             c[i] = -INFINITY;
             if (!usable(l[i])) continue;
-            const float b = a.bias ? a.bias[ln.expert(i)] : 0.f;
-            c[i] = (soft ? e[i] * inv : e[i]) + b;
+            c[i] = (soft ? e[i] * inv : e[i]) + bias[i];
             if (!(c[i] > -INFINITY)) c[i] = -INFINITY;
-            else bmax = fmaxf(bmax, fabsf(b));
+            else bmax = fmaxf(bmax, fabsf(bias[i]));
         }
         bmax = unordered(wave_max_u32(ordered_bits(bmax)));
         // (an infinite bias: bmax = inf, nothing is sure)
@@ -286,29 +285,39 @@ __device__ __forceinline__ int choose32(const ScoreArgs &a, const Lanes &ln, con
     uint32_t key[NPL];                           // 0: not to be chosen
 #pragma unroll
     for (int i = 0; i < NPL; ++i) key[i] = c[i] > -INFINITY ? ordered_bits(c[i] + 0.0f) : 0u;
-    int sel = -1;
-    float above = 0.f;
-    for (int r = 0; r <= a.top_k; ++r) {         // (one past the last, to compare)
-        uint32_t bk = 0;
-        int be = 0;
+    int sel = -1, n = 0;                         // ranks with an expert, one past the last chosen among them
+    float v = 0.f;                               // the value of the lane's rank
+    for (int r = 0; r <= a.top_k; ++r) {
+        uint32_t bk = key[0];
+        int bi = 0;                              // of equals the first
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (key[i] > bk) {
-                bk = key[i];
-                be = ln.expert(i);
-            }
+        for (int i = 1; i < NPL; ++i) {
+            bi = key[i] > bk ? i : bi;
+            bk = max(bk, key[i]);
+        }
         const uint32_t top = wave_max_u32(bk);
         if (top == 0) break;
-        const float v = unordered(top);
-        if (r > 0) sure = sure && apart(above, v, 2.f);
-        above = v;
+        n = r + 1;
+        if (lane == r) v = unordered(top);
         if (r == a.top_k) break;
-        const int e = pick(__ballot(bk == top), be);
+        const int be = ln.expert(bi);
+        uint64_t who = __ballot(bk == top);
+        if (who & (who - 1)) {
+            if (!plain) sure = false;            // equal scores
+            if (!sure) break;
+            const uint32_t first = wave_min_u32(bk == top ? (uint32_t)be : 0xFFFFFFFFu);
+            who = __ballot(bk == top && (uint32_t)be == first);
+        }
+        const int w = __builtin_ctzll(who);
+        const int e = __builtin_amdgcn_readlane(be, w);
         if (lane == r) sel = e;
+        const int out = lane == w ? bi : -1;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (ln.expert(i) == e && ln.holds(i)) key[i] = 0;
+        for (int i = 0; i < NPL; ++i) key[i] = i == out ? 0u : key[i];
     }
+    // all neighbours at once
+    const float below = __shfl_down(v, 1, 64);
+    if (__ballot(lane + 1 < n && !apart(v, below, 2.f))) sure = false;
     return sel;
 }
 
@@ -320,11 +329,14 @@ route_scored_kernel(ScoreArgs a, int sh) {
     if (t >= a.M) return;
     const Lanes ln = {a.E / a.n_group, lane >> sh, lane & ((1 << sh) - 1), sh};
     const int64_t row = t * a.ld;
-    float l[NPL];
+    float l[NPL], bias[NPL];
     float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i)
-        l[i] = ln.g < a.n_group && ln.holds(i) ? load_logit<DT>(a.logits, row + ln.expert(i)) : -INFINITY;
+    for (int i = 0; i < NPL; ++i) {
+        const bool there = ln.g < a.n_group && ln.holds(i);
+        l[i] = there ? load_logit<DT>(a.logits, row + ln.expert(i)) : -INFINITY;
+        bias[i] = there && a.bias ? a.bias[ln.expert(i)] : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         l[i] = usable(l[i]) ? finite(l[i]) : -INFINITY;
@@ -339,8 +351,8 @@ route_scored_kernel(ScoreArgs a, int sh) {
         total = wave_sum(total);
     }
     bool sure;
-    int sel = choose32(a, ln, l, mx, sure);
-    if (!sure) sel = choose64(a, ln, l, mx);
+    int sel = choose32(a, ln, l, bias, mx, sure);
+    if (!sure) sel = choose64(a, ln, l, bias, mx);
     // weights: lane j holds slot j
     double s = 0.0;
     const float ls = sel >= 0 ? finite(load_logit<DT>(a.logits, row + sel)) : -INFINITY;
