@@ -324,41 +324,62 @@ __device__ __forceinline__ int choose32(const ScoreArgs &a, const Lanes &ln, con
 template <int DT, int NPL>
 __global__ void __launch_bounds__(256)
 route_scored_kernel(ScoreArgs a, int sh) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= a.M) return;
-    const Lanes ln = {a.E / a.n_group, lane >> sh, lane & ((1 << sh) - 1), sh};
-    const int64_t row = t * a.ld;
-    float l[NPL], bias[NPL];
-    float mx = -INFINITY;
+    __shared__ int chosen[4][32];
+    __shared__ float most[4];
+    __shared__ double totals[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kk = a.top_k + a.n_shared;
+    {
+        const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+        const Lanes ln = {a.E / a.n_group, lane >> sh, lane & ((1 << sh) - 1), sh};
+        float l[NPL], bias[NPL];
+        float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const bool there = ln.g < a.n_group && ln.holds(i);
-        l[i] = there ? load_logit<DT>(a.logits, row + ln.expert(i)) : -INFINITY;
-        bias[i] = there && a.bias ? a.bias[ln.expert(i)] : 0.f;
-    }
+        for (int i = 0; i < NPL; ++i) {
+            const bool there = ln.g < a.n_group && ln.holds(i);
+            l[i] = there && t < a.M ? load_logit<DT>(a.logits, t * a.ld + ln.expert(i)) : -INFINITY;
+            bias[i] = there && a.bias ? a.bias[ln.expert(i)] : 0.f;
+        }
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        l[i] = usable(l[i]) ? finite(l[i]) : -INFINITY;
-        mx = fmaxf(mx, l[i]);
-    }
-    mx = unordered(wave_max_u32(ordered_bits(mx)));
-    double total = 0.0;
-    if (a.score == kScoreSoftmax && !a.renorm) {             // (renormalised weights need no denominator)
+        for (int i = 0; i < NPL; ++i) {
+            l[i] = usable(l[i]) ? finite(l[i]) : -INFINITY;
+            mx = fmaxf(mx, l[i]);
+        }
+        mx = unordered(wave_max_u32(ordered_bits(mx)));
+        double total = 0.0;
+        if (a.score == kScoreSoftmax && !a.renorm) {         // (renormalised weights need no denominator)
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (usable(l[i])) total += exp((double)l[i] - (double)mx);
-        total = wave_sum(total);
+            for (int i = 0; i < NPL; ++i)
+                if (usable(l[i])) total += exp((double)l[i] - (double)mx);
+            total = wave_sum(total);
+        }
+        bool sure;
+        int sel = choose32(a, ln, l, bias, mx, sure);
+        if (!sure) sel = choose64(a, ln, l, bias, mx);
+        if (lane < 32) chosen[wave][lane] = lane < a.top_k ? sel : -1;
+        if (lane == 0) {
+            most[wave] = mx;
+            totals[wave] = total;
+        }
+        if (t < a.M && lane < a.top_k) a.ids[t * kk + lane] = sel;
+        else if (t < a.M && lane < kk) {         // the shared expert
+            a.ids[t * kk + lane] = a.E;
+            a.w[t * kk + lane] = 1.0f;
+        }
     }
-    bool sure;
-    int sel = choose32(a, ln, l, bias, mx, sure);
-    if (!sure) sel = choose64(a, ln, l, bias, mx);
-    // weights: lane j holds slot j
+    // The weights of all four tokens at once, 16 or 32 lanes a token: lane j of
+    // them holds slot j.  (In every wave for its own token they took 1.4 us of 17.4.)
+    __syncthreads();
+    const int width = a.top_k <= 16 ? 16 : 32, q = (int)threadIdx.x / width, j = lane & (width - 1);
+    if (wave * 64 >= 4 * width) return;
+    const int64_t t = (int64_t)blockIdx.x * 4 + q;
+    const int sel = chosen[q][j];
     double s = 0.0;
-    const float ls = sel >= 0 ? finite(load_logit<DT>(a.logits, row + sel)) : -INFINITY;
+    const float ls = sel >= 0 ? finite(load_logit<DT>(a.logits, t * a.ld + sel)) : -INFINITY;
     if (a.renorm) {
         // up to a factor that renormalising takes out, so that not all underflow
-        const float top = unordered(wave_max_u32(ordered_bits(ls)));
+        uint32_t bits = row_max_u32(ordered_bits(ls));
+        if (width == 32) bits = max(bits, (uint32_t)__shfl_xor((int)bits, 16, 64));
+        const float top = unordered(bits);
         const float m = a.score == kScoreSoftmax ? top : fminf(top, 0.f);
         if (sel >= 0)
             s = a.score == kScoreSoftmax ? exp((double)ls - (double)m)
@@ -367,16 +388,9 @@ route_scored_kernel(ScoreArgs a, int sh) {
         for (int d = 1; d < a.top_k; d <<= 1) sum += __shfl_xor(sum, d, 64);
         s = sum > 0.0 ? s / sum : 0.0;
     } else if (sel >= 0) {
-        s = a.score == kScoreSoftmax ? exp((double)ls - (double)mx) / total : sigmoid64(ls);
+        s = a.score == kScoreSoftmax ? exp((double)ls - (double)most[q]) / totals[q] : sigmoid64(ls);
     }
-    const int kk = a.top_k + a.n_shared;
-    if (lane < a.top_k) {
-        a.ids[t * kk + lane] = sel;
-        a.w[t * kk + lane] = (float)(s * (double)a.scale);
-    } else if (lane < kk) {                      // the shared expert
-        a.ids[t * kk + lane] = a.E;
-        a.w[t * kk + lane] = 1.0f;
-    }
+    if (t < a.M && j < a.top_k) a.w[t * kk + j] = (float)(s * (double)a.scale);
 }
 
 // ----------------------------------------------------------------- backward
