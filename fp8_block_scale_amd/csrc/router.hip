@@ -8,10 +8,10 @@
 // One wave routes one token: the choice is top_k + 1 dependent reductions, and a
 // reduction over 64 lanes by DPP and scalar registers costs what one over 16 does.
 // What bounds it: instructions, at few tokens their latency.  Measured: 16 tokens
-// of 256 experts in 8 groups 6.9 us (decided in 64 bits throughout 13.9), 8192
-// tokens of 288 experts, softmax with a bias, 17.4 (25.5): 13.2 and the about 20
-// tokens that FP32 does not decide, whose waves end last; the weights in 64 bits
-// take 1.4 of it.  Reading the logits (4.7 MB) takes 1.
+// of 256 experts in 8 groups 6.6 us (decided in 64 bits throughout 13.9), 8192
+// tokens of 288 experts, softmax with a bias, 16.3 (25.5): 13 and the about 20
+// tokens that FP32 does not decide, whose waves end last.  Reading the logits
+// (4.7 MB) takes 1.
 #include <algorithm>
 
 #include "common.h"
@@ -78,12 +78,6 @@ __device__ __forceinline__ uint64_t dpp64(uint64_t v) {
     return (uint64_t)hi << 32 | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
 
-// The lowest expert e that the lanes `who` (one at least) hold.
-__device__ __forceinline__ int pick(uint64_t who, int e) {
-    if ((who & (who - 1)) == 0) return __builtin_amdgcn_readlane(e, __builtin_ctzll(who));
-    return (int)wave_min_u32((who >> (threadIdx.x & 63)) & 1 ? (uint32_t)e : 0xFFFFFFFFu);
-}
-
 // Chooses in 64 bits: lane r < top_k gets the expert of rank r (-1: none is
 // left).  mx: the largest logit.
 template <int NPL>
@@ -94,18 +88,15 @@ __device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, con
     double s[NPL], total = 0.0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        s[i] = usable(l[i]) ? exp(soft ? (double)l[i] - (double)mx : -(double)l[i]) : 0.0;
+        s[i] = exp(soft ? (double)l[i] - (double)mx : -(double)l[i]);      // (no branches: one chain beside the other)
         total += s[i];
     }
     if (soft) total = wave_sum(total);
     uint64_t key[NPL];                           // 0: not to be chosen
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-        key[i] = 0;
-        if (!usable(l[i])) continue;
-        double c = (soft ? s[i] : 1.0) / (soft ? total : 1.0 + s[i]);
-        c += (double)bias[i];
-        if (c > -INFINITY) key[i] = ordered64(c);
+        const double c = (soft ? s[i] : 1.0) / (soft ? total : 1.0 + s[i]) + (double)bias[i];
+        key[i] = usable(l[i]) && c > -INFINITY ? ordered64(c) : 0;
     }
     auto value = [](uint64_t k) {
         return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
@@ -142,14 +133,13 @@ __device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, con
     }
     int sel = -1;
     for (int r = 0; r < a.top_k; ++r) {
-        uint64_t bk = 0;
-        int be = 1 << 30;
+        uint64_t bk = key[0];
+        int bi = 0;                              // of equals the first
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (key[i] > bk) {
-                bk = key[i];
-                be = ln.expert(i);
-            }
+        for (int i = 1; i < NPL; ++i) {
+            bi = key[i] > bk ? i : bi;
+            bk = key[i] > bk ? key[i] : bk;
+        }
         // the largest high halves, of those the largest low halves, of those the
         // lowest expert
         const uint32_t hi = (uint32_t)(bk >> 32), top = wave_max_u32(hi);
@@ -159,11 +149,17 @@ __device__ __forceinline__ int choose64(const ScoreArgs &a, const Lanes &ln, con
             const uint32_t lo = hi == top ? (uint32_t)bk : 0u, low = wave_max_u32(lo);
             who = __ballot(hi == top && lo == low);
         }
-        const int e = pick(who, be);
+        const int be = ln.expert(bi);
+        if (who & (who - 1)) {
+            const uint32_t first = wave_min_u32((who >> lane) & 1 ? (uint32_t)be : 0xFFFFFFFFu);
+            who = __ballot(((who >> lane) & 1) && (uint32_t)be == first);
+        }
+        const int w = __builtin_ctzll(who);
+        const int e = __builtin_amdgcn_readlane(be, w);
         if (lane == r) sel = e;
+        const int out = lane == w ? bi : -1;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (ln.expert(i) == e && ln.holds(i)) key[i] = 0;
+        for (int i = 0; i < NPL; ++i) key[i] = i == out ? 0 : key[i];
     }
     return sel;
 }
@@ -282,6 +278,7 @@ __device__ __forceinline__ int choose32(const ScoreArgs &a, const Lanes &ln, con
             for (int i = 0; i < NPL; ++i) c[i] = -INFINITY;
         }
     }
+    if (!sure) return -1;
     uint32_t key[NPL];                           // 0: not to be chosen
 #pragma unroll
     for (int i = 0; i < NPL; ++i) key[i] = c[i] > -INFINITY ? ordered_bits(c[i] + 0.0f) : 0u;
@@ -303,8 +300,10 @@ __device__ __forceinline__ int choose32(const ScoreArgs &a, const Lanes &ln, con
         const int be = ln.expert(bi);
         uint64_t who = __ballot(bk == top);
         if (who & (who - 1)) {
-            if (!plain) sure = false;            // equal scores
-            if (!sure) break;
+            if (!plain) {                        // equal scores
+                sure = false;
+                break;
+            }
             const uint32_t first = wave_min_u32(bk == top ? (uint32_t)be : 0xFFFFFFFFu);
             who = __ballot(bk == top && (uint32_t)be == first);
         }
@@ -367,7 +366,7 @@ route_scored_kernel(ScoreArgs a, int sh) {
         }
     }
     // The weights of all four tokens at once, 16 or 32 lanes a token: lane j of
-    // them holds slot j.  (In every wave for its own token they took 1.4 us of 17.4.)
+    // them holds slot j.  (In every wave for its own token they took 1.4 us of 17.4, 8192 tokens.)
     __syncthreads();
     const int width = a.top_k <= 16 ? 16 : 32, q = (int)threadIdx.x / width, j = lane & (width - 1);
     if (wave * 64 >= 4 * width) return;
