@@ -366,7 +366,7 @@ route_scored_kernel(ScoreArgs a, int sh) {
         }
     }
     // The weights of all four tokens at once, 16 or 32 lanes a token: lane j of
-    // them holds slot j.  (In every wave for its own token they took 1.4 us of 17.4, 8192 tokens.)
+    // them holds slot j.  (In every wave for its own token they took 1.4 of 17.4 us for 8192 tokens.)
     __syncthreads();
     const int width = a.top_k <= 16 ? 16 : 32, q = (int)threadIdx.x / width, j = lane & (width - 1);
     if (wave * 64 >= 4 * width) return;
@@ -396,10 +396,12 @@ route_scored_kernel(ScoreArgs a, int sh) {
 
 // With a_j = scale dL/dw_j for the token's slots j that hold an expert:
 //   softmax                dl_e = p_e (sum_{j: e_j = e} a_j - sum_j a_j p_j)
-//   softmax, renormalised  dl_e = sum_{j: e_j = e} p_j (a_j - sum a p), p over the slots
+//   softmax, renormalised  dl_e = sum_{j: e_j = e} p_j sum_i p_i (a_j - a_i), p over the slots
 //   sigmoid                dl_e = sum_{j: e_j = e} s_j (1 - s_j) a_j
-//   sigmoid, renormalised  ... with (a_j - sum a s / S) / S in the place of a_j, S = sum s
-// (1 - s is the sigmoid of -l: no cancellation where s is near 1.)
+//   sigmoid, renormalised  ... with sum_i s_i (a_j - a_i) / S^2 in the place of a_j, S = sum s
+// (1 - s is the sigmoid of -l: no cancellation where s is near 1; the differences
+// a_j - a_i are taken first: none where one slot holds nearly the whole sum, and a
+// single slot's gradient is 0.)
 // One wave a token, for gradients that every logit has (2048 tokens of 512
 // experts, BF16: 6.1 us, 4.2 MB, bound by its latency) and for more than 16 slots.
 template <int DT, int NPL>
@@ -422,6 +424,13 @@ route_scored_bwd_kernel(ScoreArgs a) {
     if (!usable(ls)) id = -1;                    // never chosen: weight 0, whatever its logit
     ls = id >= 0 ? finite(ls) : -INFINITY;
     if (id < 0) av = 0.f;
+    auto apart = [&](float s) {                  // sum_i s_i (a_j - a_i)
+        float sum = 0.f;
+        for (int i = 0; i < a.slots; ++i)
+            sum = fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s), i)),
+                       av - __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(av), i)), sum);
+        return sum;
+    };
     float p[NPL], mx = -INFINITY, inv = 0.f, v = 0.f, dot = 0.f;
     if (dense) {
 #pragma unroll
@@ -447,15 +456,15 @@ route_scored_bwd_kernel(ScoreArgs a) {
         const float ex = id >= 0 ? expf(ls - m) : 0.f;
         const float sum = wave_sum(ex);
         const float q = sum > 0.f ? ex / sum : 0.f;
-        v = q * (av - wave_sum(av * q));
+        v = q * apart(q);
     } else {
         // renormalised: s up to a factor, which cancels, so that not all underflow
         const float m = a.renorm ? fminf(wave_max(ls), 0.f) : 0.f;
         const float s = id >= 0 ? 1.0f / (expf(m) + expf(m - ls)) : 0.f;
         const float rest = id >= 0 ? 1.0f / (1.0f + expf(ls)) : 0.f;
         if (a.renorm) {
-            const float S = wave_sum(s), as = wave_sum(av * s);
-            av = S > 0.f ? (av - as / S) / S : 0.f;
+            const float S = wave_sum(s);
+            av = S > 0.f ? apart(s) / S / S : 0.f;
         }
         v = s * rest * av;
     }
@@ -479,7 +488,7 @@ route_scored_bwd_kernel(ScoreArgs a) {
 // The same for weights whose gradient is 0 outside the slots, up to 16 of them: a
 // row of 16 lanes takes a token (its sums are DPP steps), a wave four.  The rows
 // of d_logits are put together in LDS and stored 16 bytes a lane: it is their
-// writing that bounds the kernel (16384 tokens of 256 experts, FP32, 16.8 MB: 6.3 us;
+// writing that bounds the kernel (16384 tokens of 256 experts, FP32, 16.8 MB: 6.5 us;
 // one wave a token took 12.9).
 constexpr int kRowWaves = 2;
 
@@ -490,6 +499,21 @@ __device__ __forceinline__ float row_sum(float v) {
     v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x141, 0xF, 0xF, false));
     v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x140, 0xF, 0xF, false));
     return v;
+}
+
+// sum += s_i (a - a_i) over the row's lanes i from J on, up to lane 15
+template <int J>
+__device__ __forceinline__ void add_apart(float s, float a, int slots, float &sum) {
+    if constexpr (J < 16) {
+        if (J < slots) {
+            const float sj =
+                __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(s), 0x150 + J, 0xF, 0xF, false));
+            const float aj =
+                __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(a), 0x150 + J, 0xF, 0xF, false));
+            sum = fmaf(sj, a - aj, sum);
+            add_apart<J + 1>(s, a, slots, sum);
+        }
+    }
 }
 
 // s += v of row lane J where that holds the same expert; up to lane 15
@@ -533,15 +557,19 @@ route_scored_bwd_rows_kernel(ScoreArgs a, int pitch) {
         const float ex = id >= 0 ? expf(ls - top) : 0.f;
         const float sum = row_sum(ex);
         const float q = sum > 0.f ? ex / sum : 0.f;
-        v = q * (av - row_sum(av * q));
+        float d = 0.f;
+        add_apart<0>(q, av, a.slots, d);
+        v = q * d;
     } else {
         // renormalised: s up to a factor, which cancels, so that not all underflow
         const float m = a.renorm ? fminf(top, 0.f) : 0.f;
         const float s = id >= 0 ? 1.0f / (expf(m) + expf(m - ls)) : 0.f;
         const float rest = id >= 0 ? 1.0f / (1.0f + expf(ls)) : 0.f;
         if (a.renorm) {
-            const float S = row_sum(s), as = row_sum(av * s);
-            av = S > 0.f ? (av - as / S) / S : 0.f;
+            const float S = row_sum(s);
+            float d = 0.f;
+            add_apart<0>(s, av, a.slots, d);
+            av = S > 0.f ? d / S / S : 0.f;
         }
         v = s * rest * av;
     }

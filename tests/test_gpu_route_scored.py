@@ -310,6 +310,39 @@ def test_gradient_far_from_zero(renorm):
         assert ((got - ref).abs() <= 2.0 ** -15 * ref.abs() + 2.0 ** -23).all(), (score, got, ref)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("score", list(SCORE))
+def test_gradient_of_a_single_choice(score, dtype):
+    """Renormalised, one expert's weight is the scale whatever its logit."""
+    l = logits_of(200, 40, 3, dtype)
+    ids, w = route(l, 1, score, renorm=True)
+    dw = torch.randn(ids.shape, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+    assert (bwd(l, ids, dw, score, True, 2.5) == 0).all()
+    wide = torch.full((200, 20), -1, dtype=torch.int32, device=DEV)
+    wide[:, 17] = ids[:, 0]
+    assert (bwd(l, wide, dw.expand(200, 20).contiguous(), score, True, 2.5) == 0).all()
+
+
+@pytest.mark.parametrize("slots", [4, 16, 20])
+@pytest.mark.parametrize("score", list(SCORE))
+def test_gradient_beside_a_dominant_choice(score, slots):
+    """One slot holds nearly the whole sum.  Its gradient is s' / S^2 sum_j s_j (a_i -
+    a_j): against the magnitudes of that sum (scale 1: the differences have one
+    rounding), not against those of a_i, 2^17 times larger."""
+    g = torch.Generator(device=DEV).manual_seed(slots)
+    l = torch.randn((300, 40), generator=g, device=DEV) - 12
+    ids = torch.rand((300, 40), generator=g, device=DEV).argsort(1)[:, :slots].to(torch.int32).contiguous()
+    l.scatter_(1, ids[:, 1:2].long(), 0.25)
+    dw = torch.randn(ids.shape, generator=g, device=DEV)
+    got = bwd(l, ids, dw, score, True, 1.0).double().gather(1, ids.long())
+    z, a = l.double().gather(1, ids.long()), dw.double()
+    s = torch.sigmoid(z) if score == "sigmoid" else torch.softmax(z, 1)
+    f = (s * torch.sigmoid(-z) if score == "sigmoid" else s) / s.sum(1, keepdim=True) ** 2
+    diff = a[:, :, None] - a[:, None, :]
+    ref, mag = f * (diff * s[:, None, :]).sum(2), f * (diff.abs() * s[:, None, :]).sum(2)
+    assert ((got - ref).abs() <= (48 + 2 * 20) * 2.0 ** -24 * mag).all()
+
+
 def test_graph_streams_and_bits():
     l = logits_of(700, 256, 1, "bf16")
     bias = bias_of(256, 1)
