@@ -10,6 +10,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "i8_index.h"
 #include "i8_mm.h"
 #include "tiles.h"
 
@@ -62,7 +63,7 @@ i8_stream_kernel(I8Args a) {
         const int c = c0 + (SW ? i & 7 : i);
         return (c < a.n_out ? c : a.n_out - 1) + (SW && i >= 8 ? a.n_out : 0);
     };
-    const int8_t *ap = a.w + ((int64_t)e * a.N + wrow(i16)) * a.K + grp * 16;
+    const int8_t *ap = a.w + ((int64_t)e * a.N + wrow(i16)) * a.K;
     const u32x4 zero = {0u, 0u, 0u, 0u};
     // the output row of row i (-1: none) and its row of x
     auto out_row = [&](int i) -> int64_t {
@@ -86,18 +87,18 @@ i8_stream_kernel(I8Args a) {
         v4i acc[NQ];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) acc[n] = v4i{0, 0, 0, 0};
-        for (int k0 = w * 128; k0 < a.K; k0 += NW * U * 128) {
+        for (int k0 = w * kI8Step; k0 < a.K; k0 += NW * U * kI8Step) {
             u32x4 av[U][2], x[U][NQ][2];
             bool ok[U][2];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int k = k0 + u * NW * 128;
+                const int k = k0 + u * NW * kI8Step;
                 if (k >= a.K) break;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    ok[u][h] = k + 64 * h + grp * 16 < a.K;
-                    const int o = ok[u][h] ? k + 64 * h : 0;
-                    av[u][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(ap + o));
+                    ok[u][h] = i8_weights_count(k, h, grp, a.K);
+                    av[u][h] = __builtin_nontemporal_load(
+                        reinterpret_cast<const u32x4 *>(ap + i8_weights_load(k, h, grp, a.K)));
                 }
                 const bool in = k + ((l & 7) ^ (l >> 3)) * 16 < a.K;
 #pragma unroll
@@ -108,7 +109,7 @@ i8_stream_kernel(I8Args a) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // the wave's own copies
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (k0 + u * NW * 128 >= a.K) break;
+                if (k0 + u * NW * kI8Step >= a.K) break;
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     x[u][n][0] = lds_read16(lds + (u * NQ + n) * 2048 + x_off);
@@ -119,7 +120,7 @@ i8_stream_kernel(I8Args a) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (k0 + u * NW * 128 >= a.K) break;
+                if (k0 + u * NW * kI8Step >= a.K) break;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const u32x4 v = ok[u][h] ? av[u][h] : zero;
