@@ -1316,6 +1316,9 @@ MOE_API moe_status moe_route_scored(const void *router_logits, int32_t dtype, in
     if (!aligned_to(router_logits, dtype) || ((uintptr_t)bias & 3u) || ((uintptr_t)topk_ids & 3u) ||
         ((uintptr_t)topk_weights & 3u))
         return fail(MOE_ERR_ALIGN, "every tensor must be aligned to its elements");
+    const void *ids = topk_ids, *w = topk_weights;
+    if (ids == router_logits || ids == bias || w == router_logits || w == bias || ids == w)
+        return fail(MOE_ERR_SHAPE, "an output is one of the inputs or the other output");
     moe::ScoreArgs a = {};
     a.logits = router_logits;
     a.dtype = dtype;
