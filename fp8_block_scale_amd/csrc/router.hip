@@ -395,15 +395,19 @@ route_scored_kernel(ScoreArgs a, int sh) {
 // ----------------------------------------------------------------- backward
 
 // With a_j = scale dL/dw_j for the token's slots j that hold an expert:
-//   softmax                dl_e = p_e (sum_{j: e_j = e} a_j - sum_j a_j p_j)
+//   softmax                dl_e = p_e sum_f p_f (A_e - A_f) over all experts f, A_e = sum_{j: e_j = e} a_j:
+//                          p_e (A_e sum_{f in no slot} p_f + sum_{f in a slot} p_f (A_e - A_f)) for one in a slot,
+//                          -p_e sum_f p_f A_f for the others
 //   softmax, renormalised  dl_e = sum_{j: e_j = e} p_j sum_i p_i (a_j - a_i), p over the slots
 //   sigmoid                dl_e = sum_{j: e_j = e} s_j (1 - s_j) a_j
 //   sigmoid, renormalised  ... with sum_i s_i (a_j - a_i) / S^2 in the place of a_j, S = sum s
 // (1 - s is the sigmoid of -l: no cancellation where s is near 1; the differences
-// a_j - a_i are taken first: none where one slot holds nearly the whole sum, and a
-// single slot's gradient is 0.)
+// of a or A are taken first, and the p of experts in no slot added up, not taken from
+// 1: none where one expert holds nearly the whole sum, and a single slot's gradient
+// is 0 with renormalised weights.)
 // One wave a token, for gradients that every logit has (2048 tokens of 512
-// experts, BF16: 6.1 us, 4.2 MB, bound by its latency) and for more than 16 slots.
+// experts, BF16: 6.5 us, 4.2 MB, bound by its latency; without the differences 6.3)
+// and for more than 16 slots.
 template <int DT, int NPL>
 __global__ void __launch_bounds__(256)
 route_scored_bwd_kernel(ScoreArgs a) {
@@ -431,8 +435,8 @@ route_scored_bwd_kernel(ScoreArgs a) {
                        av - __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(av), i)), sum);
         return sum;
     };
-    float p[NPL], mx = -INFINITY, inv = 0.f, v = 0.f, dot = 0.f;
     if (dense) {
+        float p[NPL], mx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int e = lane + 64 * i;
@@ -448,10 +452,56 @@ route_scored_bwd_kernel(ScoreArgs a) {
             sum += p[i];
         }
         sum = wave_sum(sum);
-        inv = sum > 0.f ? 1.0f / sum : 0.f;
-        dot = wave_sum(id >= 0 ? av * expf(ls - mx) * inv : 0.f);
-        v = av;
-    } else if (a.score == kScoreSoftmax) {
+        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+        // of the lane's slot: A, and p where it is the first one of its expert
+        const float ps = id >= 0 ? expf(ls - mx) * inv : 0.f;
+        float A = av, pf = ps, diff = 0.f;       // diff: sum_{f in a slot} p_f (A - A_f)
+        auto value = [](float x, int j) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), j)); };
+        int slot[NPL];                           // the last slot of the lane's experts
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) slot[i] = -1;
+        for (int j = 0; j < a.slots; ++j) {
+            const int ej = __builtin_amdgcn_readlane(id, j);
+            const float pj = value(pf, j), aj = value(A, j);
+            if (ej != id) diff = fmaf(pj, A - aj, diff);
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) slot[i] = lane + 64 * i == ej ? j : slot[i];
+        }
+        float rest = 0.f;                        // of the experts in no slot
+        int listed = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            rest += slot[i] < 0 ? p[i] : 0.f;
+            listed += __builtin_popcountll(__ballot(slot[i] >= 0));
+        }
+        rest = wave_sum(rest) * inv;
+        if (listed < __builtin_popcountll(__ballot(id >= 0))) {        // an expert twice
+            A = diff = 0.f;
+            for (int j = 0; j < a.slots; ++j) {
+                const float aj = value(av, j);
+                if (__builtin_amdgcn_readlane(id, j) == id) {
+                    A += aj;
+                    if (j < lane) pf = 0.f;
+                }
+            }
+            for (int j = 0; j < a.slots; ++j) {
+                const float pj = value(pf, j), aj = value(A, j);
+                if (__builtin_amdgcn_readlane(id, j) != id) diff = fmaf(pj, A - aj, diff);
+            }
+        }
+        const float dot = wave_sum(pf * A);
+        diff = fmaf(A, rest, diff);
+        const float v = ps * diff;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 64 * i;
+            const float of = __shfl(v, slot[i], 64);
+            if (e < a.E) store_grad<DT>(a.dl, t * a.ld_dl + e, slot[i] < 0 ? -(p[i] * inv * dot) : of);
+        }
+        return;
+    }
+    float v;
+    if (a.score == kScoreSoftmax) {
         const float m = wave_max(ls);
         const float ex = id >= 0 ? expf(ls - m) : 0.f;
         const float sum = wave_sum(ex);
@@ -481,7 +531,7 @@ route_scored_bwd_kernel(ScoreArgs a) {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         const int e = lane + 64 * i;
-        if (e < a.E) store_grad<DT>(a.dl, t * a.ld_dl + e, dense ? p[i] * inv * (d[i] - dot) : d[i]);
+        if (e < a.E) store_grad<DT>(a.dl, t * a.ld_dl + e, d[i]);
     }
 }
 
