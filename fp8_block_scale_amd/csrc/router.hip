@@ -398,9 +398,10 @@ route_scored_kernel(ScoreArgs a, int sh) {
 //   softmax                dl_e = p_e sum_f p_f (A_e - A_f) over all experts f, A_e = sum_{j: e_j = e} a_j:
 //                          p_e (A_e sum_{f in no slot} p_f + sum_{f in a slot} p_f (A_e - A_f)) for one in a slot,
 //                          -p_e sum_f p_f A_f for the others
-//   softmax, renormalised  dl_e = sum_{j: e_j = e} p_j sum_i p_i (a_j - a_i), p over the slots
+//   softmax, renormalised  dl_e = sum_{j: e_j = e} p_j sum_{i: e_i != e} p_i (a_j - a_i), p over the slots
 //   sigmoid                dl_e = sum_{j: e_j = e} s_j (1 - s_j) a_j
-//   sigmoid, renormalised  ... with sum_i s_i (a_j - a_i) / S^2 in the place of a_j, S = sum s
+//   sigmoid, renormalised  ... with sum_{i: e_i != e} s_i (a_j - a_i) / S^2 in the place of a_j, S = sum s
+//                          (the differences between slots of one expert cancel, and are left out)
 // (1 - s is the sigmoid of -l: no cancellation where s is near 1; the differences
 // of a or A are taken first, and the p of experts in no slot added up, not taken from
 // 1: none where one expert holds nearly the whole sum, and a single slot's gradient
@@ -428,11 +429,13 @@ route_scored_bwd_kernel(ScoreArgs a) {
     if (!usable(ls)) id = -1;                    // never chosen: weight 0, whatever its logit
     ls = id >= 0 ? finite(ls) : -INFINITY;
     if (id < 0) av = 0.f;
-    auto apart = [&](float s) {                  // sum_i s_i (a_j - a_i)
+    auto value = [](float x, int j) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), j)); };
+    auto apart = [&](float s) {                  // sum_{i: e_i != e_j} s_i (a_j - a_i)
         float sum = 0.f;
-        for (int i = 0; i < a.slots; ++i)
-            sum = fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s), i)),
-                       av - __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(av), i)), sum);
+        for (int i = 0; i < a.slots; ++i) {
+            const float si = value(s, i), ai = value(av, i);
+            if (__builtin_amdgcn_readlane(id, i) != id) sum = fmaf(si, av - ai, sum);
+        }
         return sum;
     };
     if (dense) {
@@ -456,7 +459,6 @@ route_scored_bwd_kernel(ScoreArgs a) {
         // of the lane's slot: A, and p where it is the first one of its expert
         const float ps = id >= 0 ? expf(ls - mx) * inv : 0.f;
         float A = av, pf = ps, diff = 0.f;       // diff: sum_{f in a slot} p_f (A - A_f)
-        auto value = [](float x, int j) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), j)); };
         int slot[NPL];                           // the last slot of the lane's experts
 #pragma unroll
         for (int i = 0; i < NPL; ++i) slot[i] = -1;
@@ -551,17 +553,37 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// sum += s_i (a - a_i) over the row's lanes i from J on, up to lane 15
+// The value of lane J of the lane's row.
 template <int J>
-__device__ __forceinline__ void add_apart(float s, float a, int slots, float &sum) {
+__device__ __forceinline__ int row_lane(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, 0x150 + J, 0xF, 0xF, false);      // row broadcast
+}
+template <int J>
+__device__ __forceinline__ float row_lane(float v) {
+    return __uint_as_float(row_lane<J>((int)__float_as_uint(v)));
+}
+
+// n += the row's lanes from J on, up to lane 15, that hold the same expert
+template <int J>
+__device__ __forceinline__ void count_same(int id, int slots, int &n) {
     if constexpr (J < 16) {
         if (J < slots) {
-            const float sj =
-                __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(s), 0x150 + J, 0xF, 0xF, false));
-            const float aj =
-                __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(a), 0x150 + J, 0xF, 0xF, false));
-            sum = fmaf(sj, a - aj, sum);
-            add_apart<J + 1>(s, a, slots, sum);
+            n += row_lane<J>(id) == id;
+            count_same<J + 1>(id, slots, n);
+        }
+    }
+}
+
+// sum += s_i (a - a_i) over the row's lanes i from J on, up to lane 15; TWICE: that
+// hold another expert
+template <bool TWICE, int J = 0>
+__device__ __forceinline__ void add_apart(int id, float s, float a, int slots, float &sum) {
+    if constexpr (J < 16) {
+        if (J < slots) {
+            const int ej = TWICE ? row_lane<J>(id) : -1;
+            const float more = fmaf(row_lane<J>(s), a - row_lane<J>(a), sum);
+            sum = TWICE && ej == id ? sum : more;
+            add_apart<TWICE, J + 1>(id, s, a, slots, sum);
         }
     }
 }
@@ -571,9 +593,8 @@ template <int J>
 __device__ __forceinline__ void add_same(int id, float v, int slots, float &s) {
     if constexpr (J < 16) {
         if (J < slots) {
-            const int ej = __builtin_amdgcn_update_dpp(0, id, 0x150 + J, 0xF, 0xF, false);      // row broadcast
-            const float vj =
-                __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x150 + J, 0xF, 0xF, false));
+            const int ej = row_lane<J>(id);
+            const float vj = row_lane<J>(v);     // (in every lane, before the choice)
             s += ej == id ? vj : 0.f;
             add_same<J + 1>(id, v, slots, s);
         }
@@ -598,18 +619,26 @@ route_scored_bwd_rows_kernel(ScoreArgs a, int pitch) {
         if (id < 0 || id >= a.E) id = -1;
         if (id >= 0) ls = load_logit<DT>(a.logits, t * a.ld + id);
     }
+    // whether a token of the wave lists an expert twice (while the logits arrive)
+    int same = 0;
+    count_same<0>(id, a.slots, same);
+    const bool twice = __ballot(id >= 0 && same > 1) != 0;
     if (!usable(ls)) id = -1;                    // never chosen: weight 0, whatever its logit
     ls = id >= 0 ? finite(ls) : -INFINITY;
     if (id < 0) av = 0.f;
+    auto apart = [&](float s) {
+        float d = 0.f;
+        if (twice) add_apart<true>(id, s, av, a.slots, d);
+        else add_apart<false>(id, s, av, a.slots, d);
+        return d;
+    };
     const float top = unordered(row_max_u32(ordered_bits(ls)));
     float v;
     if (a.score == kScoreSoftmax) {
         const float ex = id >= 0 ? expf(ls - top) : 0.f;
         const float sum = row_sum(ex);
         const float q = sum > 0.f ? ex / sum : 0.f;
-        float d = 0.f;
-        add_apart<0>(q, av, a.slots, d);
-        v = q * d;
+        v = q * apart(q);
     } else {
         // renormalised: s up to a factor, which cancels, so that not all underflow
         const float m = a.renorm ? fminf(top, 0.f) : 0.f;
@@ -617,15 +646,15 @@ route_scored_bwd_rows_kernel(ScoreArgs a, int pitch) {
         const float rest = id >= 0 ? 1.0f / (1.0f + expf(ls)) : 0.f;
         if (a.renorm) {
             const float S = row_sum(s);
-            float d = 0.f;
-            add_apart<0>(s, av, a.slots, d);
-            av = S > 0.f ? d / S / S : 0.f;
+            av = S > 0.f ? apart(s) / S / S : 0.f;
         }
         v = s * rest * av;
     }
-    // an expert listed twice: both lanes hold the same sum
-    float d = 0.f;
-    add_same<0>(id, v, a.slots, d);
+    float d = v;
+    if (twice) {                                 // both lanes hold the same sum
+        d = 0.f;
+        add_same<0>(id, v, a.slots, d);
+    }
     __builtin_amdgcn_s_waitcnt(0xC07F);          // the zeros are written
     __builtin_amdgcn_wave_barrier();
     if (id >= 0) mine[(lane >> 4) * pitch + id] = d;

@@ -91,3 +91,35 @@ def test_softmax_with_the_dominant_expert_listed_twice():
     ids[1::4, 5] = -1
     ids[2::4, 2] = 64
     check_softmax(l, ids, dw)
+
+
+def renormalised_ref(l, ids, dw, score):
+    """(dl, the magnitudes that it adds): sum_{j: e_j = e} f_j sum_{i: e_i != e} s_i
+    (a_j - a_i), the differences between slots of one expert, which cancel, left out"""
+    z, a = l.double().gather(1, ids.long()), dw.double()
+    s = torch.sigmoid(z) if score == "sigmoid" else torch.softmax(z, 1)
+    f = (s * torch.sigmoid(-z) if score == "sigmoid" else s) / s.sum(1, keepdim=True) ** 2
+    d = a[:, :, None] - a[:, None, :]
+    d = torch.where(ids[:, :, None] == ids[:, None, :], 0.0, d) * s[:, None, :]
+    ref, mag = torch.zeros_like(l, dtype=torch.float64), torch.zeros_like(l, dtype=torch.float64)
+    return ref.scatter_add_(1, ids.long(), f * d.sum(2)), mag.scatter_add_(1, ids.long(), f * d.abs().sum(2))
+
+
+@pytest.mark.parametrize("slots", [2, 4, 16, 20])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("gap", [5.0, 17.0])
+def test_renormalised_with_the_dominant_expert_listed_twice(score, slots, gap):
+    """Its two slots' weights hold nearly the whole sum: what they take from each other
+    is far more than their expert's gradient."""
+    l, ids, dw = inputs(90, 40, slots, "f32", slots, gap)
+    l -= 12
+    ids[:, -1] = ids[:, 0]
+    if slots > 3:
+        ids[::2, 2] = ids[::2, 1]
+    d = torch.full_like(l, 7.0)
+    moe.moe_route_scored_bwd(l, ids, dw, d, {"softmax": moe.MOE_SCORE_SOFTMAX, "sigmoid": moe.MOE_SCORE_SIGMOID}[score])
+    ref, mag = renormalised_ref(l, ids, dw, score)
+    arg = l.abs().amax().item()
+    tol = (2 * arg + slots + 40 + slots) * 2.0 ** -24 * mag + 2.0 ** -130      # (and a slot's sum over its expert's slots)
+    err = (d.double() - ref).abs()
+    assert (err <= tol).all(), (err / tol).max().item()
