@@ -52,7 +52,7 @@ EXPORTED = ("moe_plan_capacity", "moe_plan_workspace_size", "moe_plan", "moe_qua
             "moe_group_mm_dx", "moe_group_mm_dw", "moe_fp8_linear_workspace_size",
             "moe_fp8_linear", "moe_route_scored", "moe_route_scored_bwd", "moe_combine", "moe_combine_bwd",
             "moe_quant_i8", "moe_i8_linear_workspace_size", "moe_i8_linear",
-            "moe_i8_group_mm_workspace_size", "moe_i8_group_mm")
+            "moe_i8_group_mm_workspace_size", "moe_i8_group_mm", "moe_debug_i8_schedule")
 
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -146,6 +146,8 @@ _c = {
                                              _i32, _i32, _i64, _i32, _i32),
     "moe_i8_group_mm": _proto("moe_i8_group_mm", _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
                               _i64, _i64, _i32, _i32, _i32, _i64, _i32, _vp, _i32, _i64, _vp, _sz, _vp),
+    "moe_debug_i8_schedule": _proto("moe_debug_i8_schedule", _i32, _i64, _i64, _i64, _i32, _i32, _i32, _i64, _i32,
+                                    _vp),
     "moe_status_str": _proto("moe_status_str", ctypes.c_char_p, _i32),
     "moe_last_hip_error": _proto("moe_last_hip_error", ctypes.c_char_p),
     "moe_last_error": _proto("moe_last_error", ctypes.c_char_p),
@@ -844,6 +846,14 @@ def moe_i8_group_mm(x_q, x_s, w, w_s, sorted_token_ids, expert_ids, num_tokens_p
     _launch(where, stream, (x_q, x_s, w, w_s, out, bias, sorted_token_ids, expert_ids, num_tokens_post_padded,
                             workspace), qp, xsp, per_route, wp, wsp, bp, *plan, R // top_k, K, N, E, top_k,
             block_m, cap, act, op, _DT16[ot], ld_out, *_ws(where, workspace))
+
+
+def moe_debug_i8_schedule(M, K, N, E=0, top_k=1, block_m=8, sorted_cap=0, act=MOE_ACT_NONE):
+    """The kernel of moe_i8_linear (E = 0) or moe_i8_group_mm at these sizes: (the
+    few-rows kernel's rows per pass or 0, a tile's rows, its weight rows)."""
+    info = (ctypes.c_int32 * 3)()
+    _check(_c["moe_debug_i8_schedule"](M, K, N, E, top_k, block_m, sorted_cap, act, info), "moe_debug_i8_schedule")
+    return tuple(info)
 
 
 def moe_status_str(status):

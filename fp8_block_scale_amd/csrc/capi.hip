@@ -1657,6 +1657,28 @@ MOE_API moe_status moe_i8_group_mm(const int8_t *x_q, const float *x_s, int32_t 
     return run_i8(a, workspace, workspace_bytes, stream, "moe_i8_group_mm: launch");
 }
 
+MOE_API moe_status moe_debug_i8_schedule(int64_t M, int64_t K, int64_t N, int32_t E, int32_t top_k,
+                                         int32_t block_m, int64_t sorted_cap, int32_t act, int32_t *info) {
+    if (!info) return fail(MOE_ERR_NULL, "info is NULL");
+    const moe_status st =
+        E ? check_i8_group(M, K, N, E, top_k, block_m, sorted_cap, act) : check_i8_linear(M, N, K, act);
+    if (st != MOE_OK) return st;
+    info[0] = info[1] = info[2] = 0;
+    if (M == 0 || (E && sorted_cap == 0)) return MOE_OK;
+    moe::I8Args a = i8_args(M, N, K, act);
+    a.grouped = E != 0;
+    if (a.grouped)
+        a.g = group_args(moe::kGmmFwd, MOE_DT_BF16, nullptr, nullptr, nullptr, M, K, N, E, top_k, block_m,
+                         sorted_cap, 0);
+    moe::i8_workspace(a, nullptr);
+    info[0] = 16 * a.stream_nq;
+    if (!a.stream_nq) {
+        info[1] = a.tile_rows;
+        info[2] = a.tile_cols;
+    }
+    return MOE_OK;
+}
+
 // ------------------------------------------------- no-allocation variant
 
 // The static workspace of moe_fp8_experts_noalloc: one copy per device,

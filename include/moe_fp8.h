@@ -740,6 +740,15 @@ const char *moe_last_error(void);
  * in/out are device pointers; n >= 0. */
 moe_status moe_debug_e4m3_encode(const float *in, uint8_t *out, int64_t n, void *stream);
 
+/* Test hook: the kernel that moe_i8_linear (E = 0; top_k, block_m and sorted_cap
+ * are ignored) or moe_i8_group_mm (E >= 1) takes for these sizes (host only,
+ * nothing enqueued): info[0] = the few-rows kernel's rows of x per pass (16, 32,
+ * 48 or 64), or 0 and info[1], info[2] = rows of x and weight rows of a tile.
+ * info is host memory of 3 int32, all 0 where no kernel runs (M = 0, sorted_cap
+ * = 0).  Errors: MOE_ERR_NULL (info) and those of the products' sizes. */
+moe_status moe_debug_i8_schedule(int64_t M, int64_t K, int64_t N, int32_t E, int32_t top_k,
+                                 int32_t block_m, int64_t sorted_cap, int32_t act, int32_t *info);
+
 /* Debug check of the MOE_F_MMA_E8M0 precondition (SGLang PR #43556,
  * Motivation: scales that are not powers of two, fed to an E8M0-scaled MFMA,
  * give wrong results without any error).  Writes to count[0] (device memory,
