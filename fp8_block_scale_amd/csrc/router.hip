@@ -10,8 +10,13 @@
 // What bounds it: instructions, at few tokens their latency.  Measured: 16 tokens
 // of 256 experts in 8 groups 6.6 us (decided in 64 bits throughout 13.9), 8192
 // tokens of 288 experts, softmax with a bias, 16.3 (25.5): 13 and the about 20
-// tokens that FP32 does not decide, whose waves end last.  Reading the logits
-// (4.7 MB) takes 1.
+// tokens that FP32 does not decide, whose waves end last.  That is with a bias that
+// differs from expert to expert.  Where equal logits give equal choice scores (a bias
+// of zeros, or group sums without a bias) FP32 does not decide those tokens either:
+// of BF16 logits of that spread 37% have a tie among their nine largest, and the
+// same call takes 21.3 us (FP16: 5%, 18.7; FP32: none, 16.1).  Without bias and sums
+// logits are compared, and ties are decided: 11.3.  Reading the logits (4.7 MB)
+// takes 1.
 #include <algorithm>
 
 #include "common.h"
@@ -697,6 +702,12 @@ hipError_t fwd(const ScoreArgs &a, hipStream_t st) {
     int sh = 6;                                  // log2 of a group's lanes
     while (sh > 0 && (a.n_group << sh) > 64) --sh;
     const int n = a.E / a.n_group, npl = (n + (1 << sh) - 1) >> sh;
+    // Experts of a lane, rounded up to a width with code.  Powers of two, and 5: what
+    // one group of 257 to 320 experts takes (8192 tokens of 288, FP32 logits, 14.8 us,
+    // in code for 8 18.0; of 320 16.2, 20.1).  8192 tokens of 384 and 512 experts in
+    // one group (8) take 20.2 and 20.9, of 576 and 1024 (16) 33.5 and 35.6, of 1024 in
+    // 32 groups (16) 58; more than 16 only where the number of groups is no power of
+    // two and lanes are left over (1023 in 33 groups, a lane each: 105).
     if (npl <= 2) return launch_fwd<DT, 2>(a, sh, st);
     if (npl <= 4) return launch_fwd<DT, 4>(a, sh, st);
     if (npl <= 5) return launch_fwd<DT, 5>(a, sh, st);

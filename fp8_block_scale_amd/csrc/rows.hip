@@ -1,6 +1,7 @@
 // Row-wise operators around the experts' products: 8-bit codes of rows, and
 // the weighted sum of a token's routes with its gradient.  All of them are
-// bound by memory: every value is read once and written once.
+// bound by memory: every value is read once (rows to be coded of more than 8192
+// values past those twice, the second time from the caches) and written once.
 #include <algorithm>
 
 #include "common.h"

@@ -593,7 +593,8 @@ moe_status moe_route_scored(const void *router_logits, int32_t dtype, int64_t M,
  *   n_shared there); d_logits [M, ld_d_logits] of dtype out: all E_routed
  *   columns are written, 0 where there is no gradient.
  * With MOE_SCORE_SOFTMAX and renorm = 0 every expert's logit has a gradient;
- * otherwise the chosen ones'.  Computed in FP32, rounded once.
+ * otherwise the chosen ones'.  Computed in FP32 from differences of d_weights, so
+ * that nothing cancels beside an expert with nearly all of the sum; rounded once.
  * Constraints and errors as above; 1 <= slots <= 33; d_logits is none of the
  * inputs. */
 moe_status moe_route_scored_bwd(const void *router_logits, int32_t dtype, int64_t M, int64_t ld_logits,
@@ -663,7 +664,8 @@ moe_status moe_quant_i8(const void *x, int32_t dtype, int64_t M, int64_t K, int6
  * The sums are exact 32-bit integers (any int8 codes, -128 too); scales, bias,
  * activation (as moe_fp8_linear's: with MOE_ACT_SWIGLU rows [0, N/2) of w are the
  * gate and rows [N/2, N) the up projection, and there are N/2 output columns)
- * and residual are FP32, with one rounding.
+ * and residual are FP32, with one rounding.  The sum is multiplied by x_s first:
+ * their product must lie in FP32's range too.
  *   x_q [M, K] (per route [M * top_k, K]) int8, x_s one FP32 per row;
  *   w [N, K] or [E, N, K] int8, w_s and bias (or NULL) [N] or [E, N] FP32;
  *   out / y BF16 or FP16 (out_dtype / y_dtype), residual [M, ld_res] of the same
@@ -677,8 +679,8 @@ moe_status moe_quant_i8(const void *x, int32_t dtype, int64_t M, int64_t K, int6
  * outputs and residual 2-byte aligned, leading dimensions at most 2^30; outputs
  * overlap nothing else.  The workspace (256-byte aligned) holds
  * the *_workspace_size bytes (0: none needed, NULL accepted; also 0 for sizes
- * it rejects) and is written from scratch by each call: calls on one stream may
- * share it, calls that overlap may not.
+ * it rejects; moe_i8_linear needs none at any size) and is written from scratch
+ * by each call: calls on one stream may share it, calls that overlap may not.
  * Errors: MOE_ERR_SHAPE, MOE_ERR_NULL, MOE_ERR_ALIGN, MOE_ERR_CAPACITY
  * (workspace), MOE_ERR_UNSUPPORTED (sizes out of range, or more output tiles
  * than int32 counts), MOE_ERR_HIP. */
